@@ -135,7 +135,9 @@ typedef struct {
  * rotations), "automorph", "modup",
  * "moddown_conv", "rescale", "tensor", "ptmac", "ctmac", "add",
  * "const_mul", "term_mac" (polynomial evaluation's constant multiples),
- * "ip_gather".  NULL or "" stops tracing.
+ * "ip_gather", "sum_ip" and "sum_combine" (inner product and last step of a
+ * stage of ckks_rotate_sum), "attn_mac" (slotwise products of the attention
+ * calls).  NULL or "" stops tracing.
  * Tracing adds two event records per traced launch and nothing else. */
 int ckks_trace_begin(ckks_ctx* ctx, const char* kernel);
 /* Waits for the recorded events, returns the totals and stops tracing. */
@@ -339,6 +341,138 @@ int ckks_ctmatvec(ckks_ctx* ctx, const uint64_t* d_x, int n_in, const uint64_t* 
                   const uint64_t* d_rlk, const uint32_t* baby_galois, const uint64_t* const* d_evk_baby,
                   const uint32_t* giant_galois, const uint64_t* const* d_evk_giant, uint64_t* d_y, int level,
                   unsigned flags, ckks_stream_t stream);
+
+/* ---- attention on packed heads ------------------------------------------------
+ *
+ * The products of an attention layer whose operands are all ciphertexts.  The
+ * calls work slot by slot and on sums over a packed axis; the packing is the
+ * caller's.  A layout that serves all of them keeps the summed index
+ * outermost: slot = f * (n/F) + r for F features f, r running over (head,
+ * token) or (head, value feature); the rotations by multiples of n/F then sum
+ * exactly over f, cyclically, and leave the sum in every f.
+ *
+ * Scales follow from the operations: a product multiplies them, a rescale
+ * divides by the dropped prime.  Sums need equal scales; the caller sees to
+ * it.  Level l operands hold limbs q_0..q_l.
+ *
+ * Plaintext rows (masks, weights, decays) are in NTT form, one per head group:
+ * item g of n_grp uses row g mod n_rows, so groups that share their heads'
+ * constants (the sequences of a batch, in the order [sequence][head group])
+ * share the rows.  A row of zeros removes its term: a padded token or key
+ * block, or a sequence that is empty altogether, contributes nothing, and
+ * sums over nothing decrypt to zero (there is no division).
+ *
+ * Buffers and streams: intermediates live in the context's buffers, grown on
+ * demand; growing synchronises the device.  A call no larger than an earlier
+ * one on the same context allocates nothing and may be captured into a graph;
+ * a larger one returns CKKS_EHIP while its stream is capturing.  Buffers a
+ * capture has recorded stay allocated until the context is destroyed, so a
+ * captured call stays valid while larger calls follow.  Replays use the
+ * context like calls do: one at a time. */
+
+#define CKKS_SUM_MAX_RADIX 32
+#define CKKS_SUM_MAX_STAGES 16
+
+/* Sum over a packed axis, in stages.  Stage s turns x into
+ *   x + sum_{r < radix[s]-1} Rot_{g_r}(x),
+ * its radix[s]-1 elements and keys following those of the stages before it.
+ * For an axis of length prod(radix) at stride d, stage s holds the rotations
+ * by d_s, 2 d_s, .., (radix[s]-1) d_s with d_s = d * radix[0] * .. *
+ * radix[s-1].  One decomposition and one ModDown serve a whole stage:
+ *   D_j     raised digits of c1, as in ckks_rotate_hoisted
+ *   U       = sum_r sum_j tau_{g_r}(D_j) * evk_{r,j}    (extended basis)
+ *   out     = (c0 + sum_r tau_{g_r}(c0) + ModDown(U_0), c1 + ModDown(U_1))
+ * so a radix of 4 to 8 takes about half the time of the same sum by
+ * ckks_rotate with CKKS_ROT_ACCUMULATE (radix 2 is that rotation up to the
+ * words of the decomposition), for radix-1 keys instead of log2(radix). */
+typedef struct {
+  int n_stage;                    /* 0..CKKS_SUM_MAX_STAGES */
+  const int* radix;               /* host [n_stage], each 2..CKKS_SUM_MAX_RADIX */
+  const uint32_t* galois_elts;    /* host [sum(radix) - n_stage], none of them 1 */
+  const uint64_t* const* d_evks;  /* host list of switch keys, one per element */
+} ckks_sum_steps;
+
+/* Source: AEGIS summary, "Problem", challenge 2 and "Methodology", items 3-4
+ * (rotations aggregate the partial products of Q x K^T; several offsets of one
+ * ciphertext are in flight at once).
+ * Sum of each of the batch ciphertexts d_ct_in ([batch][2][level+1][N]) by
+ * `steps` into d_ct_out (same shape).  Needs n_stage >= 1 and K > 0. */
+int ckks_rotate_sum(ckks_ctx* ctx, const uint64_t* d_ct_in, uint64_t* d_ct_out, int batch, int level,
+                    const ckks_sum_steps* steps, ckks_stream_t stream);
+
+/* Source: AEGIS summary, "Methodology", item 3 (self-attention: Q x K^T on
+ * encrypted operands); cross attention takes K from an encoder's states, of
+ * another length.
+ * Scores of every query ciphertext against every key ciphertext of its group:
+ *   s[g][i][j] = Sum(rescale(relin(q[g][i] x k[g][j])))
+ *   d_q  [n_grp][n_q][2][level+1][N]     d_k  [n_grp][n_k][2][level+1][N]
+ *   d_s  [n_grp][n_q][n_k][2][level][N]
+ * d_rlk is the s^2 -> s key; `steps` with n_stage 0 (or NULL) leaves the
+ * slotwise products unsummed.  The polynomial softmax between the scores and
+ * ckks_attn_mix is ckks_poly_eval_tree.  CKKS_ERANGE at level 0. */
+int ckks_attn_scores(ckks_ctx* ctx, const uint64_t* d_q, int n_q, const uint64_t* d_k, int n_k, int n_grp, int level,
+                     const uint64_t* d_rlk, const ckks_sum_steps* steps, uint64_t* d_s, ckks_stream_t stream);
+
+/* Source: AEGIS summary, "Methodology", item 3 (the weights multiplied with V
+ * and summed).
+ * Masked weighted sum of the value ciphertexts, and the sum of the weights:
+ *   num[g][i] = Sum(rescale(rescale(relin(sum_j m_j a[g][i][j] x v[g][j]))))
+ *   den[g][i] = Sum(rescale(sum_j m_j a[g][i][j]))
+ *   d_a   [n_grp][n_q][n_k][2][level+1][N]   d_v  [n_grp][n_k][2][level+1][N]
+ *   d_mask  [n_mask][n_k][level+1][N] plaintexts, 1 <= n_mask <= n_grp, or
+ *         NULL with n_mask 0: no mask and one rescale less in each line
+ *   d_num  [n_grp][n_q][2][level-1][N]  ([..][level][N] without a mask)
+ *   d_den  [n_grp][n_q][2][level][N]    ([..][level+1][N] without a mask),
+ *         or NULL
+ * One relinearisation per (g, i).  The quotient num / den is the caller's (a
+ * polynomial in den, or a division after decryption).  Needs n_k >= 1;
+ * CKKS_ERANGE below level 2 with a mask, 1 without. */
+int ckks_attn_mix(ckks_ctx* ctx, const uint64_t* d_a, int n_q, const uint64_t* d_v, int n_k, int n_grp,
+                  const uint64_t* d_mask, int n_mask, int level, const uint64_t* d_rlk, const ckks_sum_steps* steps,
+                  uint64_t* d_num, uint64_t* d_den, ckks_stream_t stream);
+
+/* Linear attention with a decay for each head, chunked form: n_tok tokens of
+ * a prompt at once (attention without the softmax, which needs no polynomial
+ * approximation; the pages' attention, AEGIS summary, "Methodology", item 3,
+ * keeps it).  Per group g and token t, slotwise on a state whose slots hold
+ * the outer products of key and value features:
+ *   X_t   = sum_{u <= t} w_u (k_u x v_u)          three parts, not relinearised
+ *   S_t   = state_in + rescale(rescale(relin(X_t)))               level-2
+ *   y_t   = Sum(rescale(relin(rescale(r_t q_t) x S_t)))           level-3
+ *   state_out = rescale(carry S_{n_tok-1})  (level-3), or S_{n_tok-1} (level-2)
+ * With decay gamma per head, w_u = gamma^-u, r_t = gamma^t and carry =
+ * gamma^n_tok give S_t = gamma^t state_in + sum gamma^(t-u) k_u v_u as read by
+ * y_t, at two levels however long the chunk is.
+ *   d_q, d_k, d_v  [n_tok][n_grp][2][level+1][N]
+ *   d_w, d_r       [n_tok][n_row][level+1][N] plaintexts; d_r may be NULL
+ *                  (q_t's limbs 0..level-2 as they are)
+ *   d_carry        [n_row][level-1][N] plaintexts, or NULL
+ *   d_state_in     [n_grp][2][level-1][N], or NULL (zero)
+ *   d_y            [n_tok][n_grp][2][level-2][N]
+ *   d_state_out    [n_grp][2][level-1][N], with d_carry [n_grp][2][level-2][N]
+ * Needs n_tok >= 1, 1 <= n_row <= n_grp; CKKS_ERANGE below level 3. */
+int ckks_linattn_chunk(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, const uint64_t* d_v, int n_tok,
+                       int n_grp, const uint64_t* d_w, const uint64_t* d_r, const uint64_t* d_carry, int n_row,
+                       const uint64_t* d_state_in, int level, const uint64_t* d_rlk, const ckks_sum_steps* steps,
+                       uint64_t* d_y, uint64_t* d_state_out, ckks_stream_t stream);
+
+/* Recurrent form of the same, one token per group:
+ *   with d_decay:  state_out = rescale(relin(k x v) + decay state_in)
+ *   without:       state_out = state_in + rescale(relin(k x v))
+ *   y = Sum(rescale(relin(q x state_out))), q at state_out's limbs
+ *   d_q, d_k, d_v  [n_grp][2][level+1][N]
+ *   d_decay        [n_row][level+1][N] plaintexts, 1 <= n_row <= n_grp, or
+ *                  NULL with n_row 0 (the caller weighs k instead, and the
+ *                  state keeps its level from token to token)
+ *   d_state_in     [n_grp][2][level+1][N] with d_decay, [n_grp][2][level][N]
+ *                  without, or NULL (zero: the first token)
+ *   d_y            [n_grp][2][level-1][N]
+ *   d_state_out    [n_grp][2][level][N]
+ * CKKS_ERANGE below level 2. */
+int ckks_linattn_step(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, const uint64_t* d_v, int n_grp,
+                      const uint64_t* d_decay, int n_row, const uint64_t* d_state_in, int level,
+                      const uint64_t* d_rlk, const ckks_sum_steps* steps, uint64_t* d_y, uint64_t* d_state_out,
+                      ckks_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -438,6 +438,137 @@ def ctmatvec(P: Params, level: int, x, diags, rlk, g_baby, evk_baby, g_giant, ev
 
 
 # ---------------------------------------------------------------------------
+# Attention on packed heads, composed from the steps above (readings: the
+# pages give no packing and no recurrence)
+# ---------------------------------------------------------------------------
+
+def poly_mul(P: Params, a, b):
+    """Product limb by limb of NTT-form polynomials [k][N], limbs q_0.."""
+    a, b = _arr(a), _arr(b)
+    out = np.empty_like(a)
+    lib().orc_poly_mul(_u64(a), _u64(b), _u64(out), a.shape[0], P.log_n, _u64(P._mods))
+    return out
+
+
+def poly_add(P: Params, a, b, mods=None):
+    a, b = _arr(a), _arr(b)
+    out = np.empty_like(a)
+    m = P._mods if mods is None else _arr(mods)
+    lib().orc_poly_add(_u64(a), _u64(b), _u64(out), a.shape[0], P.log_n, _u64(m))
+    return out
+
+
+def ct_add(P: Params, a, b):
+    """Sum of ciphertexts (any number of parts) of one level."""
+    return np.stack([poly_add(P, x, y) for x, y in zip(a, b)])
+
+
+def ct_scale(P: Params, a, pt):
+    """Ciphertext times a plaintext polynomial in NTT form."""
+    return np.stack([poly_mul(P, x, pt) for x in a])
+
+
+def relin(P: Params, level: int, d, rlk):
+    """Three parts [3][l+1][N] -> (d0, d1) + KS(d2)."""
+    return ct_add(P, d[:2], keyswitch(P, level, np.ascontiguousarray(d[2]), rlk))
+
+
+def rotate_sum(P: Params, level: int, ct, galois, evks):
+    """Stages of x + sum_r Rot_{g_r}(x); galois and evks list the stages'
+    elements and keys.  Per stage, with D_j the raised digits of c1:
+      U = sum_r sum_j tau_{g_r}(D_j) * evk_{r,j}     (extended basis)
+      x = (c0 + sum_r tau_{g_r}(c0) + ModDown(U_0), c1 + ModDown(U_1))."""
+    ct = _arr(ct)
+    ext = P.ext_mods(level)
+    psis = P.psi[: level + 1] + P.psi[P.L:]
+    rows = list(range(level + 1)) + list(range(P.L, P.L + P.K))
+    m = _arr(ext)
+    for gs, keys in zip(galois, evks):
+        coef = ntt_params(P, ct[1], inverse=True)
+        dt = [ntt(modup(P, level, j, coef), ext, psis, P.log_n) for j in range(P.beta(level))]
+        acc = np.zeros((2, len(ext), P.N), dtype=np.uint64)
+        c0 = ct[0]
+        for g, evk in zip(gs, keys):
+            for j, d in enumerate(dt):
+                t = automorph_ntt(d, P.log_n, g)
+                for comp in range(2):
+                    prod = np.empty_like(t)
+                    lib().orc_poly_mul(_u64(t), _u64(_arr(evk[j, comp][rows])), _u64(prod), len(ext), P.log_n, _u64(m))
+                    acc[comp] = poly_add(P, acc[comp], prod, ext)
+            c0 = poly_add(P, c0, automorph_ntt(ct[0], P.log_n, g))
+        ct = np.stack([poly_add(P, c0, moddown(P, level, acc[0])), poly_add(P, ct[1], moddown(P, level, acc[1]))])
+    return ct
+
+
+def attn_scores(P: Params, level: int, q, k, rlk, galois, evks):
+    """q [G][n_q], k [G][n_k] ciphertexts -> Sum(rescale(relin(q x k)))."""
+    return np.stack([[rotate_sum(P, level - 1, rescale(P, level, relin(P, level, tensor(P, level, x, y), rlk)), galois,
+                                 evks) for y in kg] for qg, kg in zip(q, k) for x in qg]).reshape(
+        (len(q), q.shape[1], k.shape[1], 2, level, P.N))
+
+
+def attn_mix(P: Params, level: int, a, v, mask, rlk, galois, evks):
+    """a [G][n_q][n_k], v [G][n_k] ciphertexts, mask [M][n_k] plaintexts or
+    None -> (num, den): the masked weighted sums of v and of 1."""
+    num, den = [], []
+    for g in range(a.shape[0]):
+        for i in range(a.shape[1]):
+            top = bottom = None
+            for j in range(a.shape[2]):
+                x = a[g, i, j] if mask is None else ct_scale(P, a[g, i, j], mask[g % len(mask), j])
+                d = tensor(P, level, x, v[g, j])
+                top = d if top is None else ct_add(P, top, d)
+                bottom = x if bottom is None else ct_add(P, bottom, x)
+            top, lt, lb = rescale(P, level, relin(P, level, top, rlk)), level - 1, level
+            if mask is not None:
+                top, bottom, lt, lb = rescale(P, lt, top), rescale(P, lb, bottom), lt - 1, lb - 1
+            num.append(rotate_sum(P, lt, top, galois, evks))
+            den.append(rotate_sum(P, lb, bottom, galois, evks))
+    lead = a.shape[:2]
+    return np.stack(num).reshape(lead + num[0].shape), np.stack(den).reshape(lead + den[0].shape)
+
+
+def linattn_chunk(P: Params, level: int, q, k, v, w, r, carry, state, rlk, galois, evks):
+    """Chunked linear attention: q, k, v [T][G] ciphertexts, w and r [T][R]
+    and carry [R] plaintexts (r, carry and state may be None) ->
+    (y [T][G], state out [G])."""
+    T, G = q.shape[:2]
+    ys, last = [[None] * G for _ in range(T)], []
+    for g in range(G):
+        x = s = None
+        for t in range(T):
+            d = tensor(P, level, ct_scale(P, k[t, g], w[t, g % w.shape[1]]), v[t, g])
+            x = d if x is None else ct_add(P, x, d)
+            s = rescale(P, level - 1, rescale(P, level, relin(P, level, x, rlk)))
+            if state is not None:
+                s = ct_add(P, s, state[g])
+            qt = q[t, g] if r is None else rescale(P, level, ct_scale(P, q[t, g], r[t, g % r.shape[1]]))
+            d = tensor(P, level - 2, np.ascontiguousarray(qt[:, : level - 1]), s)
+            y = rescale(P, level - 2, relin(P, level - 2, d, rlk))
+            ys[t][g] = rotate_sum(P, level - 3, y, galois, evks)
+        last.append(s if carry is None else rescale(P, level - 2, ct_scale(P, s, carry[g % len(carry)])))
+    return np.array(ys), np.stack(last)
+
+
+def linattn_step(P: Params, level: int, q, k, v, decay, state, rlk, galois, evks):
+    """Recurrent linear attention, one token: q, k, v [G] ciphertexts, decay
+    [R] plaintexts or None, state [G] or None -> (y [G], state out [G])."""
+    ys, ss = [], []
+    for g in range(len(q)):
+        d = relin(P, level, tensor(P, level, k[g], v[g]), rlk)
+        if decay is not None and state is not None:
+            d = ct_add(P, d, ct_scale(P, state[g], decay[g % len(decay)]))
+        s = rescale(P, level, d)
+        if decay is None and state is not None:
+            s = ct_add(P, s, state[g])
+        d = tensor(P, level - 1, np.ascontiguousarray(q[g][:, :level]), s)
+        y = rescale(P, level - 1, relin(P, level - 1, d, rlk))
+        ys.append(rotate_sum(P, level - 2, y, galois, evks))
+        ss.append(s)
+    return np.stack(ys), np.stack(ss)
+
+
+# ---------------------------------------------------------------------------
 # Keys, encryption, decryption
 # ---------------------------------------------------------------------------
 

@@ -32,7 +32,8 @@ EXPORTED = [
     "ckks_ctx_create", "ckks_ctx_destroy", "ckks_ctx_psi",
     "ckks_ntt", "ckks_automorph", "ckks_keyswitch", "ckks_rotate", "ckks_rotate_noalloc", "ckks_rotate_hoisted",
     "ckks_rescale",
-    "ckks_mul_relin_rescale", "ckks_poly_eval", "ckks_poly_eval_tree", "ckks_ptmatvec", "ckks_ctmatvec", "ckks_trace_begin",
+    "ckks_mul_relin_rescale", "ckks_poly_eval", "ckks_poly_eval_tree", "ckks_ptmatvec", "ckks_ctmatvec", "ckks_rotate_sum",
+    "ckks_attn_scores", "ckks_attn_mix", "ckks_linattn_chunk", "ckks_linattn_step", "ckks_trace_begin",
     "ckks_trace_end", "ckks_probe_list", "ckks_probe_rate",
 ]
 
@@ -65,6 +66,15 @@ class ckks_params(ctypes.Structure):
     ]
 
 
+class ckks_sum_steps(ctypes.Structure):
+    _fields_ = [
+        ("n_stage", ctypes.c_int),
+        ("radix", ctypes.POINTER(ctypes.c_int)),
+        ("galois_elts", ctypes.POINTER(ctypes.c_uint32)),
+        ("d_evks", ctypes.POINTER(ctypes.c_void_p)),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libckks_mi355x.so is not built (%s); run __graft_entry__.build() or "
@@ -73,6 +83,7 @@ def _load():
     vp, u64p, u32p = ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint32)
     i, u32 = ctypes.c_int, ctypes.c_uint32
     pp = ctypes.POINTER(vp)
+    sp = ctypes.POINTER(ckks_sum_steps)
     sig = {
         "ckks_find_primes": (i, [u32, u32, u32, u64p]),
         "ckks_params_validate": (i, [ctypes.POINTER(ckks_params)]),
@@ -95,6 +106,11 @@ def _load():
                                     ctypes.POINTER(ctypes.c_double), vp]),
         "ckks_ptmatvec": (i, [vp, vp, i, vp, i, i, i, u32p, pp, u32p, pp, vp, i, ctypes.c_uint, vp]),
         "ckks_ctmatvec": (i, [vp, vp, i, vp, i, i, i, vp, u32p, pp, u32p, pp, vp, i, ctypes.c_uint, vp]),
+        "ckks_rotate_sum": (i, [vp, vp, vp, i, i, sp, vp]),
+        "ckks_attn_scores": (i, [vp, vp, i, vp, i, i, i, vp, sp, vp, vp]),
+        "ckks_attn_mix": (i, [vp, vp, i, vp, i, i, vp, i, i, vp, sp, vp, vp, vp]),
+        "ckks_linattn_chunk": (i, [vp, vp, vp, vp, i, i, vp, vp, vp, i, vp, i, vp, sp, vp, vp, vp]),
+        "ckks_linattn_step": (i, [vp, vp, vp, vp, i, vp, i, vp, i, vp, sp, vp, vp, vp]),
         "ckks_trace_begin": (i, [vp, ctypes.c_char_p]),
         "ckks_trace_end": (i, [vp, ctypes.POINTER(ckks_trace_stats)]),
         "ckks_probe_list": (i, [ctypes.c_char_p, i]),
@@ -389,6 +405,93 @@ def ckks_ctmatvec(ctx, d_x, n_in, d_diags, n_out, n1, n2, d_rlk, baby_galois, d_
     _check(_lib.ckks_ctmatvec(ctx.handle, x, n_in, _dev(ctx, d_diags, dw, "d_diags"), n_out, n1, n2,
                               _dev(ctx, d_rlk, ctx.key_words, "d_rlk"), gb, kb, gg, kg, y, level, flags,
                               _stream(stream)), "ckks_ctmatvec")
+
+
+class RotateSum:
+    """Stages of a sum over a packed axis (ckks_sum_steps): stage s turns x into
+    x + sum_r Rot_{galois[s][r]}(x), galois[s][r] switched with keys[s][r]."""
+
+    def __init__(self, galois, keys):
+        _count(keys, len(galois), "keys")
+        for s, (g, k) in enumerate(zip(galois, keys)):
+            _count(k, len(g), "keys[%d]" % s)
+        self.radix = [len(g) + 1 for g in galois]
+        self.galois = [int(v) for g in galois for v in g]
+        self.keys = [t for k in keys for t in k]
+
+    def _c(self, ctx):
+        """The C structure for a call on ctx (it holds its arrays)."""
+        radix, elts = (ctypes.c_int * max(1, len(self.radix)))(*self.radix), _u32_list(self.galois)
+        keys = _key_list(ctx, self.keys, [0] * len(self.keys), "keys")
+        st = ckks_sum_steps(len(self.radix), radix, elts, keys)
+        st._keep = (radix, elts, keys)
+        return st
+
+
+def _steps(ctx, steps):
+    return None if steps is None else ctypes.byref(steps._c(ctx))
+
+
+def ckks_rotate_sum(ctx, d_ct_in, d_ct_out, batch, level, steps, stream=None):
+    """Sum of each ciphertext over a packed axis; steps: a RotateSum."""
+    n = _w(batch, 2, _lvl(ctx, level), ctx.N)
+    _check(_lib.ckks_rotate_sum(ctx.handle, _dev(ctx, d_ct_in, n, "d_ct_in"), _dev(ctx, d_ct_out, n, "d_ct_out"),
+                                batch, level, _steps(ctx, steps), _stream(stream)), "ckks_rotate_sum")
+
+
+def _drop(nl, levels):
+    """Limbs left after `levels` rescales, or None (the library reports the range error)."""
+    return nl - levels if nl is not None and nl > levels else None
+
+
+def ckks_attn_scores(ctx, d_q, n_q, d_k, n_k, n_grp, level, d_rlk, steps, d_s, stream=None):
+    nl = _lvl(ctx, level)
+    _check(_lib.ckks_attn_scores(ctx.handle, _dev(ctx, d_q, _w(n_grp, n_q, 2, nl, ctx.N), "d_q"), n_q,
+                                 _dev(ctx, d_k, _w(n_grp, n_k, 2, nl, ctx.N), "d_k"), n_k, n_grp, level,
+                                 _dev(ctx, d_rlk, ctx.key_words, "d_rlk"), _steps(ctx, steps),
+                                 _dev(ctx, d_s, _w(n_grp, n_q, n_k, 2, _drop(nl, 1), ctx.N), "d_s"), _stream(stream)),
+           "ckks_attn_scores")
+
+
+def ckks_attn_mix(ctx, d_a, n_q, d_v, n_k, n_grp, d_mask, n_mask, level, d_rlk, steps, d_num, d_den=None, stream=None):
+    nl = _lvl(ctx, level)
+    low = 0 if d_mask is None else 1
+    _check(_lib.ckks_attn_mix(ctx.handle, _dev(ctx, d_a, _w(n_grp, n_q, n_k, 2, nl, ctx.N), "d_a"), n_q,
+                              _dev(ctx, d_v, _w(n_grp, n_k, 2, nl, ctx.N), "d_v"), n_k, n_grp,
+                              _dev(ctx, d_mask, _w(n_mask, n_k, nl, ctx.N), "d_mask", optional=True), n_mask, level,
+                              _dev(ctx, d_rlk, ctx.key_words, "d_rlk"), _steps(ctx, steps),
+                              _dev(ctx, d_num, _w(n_grp, n_q, 2, _drop(nl, low + 1), ctx.N), "d_num"),
+                              _dev(ctx, d_den, _w(n_grp, n_q, 2, _drop(nl, low), ctx.N), "d_den", optional=True),
+                              _stream(stream)), "ckks_attn_mix")
+
+
+def ckks_linattn_chunk(ctx, d_q, d_k, d_v, n_tok, n_grp, d_w, d_r, d_carry, n_row, d_state_in, level, d_rlk, steps,
+                       d_y, d_state_out, stream=None):
+    nl = _lvl(ctx, level)
+    ct, pt = _w(n_tok, n_grp, 2, nl, ctx.N), _w(n_tok, n_row, nl, ctx.N)
+    ns, ny = _drop(nl, 2), _drop(nl, 3)
+    _check(_lib.ckks_linattn_chunk(
+        ctx.handle, _dev(ctx, d_q, ct, "d_q"), _dev(ctx, d_k, ct, "d_k"), _dev(ctx, d_v, ct, "d_v"), n_tok, n_grp,
+        _dev(ctx, d_w, pt, "d_w"), _dev(ctx, d_r, pt, "d_r", optional=True),
+        _dev(ctx, d_carry, _w(n_row, ns, ctx.N), "d_carry", optional=True), n_row,
+        _dev(ctx, d_state_in, _w(n_grp, 2, ns, ctx.N), "d_state_in", optional=True), level,
+        _dev(ctx, d_rlk, ctx.key_words, "d_rlk"), _steps(ctx, steps),
+        _dev(ctx, d_y, _w(n_tok, n_grp, 2, ny, ctx.N), "d_y"),
+        _dev(ctx, d_state_out, _w(n_grp, 2, ns if d_carry is None else ny, ctx.N), "d_state_out"),
+        _stream(stream)), "ckks_linattn_chunk")
+
+
+def ckks_linattn_step(ctx, d_q, d_k, d_v, n_grp, d_decay, n_row, d_state_in, level, d_rlk, steps, d_y, d_state_out,
+                      stream=None):
+    nl = _lvl(ctx, level)
+    ct, ns = _w(n_grp, 2, nl, ctx.N), _drop(nl, 1)
+    _check(_lib.ckks_linattn_step(
+        ctx.handle, _dev(ctx, d_q, ct, "d_q"), _dev(ctx, d_k, ct, "d_k"), _dev(ctx, d_v, ct, "d_v"), n_grp,
+        _dev(ctx, d_decay, _w(n_row, nl, ctx.N), "d_decay", optional=True), n_row,
+        _dev(ctx, d_state_in, ct if d_decay is not None else _w(n_grp, 2, ns, ctx.N), "d_state_in", optional=True),
+        level, _dev(ctx, d_rlk, ctx.key_words, "d_rlk"), _steps(ctx, steps),
+        _dev(ctx, d_y, _w(n_grp, 2, _drop(nl, 2), ctx.N), "d_y"),
+        _dev(ctx, d_state_out, _w(n_grp, 2, ns, ctx.N), "d_state_out"), _stream(stream)), "ckks_linattn_step")
 
 
 def ckks_trace_begin(ctx, kernel):

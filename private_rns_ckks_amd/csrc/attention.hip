@@ -1,0 +1,508 @@
+// Entry points of the attention calls: argument checks, and the composition of
+// slotwise products (attn_kernels.hip), relinearisation and rescale (ops.hip)
+// and the sum over a packed axis (sumrot.hip).  Items go in blocks whose
+// intermediates fit kBlockWords.
+#include <string.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "attention.h"
+
+namespace ckks {
+
+namespace {
+
+// Words of intermediates a call holds at once (4 GiB of the card's 288): at
+// N = 2^16 and 24 limbs some 25 items, enough to fill the chip many times.
+constexpr uint64_t kBlockWords = 1ull << 29;
+
+int block_items(uint64_t per_item, uint64_t items) {
+  return (int)std::max<uint64_t>(1, std::min<uint64_t>({items, kBlockWords / per_item, 1024}));
+}
+
+// Tells the context's buffers that this call's stream is being captured:
+// growing then is an error, and buffers a capture has recorded are kept.
+class CaptureScope {
+ public:
+  CaptureScope(Ctx* c, hipStream_t s) : c_(c) {
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    if (s && hipStreamIsCapturing(s, &st) == hipSuccess && st == hipStreamCaptureStatusActive)
+      c->capturing = c->captured = true;
+  }
+  ~CaptureScope() { c_->capturing = false; }
+
+ private:
+  Ctx* c_;
+};
+
+struct Range {
+  const void* p;
+  uint64_t words;
+};
+
+// Every output against every input and against the other outputs.
+int check_ranges(const std::vector<Range>& outs, const std::vector<Range>& ins) {
+  for (const std::vector<Range>* v : {&outs, &ins})
+    for (const Range& r : *v)
+      if (misaligned(r.p)) return set_error(CKKS_EINVAL, "device buffers must be 16-byte aligned");
+  for (size_t i = 0; i < outs.size(); ++i) {
+    for (const Range& r : ins) REJECT_OVERLAP(outs[i].p, outs[i].words, r.p, r.words, "an input");
+    for (size_t k = 0; k < i; ++k) REJECT_OVERLAP(outs[i].p, outs[i].words, outs[k].p, outs[k].words, "an output");
+  }
+  return CKKS_OK;
+}
+
+uint64_t key_words(const Ctx* c) { return (uint64_t)c->dnum * 2 * (c->L + c->K) * c->N; }
+
+// Checks a plan and adds its keys to the inputs; *st receives it (no stages
+// for NULL).
+int check_steps(const Ctx* c, const ckks_sum_steps* steps, std::vector<Range>& ins, ckks_sum_steps* st) {
+  memset(st, 0, sizeof(*st));
+  if (!steps || steps->n_stage == 0) return CKKS_OK;
+  *st = *steps;
+  if (st->n_stage < 0 || st->n_stage > CKKS_SUM_MAX_STAGES) return set_error(CKKS_EINVAL, "bad number of sum stages");
+  if (!st->radix || !st->galois_elts || !st->d_evks) return set_error(CKKS_EINVAL, "NULL list in the sum stages");
+  int n = 0;
+  for (int k = 0; k < st->n_stage; ++k) {
+    if (st->radix[k] < 2 || st->radix[k] > CKKS_SUM_MAX_RADIX)
+      return set_error(CKKS_EINVAL, "a sum stage's radix must be 2.." + std::to_string(CKKS_SUM_MAX_RADIX));
+    n += st->radix[k] - 1;
+  }
+  for (int r = 0; r < n; ++r) {
+    int rc = check_galois(c, st->galois_elts[r]);
+    if (rc) return rc;
+    if (st->galois_elts[r] == 1) return set_error(CKKS_EINVAL, "a sum stage's element is the identity");
+    if (!st->d_evks[r]) return set_error(CKKS_EINVAL, "NULL key pointer");
+    ins.push_back({st->d_evks[r], key_words(c)});
+  }
+  return CKKS_OK;
+}
+
+int check_count(uint64_t items) {
+  return items > (1u << 24) ? set_error(CKKS_EINVAL, "too many ciphertexts in one call") : CKKS_OK;
+}
+
+// Tail of every product: relinearise n three-part items X ([3][level+1][N]
+// each, contiguous) into R, rescale into Z, and sum Z into out; without stages
+// the rescale writes Z and the copies go to out.
+struct Tail {
+  Ctx* c;
+  hipStream_t s;
+  const uint64_t* rlk;
+  ckks_sum_steps st;
+
+  uint64_t limb(int l) const { return (uint64_t)(l + 1) * c->N; }
+
+  int relin(const uint64_t* X, uint64_t* R, int n, int level) const {
+    return relin_batch(c, s, X, 3 * limb(level), R, 2 * limb(level), n, level, rlk);
+  }
+  int rescale(const uint64_t* R, uint64_t* Z, int n, int level, const uint64_t* acc = nullptr) const {
+    const uint64_t per = (uint64_t)c->N * (2 + 2 * level);
+    int rc = ensure_workspace(c, per * std::min(n, kMaxChunk));
+    if (rc) return rc;
+    return rescale_batch(c, s, R, 2 * limb(level), Z, 2 * limb(level - 1), n, level, c->ws, c->ws_words, nullptr, acc);
+  }
+  int sum(const uint64_t* Z, uint64_t* const* out, int n, int level) const {
+    const uint64_t ct = 2 * limb(level);
+    if (st.n_stage == 0) {
+      for (int b = 0; b < n; ++b)
+        CKKS_HIP_CHECK(hipMemcpyAsync(out[b], Z + b * ct, ct * 8, hipMemcpyDeviceToDevice, s));
+      return CKKS_OK;
+    }
+    int rc = ensure_workspace(c, sum_ws_words(c, level, n, st.n_stage));
+    if (rc) return rc;
+    return sum_stages(c, s, Z, ct, out, n, level, st, c->ws);
+  }
+};
+
+std::vector<uint64_t*> item_pointers(uint64_t* base, uint64_t stride, int n) {
+  std::vector<uint64_t*> p(n);
+  for (int b = 0; b < n; ++b) p[b] = base + b * stride;
+  return p;
+}
+
+int rotate_sum(Ctx* c, const uint64_t* in, uint64_t* out, int batch, int level, const ckks_sum_steps* steps,
+               hipStream_t s) {
+  if (!in || !out || batch < 0) return set_error(CKKS_EINVAL, "NULL pointer or bad batch");
+  int rc = check_level(c, level);
+  if (rc) return rc;
+  if (c->K == 0) return set_error(CKKS_EPARAM, "rotation needs special primes");
+  const uint64_t ct = 2ull * (level + 1) * c->N;
+  if ((rc = check_count(batch))) return rc;
+  std::vector<Range> ins = {{in, ct * batch}};
+  Tail t{c, s, nullptr, {}};
+  if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges({{out, ct * batch}}, ins))) return rc;
+  if (t.st.n_stage == 0) return set_error(CKKS_EINVAL, "a sum needs at least one stage");
+  if (batch == 0) return CKKS_OK;
+  CaptureScope cap(c, s);
+  return t.sum(in, item_pointers(out, ct, batch).data(), batch, level);
+}
+
+int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, int n_grp, int level,
+                const uint64_t* rlk, const ckks_sum_steps* steps, uint64_t* out, hipStream_t s) {
+  if (!q || !k || !rlk || !out || n_q < 0 || n_k < 0 || n_grp < 0)
+    return set_error(CKKS_EINVAL, "NULL pointer or bad count");
+  int rc = check_level(c, level);
+  if (rc) return rc;
+  if (level == 0) return set_error(CKKS_ERANGE, "cannot rescale at level 0");
+  if (c->K == 0) return set_error(CKKS_EPARAM, "relinearisation needs special primes");
+  if ((rc = check_count((uint64_t)n_grp * n_q)) || (rc = check_count((uint64_t)n_grp * n_k)) ||
+      (rc = check_count((uint64_t)n_grp * n_q * n_k)))
+    return rc;
+  const int items = n_grp * n_q * n_k, l = level;
+  const uint64_t N = c->N, lim = (uint64_t)(l + 1) * N, zct = 2ull * l * N;
+  std::vector<Range> ins = {{q, 2 * lim * n_grp * n_q}, {k, 2 * lim * n_grp * n_k}, {rlk, key_words(c)}};
+  Tail t{c, s, rlk, {}};
+  if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges({{out, zct * items}}, ins))) return rc;
+  if (items == 0) return CKKS_OK;
+  CaptureScope cap(c, s);
+  const uint64_t per = 3 * lim + 2 * lim + zct;
+  const int block = block_items(per, items);
+  if ((rc = ensure_aux(c, per * block))) return rc;
+  uint64_t *X = c->aux, *R = X + 3 * lim * block, *Z = R + 2 * lim * block;
+  for (int b0 = 0; b0 < items; b0 += block) {
+    const int n = std::min(block, items - b0);
+    PairArgs a;
+    memset(&a, 0, sizeof(a));
+    a.a = q;
+    a.b = k;
+    a.out = X;
+    a.a_bstride = a.b_bstride = 2 * lim;
+    a.a_comp = a.b_comp = lim;
+    a.out_bstride = 3 * lim;
+    a.prime = c->d_prime;
+    a.log_n = (int)c->log_n;
+    a.nl = l + 1;
+    a.n_k = n_k;
+    a.n_qk = n_q * n_k;
+    a.n_row = 1;
+    a.first = b0;
+    uint64_t* dst = out + b0 * zct;
+    if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin(X, R, n, l))) return rc;
+    if ((rc = t.rescale(R, t.st.n_stage ? Z : dst, n, l))) return rc;
+    if (t.st.n_stage && (rc = t.sum(Z, item_pointers(dst, zct, n).data(), n, l - 1))) return rc;
+  }
+  return CKKS_OK;
+}
+
+int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int n_grp, const uint64_t* mask,
+             int n_mask, int level, const uint64_t* rlk, const ckks_sum_steps* steps, uint64_t* num, uint64_t* den,
+             hipStream_t s) {
+  if (!a || !v || !rlk || !num || n_q < 0 || n_k < 1 || n_grp < 0)
+    return set_error(CKKS_EINVAL, "NULL pointer or bad count");
+  if (mask ? n_mask < 1 || n_mask > std::max(n_grp, 1) : n_mask != 0)
+    return set_error(CKKS_EINVAL, "the mask needs 1..n_grp rows (0 without a mask)");
+  int rc = check_level(c, level);
+  if (rc) return rc;
+  const int l = level, drop = mask ? 2 : 1;  // levels num loses
+  if (l < drop) return set_error(CKKS_ERANGE, "the level must be at least 2 with a mask, 1 without");
+  if (c->K == 0) return set_error(CKKS_EPARAM, "relinearisation needs special primes");
+  if ((rc = check_count((uint64_t)n_grp * n_k)) || (rc = check_count((uint64_t)n_grp * n_q)) ||
+      (rc = check_count((uint64_t)n_grp * n_q * n_k)))
+    return rc;
+  const int rows = n_grp * n_q;
+  const uint64_t N = c->N, lim = (uint64_t)(l + 1) * N;
+  const uint64_t nct = 2ull * (l + 1 - drop) * N, dct = 2ull * (l + 2 - drop) * N, mid = 2ull * l * N;
+  std::vector<Range> ins = {{a, 2 * lim * rows * n_k}, {v, 2 * lim * n_grp * n_k}, {rlk, key_words(c)}};
+  if (mask) ins.push_back({mask, lim * n_mask * n_k});
+  std::vector<Range> outs = {{num, nct * rows}};
+  if (den) outs.push_back({den, dct * rows});
+  Tail t{c, s, rlk, {}};
+  if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges(outs, ins))) return rc;
+  if (rows == 0) return CKKS_OK;
+  CaptureScope cap(c, s);
+  const uint64_t per = 3 * lim + 2 * lim + 2 * lim + mid;
+  const int block = block_items(per, rows);
+  if ((rc = ensure_aux(c, per * block))) return rc;
+  uint64_t *X = c->aux, *D = X + 3 * lim * block, *R = D + 2 * lim * block, *Z = R + 2 * lim * block;
+  for (int b0 = 0; b0 < rows; b0 += block) {
+    const int n = std::min(block, rows - b0);
+    MixArgs m;
+    memset(&m, 0, sizeof(m));
+    m.a = a;
+    m.v = v;
+    m.m = mask;
+    m.num = X;
+    m.den = den ? D : nullptr;
+    m.prime = c->d_prime;
+    m.log_n = (int)c->log_n;
+    m.nl = l + 1;
+    m.n_q = n_q;
+    m.n_k = n_k;
+    m.n_row = mask ? n_mask : 1;
+    m.first = b0;
+    const std::vector<uint64_t*> to = item_pointers(num + b0 * nct, nct, n);
+    if ((rc = launch_mix(c, s, m, n)) || (rc = t.relin(X, R, n, l)) || (rc = t.rescale(R, Z, n, l))) return rc;
+    if (mask) {
+      if ((rc = t.rescale(Z, R, n, l - 1)) || (rc = t.sum(R, to.data(), n, l - 2))) return rc;
+    } else if ((rc = t.sum(Z, to.data(), n, l - 1))) {
+      return rc;
+    }
+    if (!den) continue;
+    const std::vector<uint64_t*> de = item_pointers(den + b0 * dct, dct, n);
+    if (mask) {
+      if ((rc = t.rescale(D, Z, n, l)) || (rc = t.sum(Z, de.data(), n, l - 1))) return rc;
+    } else if ((rc = t.sum(D, de.data(), n, l))) {
+      return rc;
+    }
+  }
+  return CKKS_OK;
+}
+
+// X (three parts) = state x q at `level`, both components of q read at its
+// first level+1 limbs (q's components q_comp apart).
+int state_times_q(Ctx* c, hipStream_t s, const uint64_t* state, const uint64_t* q, uint64_t q_bstride,
+                  uint64_t q_comp, uint64_t* X, int n, int level) {
+  const uint64_t lim = (uint64_t)(level + 1) * c->N;
+  PairArgs a;
+  memset(&a, 0, sizeof(a));
+  a.a = state;
+  a.b = q;
+  a.out = X;
+  a.a_bstride = 2 * lim;
+  a.a_comp = lim;
+  a.b_bstride = q_bstride;
+  a.b_comp = q_comp;
+  a.out_bstride = 3 * lim;
+  a.prime = c->d_prime;
+  a.log_n = (int)c->log_n;
+  a.nl = level + 1;
+  a.n_row = 1;
+  return launch_pair(c, s, a, n);
+}
+
+int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v, int n_tok, int n_grp,
+                  const uint64_t* w, const uint64_t* r, const uint64_t* carry, int n_row, const uint64_t* state_in,
+                  int level, const uint64_t* rlk, const ckks_sum_steps* steps, uint64_t* y, uint64_t* state_out,
+                  hipStream_t s) {
+  if (!q || !k || !v || !w || !rlk || !y || !state_out || n_tok < 1 || n_grp < 0)
+    return set_error(CKKS_EINVAL, "NULL pointer or bad count");
+  if (n_row < 1 || n_row > std::max(n_grp, 1)) return set_error(CKKS_EINVAL, "the weights need 1..n_grp rows");
+  int rc = check_level(c, level);
+  if (rc) return rc;
+  const int l = level;
+  if (l < 3) return set_error(CKKS_ERANGE, "the level must be at least 3");
+  if (c->K == 0) return set_error(CKKS_EPARAM, "relinearisation needs special primes");
+  if ((rc = check_count((uint64_t)n_tok * std::max(n_grp, 1)))) return rc;
+  const uint64_t N = c->N, lim = (uint64_t)(l + 1) * N, items = (uint64_t)n_tok * n_grp;
+  const uint64_t ct = 2 * lim, sct = 2ull * (l - 1) * N, yct = 2ull * (l - 2) * N, oct = carry ? yct : sct;
+  std::vector<Range> ins = {{q, ct * items}, {k, ct * items}, {v, ct * items}, {w, lim * n_tok * n_row},
+                            {rlk, key_words(c)}};
+  if (r) ins.push_back({r, lim * n_tok * n_row});
+  if (carry) ins.push_back({carry, sct / 2 * n_row});
+  if (state_in) ins.push_back({state_in, sct * n_grp});
+  Tail t{c, s, rlk, {}};
+  if ((rc = check_steps(c, steps, ins, &t.st)) ||
+      (rc = check_ranges({{y, yct * items}, {state_out, oct * n_grp}}, ins)))
+    return rc;
+  if (n_grp == 0) return CKKS_OK;
+  CaptureScope cap(c, s);
+  // per (token, group): X / the state's product, R, C, S, Z; per group: the
+  // prefix sums carried from one block of tokens to the next
+  const uint64_t mid = 2ull * l * N, per = 3 * lim + ct + mid + sct + yct;
+  const int gb = block_items(per + 3 * lim, n_grp);
+  const int tb = block_items((per + 3 * lim) * gb, n_tok);
+  const uint64_t nb = (uint64_t)gb * tb;
+  if ((rc = ensure_aux(c, per * nb + 3 * lim * gb))) return rc;
+  uint64_t *X = c->aux, *R = X + 3 * lim * nb, *C = R + ct * nb, *S = C + mid * nb, *Z = S + sct * nb,
+           *P = Z + yct * nb;
+  for (int g0 = 0; g0 < n_grp; g0 += gb) {
+    const int ng = std::min(gb, n_grp - g0);
+    for (int t0 = 0; t0 < n_tok; t0 += tb) {
+      const int nt = std::min(tb, n_tok - t0), n = nt * ng;
+      const uint64_t at = ((uint64_t)t0 * n_grp + g0);
+      ScanArgs sc;
+      memset(&sc, 0, sizeof(sc));
+      sc.k = k + at * ct;
+      sc.v = v + at * ct;
+      sc.w = w + (uint64_t)t0 * n_row * lim;
+      sc.init = t0 ? P : nullptr;
+      sc.out = X;
+      sc.tok_stride = (uint64_t)n_grp * ct;
+      sc.prime = c->d_prime;
+      sc.log_n = (int)c->log_n;
+      sc.nl = l + 1;
+      sc.n_tok = nt;
+      sc.n_grp = ng;
+      sc.n_row = n_row;
+      sc.g0 = g0;
+      if ((rc = launch_scan(c, s, sc))) return rc;
+      if (t0 + nt < n_tok)
+        CKKS_HIP_CHECK(hipMemcpyAsync(P, X + (uint64_t)(nt - 1) * ng * 3 * lim, 3 * lim * ng * 8,
+                                      hipMemcpyDeviceToDevice, s));
+      if ((rc = t.relin(X, R, n, l)) || (rc = t.rescale(R, C, n, l))) return rc;
+      if (state_in) {
+        for (int i = 0; i < nt; ++i)
+          if ((rc = t.rescale(C + (uint64_t)i * ng * mid, S + (uint64_t)i * ng * sct, ng, l - 1, state_in + g0 * sct)))
+            return rc;
+      } else if ((rc = t.rescale(C, S, n, l - 1))) {
+        return rc;
+      }
+      for (int i = 0; i < nt; ++i) {
+        const uint64_t* qt = q + (at + (uint64_t)i * n_grp) * ct;
+        uint64_t* xt = X + (uint64_t)i * ng * 3 * sct / 2;
+        const uint64_t* st = S + (uint64_t)i * ng * sct;
+        if (r) {
+          PlainMulArgs pm;
+          memset(&pm, 0, sizeof(pm));
+          pm.in = qt;
+          pm.in_bstride = ct;
+          pm.in_comp = lim;
+          pm.p = r + (uint64_t)(t0 + i) * n_row * lim;
+          pm.out = R;
+          pm.out_bstride = ct;
+          pm.prime = c->d_prime;
+          pm.log_n = (int)c->log_n;
+          pm.nl = l + 1;
+              pm.n_row = n_row;
+          pm.first = g0;
+          if ((rc = launch_plain_mul(c, s, pm, ng)) || (rc = t.rescale(R, C, ng, l))) return rc;
+          if ((rc = state_times_q(c, s, st, C, mid, mid / 2, xt, ng, l - 2))) return rc;
+        } else if ((rc = state_times_q(c, s, st, qt, ct, lim, xt, ng, l - 2))) {
+          return rc;
+        }
+      }
+      if ((rc = t.relin(X, R, n, l - 2)) || (rc = t.rescale(R, Z, n, l - 2))) return rc;
+      std::vector<uint64_t*> to(n);
+      for (int b = 0; b < n; ++b) to[b] = y + (at + (uint64_t)(b / ng) * n_grp + b % ng) * yct;
+      if ((rc = t.sum(Z, to.data(), n, l - 3))) return rc;
+      if (t0 + nt < n_tok) continue;
+      const uint64_t* last = S + (uint64_t)(nt - 1) * ng * sct;
+      if (!carry) {
+        CKKS_HIP_CHECK(hipMemcpyAsync(state_out + g0 * sct, last, sct * ng * 8, hipMemcpyDeviceToDevice, s));
+        continue;
+      }
+      PlainMulArgs pm;
+      memset(&pm, 0, sizeof(pm));
+      pm.in = last;
+      pm.in_bstride = sct;
+      pm.in_comp = sct / 2;
+      pm.p = carry;
+      pm.out = R;
+      pm.out_bstride = sct;
+      pm.prime = c->d_prime;
+      pm.log_n = (int)c->log_n;
+      pm.nl = l - 1;
+      pm.n_row = n_row;
+      pm.first = g0;
+      if ((rc = launch_plain_mul(c, s, pm, ng)) || (rc = t.rescale(R, state_out + g0 * yct, ng, l - 2))) return rc;
+    }
+  }
+  return CKKS_OK;
+}
+
+int linattn_step(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v, int n_grp, const uint64_t* decay,
+                 int n_row, const uint64_t* state_in, int level, const uint64_t* rlk, const ckks_sum_steps* steps,
+                 uint64_t* y, uint64_t* state_out, hipStream_t s) {
+  if (!q || !k || !v || !rlk || !y || !state_out || n_grp < 0)
+    return set_error(CKKS_EINVAL, "NULL pointer or bad count");
+  if (decay ? n_row < 1 || n_row > std::max(n_grp, 1) : n_row != 0)
+    return set_error(CKKS_EINVAL, "the decay needs 1..n_grp rows (0 without a decay)");
+  int rc = check_level(c, level);
+  if (rc) return rc;
+  const int l = level;
+  if (l < 2) return set_error(CKKS_ERANGE, "the level must be at least 2");
+  if (c->K == 0) return set_error(CKKS_EPARAM, "relinearisation needs special primes");
+  if ((rc = check_count(n_grp))) return rc;
+  const uint64_t N = c->N, lim = (uint64_t)(l + 1) * N, ct = 2 * lim, sct = 2ull * l * N, yct = 2ull * (l - 1) * N;
+  const uint64_t in_ct = decay ? ct : sct;
+  std::vector<Range> ins = {{q, ct * n_grp}, {k, ct * n_grp}, {v, ct * n_grp}, {rlk, key_words(c)}};
+  if (decay) ins.push_back({decay, lim * n_row});
+  if (state_in) ins.push_back({state_in, in_ct * n_grp});
+  Tail t{c, s, rlk, {}};
+  if ((rc = check_steps(c, steps, ins, &t.st)) ||
+      (rc = check_ranges({{y, yct * n_grp}, {state_out, sct * n_grp}}, ins)))
+    return rc;
+  if (n_grp == 0) return CKKS_OK;
+  CaptureScope cap(c, s);
+  const uint64_t per = 3 * lim + ct + yct;
+  const int block = block_items(per, n_grp);
+  if ((rc = ensure_aux(c, per * block))) return rc;
+  uint64_t *X = c->aux, *R = X + 3 * lim * block, *Z = R + ct * block;
+  for (int b0 = 0; b0 < n_grp; b0 += block) {
+    const int n = std::min(block, n_grp - b0);
+    PairArgs a;
+    memset(&a, 0, sizeof(a));
+    a.a = k;
+    a.b = v;
+    a.out = X;
+    a.a_bstride = a.b_bstride = ct;
+    a.a_comp = a.b_comp = lim;
+    a.out_bstride = 3 * lim;
+    if (state_in && decay) {
+      a.decay = decay;
+      a.state = state_in;
+      a.state_bstride = ct;
+    }
+    a.prime = c->d_prime;
+    a.log_n = (int)c->log_n;
+    a.nl = l + 1;
+    a.n_row = decay ? n_row : 1;
+    a.first = b0;
+    uint64_t* S = state_out + b0 * sct;
+    if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin(X, R, n, l)) ||
+        (rc = t.rescale(R, S, n, l, state_in && !decay ? state_in + b0 * sct : nullptr)))
+      return rc;
+    if ((rc = state_times_q(c, s, S, q + b0 * ct, ct, lim, X, n, l - 1)) || (rc = t.relin(X, R, n, l - 1)) ||
+        (rc = t.rescale(R, Z, n, l - 1)))
+      return rc;
+    if ((rc = t.sum(Z, item_pointers(y + b0 * yct, yct, n).data(), n, l - 2))) return rc;
+  }
+  return CKKS_OK;
+}
+
+}  // namespace
+}  // namespace ckks
+
+using namespace ckks;
+
+// The composition uses host containers; a failed host allocation is reported
+// like a failed device one.
+#define NO_THROW(call)                                                          \
+  try {                                                                         \
+    return call;                                                                \
+  } catch (const std::exception&) {                                             \
+    return CKKS_ENOMEM;                                                         \
+  }
+
+extern "C" {
+
+int ckks_rotate_sum(ckks_ctx* ctx, const uint64_t* d_ct_in, uint64_t* d_ct_out, int batch, int level,
+                    const ckks_sum_steps* steps, ckks_stream_t stream) {
+  CTX_OR_FAIL(ctx);
+  NO_THROW(rotate_sum(ctx, d_ct_in, d_ct_out, batch, level, steps, stream));
+}
+
+int ckks_attn_scores(ckks_ctx* ctx, const uint64_t* d_q, int n_q, const uint64_t* d_k, int n_k, int n_grp, int level,
+                     const uint64_t* d_rlk, const ckks_sum_steps* steps, uint64_t* d_s, ckks_stream_t stream) {
+  CTX_OR_FAIL(ctx);
+  NO_THROW(attn_scores(ctx, d_q, n_q, d_k, n_k, n_grp, level, d_rlk, steps, d_s, stream));
+}
+
+int ckks_attn_mix(ckks_ctx* ctx, const uint64_t* d_a, int n_q, const uint64_t* d_v, int n_k, int n_grp,
+                  const uint64_t* d_mask, int n_mask, int level, const uint64_t* d_rlk, const ckks_sum_steps* steps,
+                  uint64_t* d_num, uint64_t* d_den, ckks_stream_t stream) {
+  CTX_OR_FAIL(ctx);
+  NO_THROW(attn_mix(ctx, d_a, n_q, d_v, n_k, n_grp, d_mask, n_mask, level, d_rlk, steps, d_num, d_den, stream));
+}
+
+int ckks_linattn_chunk(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, const uint64_t* d_v, int n_tok,
+                       int n_grp, const uint64_t* d_w, const uint64_t* d_r, const uint64_t* d_carry, int n_row,
+                       const uint64_t* d_state_in, int level, const uint64_t* d_rlk, const ckks_sum_steps* steps,
+                       uint64_t* d_y, uint64_t* d_state_out, ckks_stream_t stream) {
+  CTX_OR_FAIL(ctx);
+  NO_THROW(linattn_chunk(ctx, d_q, d_k, d_v, n_tok, n_grp, d_w, d_r, d_carry, n_row, d_state_in, level, d_rlk, steps,
+                         d_y, d_state_out, stream));
+}
+
+int ckks_linattn_step(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, const uint64_t* d_v, int n_grp,
+                      const uint64_t* d_decay, int n_row, const uint64_t* d_state_in, int level,
+                      const uint64_t* d_rlk, const ckks_sum_steps* steps, uint64_t* d_y, uint64_t* d_state_out,
+                      ckks_stream_t stream) {
+  CTX_OR_FAIL(ctx);
+  NO_THROW(linattn_step(ctx, d_q, d_k, d_v, n_grp, d_decay, n_row, d_state_in, level, d_rlk, steps, d_y, d_state_out,
+                        stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,167 @@
+// Slotwise kernels of the attention calls, on ciphertext words in NTT form:
+// products with plaintext rows, tensor products and their weighted sums.  One
+// thread per word of a limb, blockIdx.y the limb, blockIdx.z the item.
+#include "arith.h"
+#include "attention.h"
+#include "convert.h"
+
+namespace ckks {
+
+namespace {
+
+template <bool WIDE>
+__device__ __forceinline__ uint64_t mul_red(const Split<WIDE>& x, const Split<WIDE>& y, const RedConst& pc) {
+  AccT<WIDE> m{};
+  acc_mac<WIDE>(m, x, y);
+  return acc_reduce<WIDE>(m, pc.q, pc.r64, pc.r64p, pc.inv1);
+}
+
+template <bool WIDE>
+__global__ __launch_bounds__(256) void plain_mul_kernel(PlainMulArgs a) {
+  const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
+  const int i = blockIdx.y, b = blockIdx.z;
+  const RedConst pc = red_const((ConstPrime)a.prime, i);
+  const uint64_t off = ((uint64_t)i << a.log_n) + c, lim = (uint64_t)a.nl << a.log_n;
+  const uint64_t row = (uint64_t)((a.first + b) % a.n_row);
+  const Split<WIDE> p = split_word<WIDE>(a.p[row * lim + off]);
+  const uint64_t* x = a.in + b * a.in_bstride + off;
+  uint64_t* o = a.out + b * a.out_bstride + off;
+  o[0] = mul_red<WIDE>(p, split_word<WIDE>(x[0]), pc);
+  o[lim] = mul_red<WIDE>(p, split_word<WIDE>(x[a.in_comp]), pc);
+}
+
+template <bool WIDE>
+__global__ __launch_bounds__(256) void pair_kernel(PairArgs a) {
+  const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
+  const int i = blockIdx.y;
+  const int item = blockIdx.z, p = a.first + item;
+  const int ia = a.n_qk ? p / a.n_k : p;
+  const int ib = a.n_qk ? (p / a.n_qk) * a.n_k + p % a.n_k : p;
+  const RedConst pc = red_const((ConstPrime)a.prime, i);
+  const uint64_t off = ((uint64_t)i << a.log_n) + c, lim = (uint64_t)a.nl << a.log_n;
+  const uint64_t* x = a.a + ia * a.a_bstride + off;
+  const uint64_t* y = a.b + ib * a.b_bstride + off;
+  uint64_t* d = a.out + item * a.out_bstride + off;
+  const Split<WIDE> x0 = split_word<WIDE>(x[0]), x1 = split_word<WIDE>(x[a.a_comp]);
+  const Split<WIDE> y0 = split_word<WIDE>(y[0]), y1 = split_word<WIDE>(y[a.b_comp]);
+  AccT<WIDE> m0{}, m1{}, m2{};
+  acc_mac<WIDE>(m0, x0, y0);
+  acc_mac<WIDE>(m1, x0, y1);
+  acc_mac<WIDE>(m1, x1, y0);
+  acc_mac<WIDE>(m2, x1, y1);
+  if (a.decay) {
+    const uint64_t* st = a.state + p * a.state_bstride + off;
+    const Split<WIDE> g = split_word<WIDE>(a.decay[(uint64_t)(p % a.n_row) * lim + off]);
+    acc_mac<WIDE>(m0, g, split_word<WIDE>(st[0]));
+    acc_mac<WIDE>(m1, g, split_word<WIDE>(st[lim]));
+  }
+  d[0] = acc_reduce<WIDE>(m0, pc.q, pc.r64, pc.r64p, pc.inv1);
+  d[lim] = acc_reduce<WIDE>(m1, pc.q, pc.r64, pc.r64p, pc.inv1);
+  d[2 * lim] = acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1);
+}
+
+template <bool WIDE>
+__global__ __launch_bounds__(256) void scan_kernel(ScanArgs a) {
+  const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
+  const int i = blockIdx.y, g = blockIdx.z;
+  const RedConst pc = red_const((ConstPrime)a.prime, i);
+  const uint64_t off = ((uint64_t)i << a.log_n) + c, lim = (uint64_t)a.nl << a.log_n;
+  const uint64_t row = (uint64_t)((a.g0 + g) % a.n_row);
+  uint64_t r0 = 0, r1 = 0, r2 = 0;
+  if (a.init) {
+    const uint64_t* x = a.init + (uint64_t)g * 3 * lim + off;
+    r0 = x[0];
+    r1 = x[lim];
+    r2 = x[2 * lim];
+  }
+  for (int t = 0; t < a.n_tok; ++t) {
+    const uint64_t* k = a.k + t * a.tok_stride + (uint64_t)g * 2 * lim + off;
+    const uint64_t* v = a.v + t * a.tok_stride + (uint64_t)g * 2 * lim + off;
+    const Split<WIDE> w = split_word<WIDE>(a.w[((uint64_t)t * a.n_row + row) * lim + off]);
+    const Split<WIDE> k0 = split_word<WIDE>(mul_red<WIDE>(w, split_word<WIDE>(k[0]), pc));
+    const Split<WIDE> k1 = split_word<WIDE>(mul_red<WIDE>(w, split_word<WIDE>(k[lim]), pc));
+    const Split<WIDE> v0 = split_word<WIDE>(v[0]), v1 = split_word<WIDE>(v[lim]);
+    AccT<WIDE> m0{}, m1{}, m2{};
+    acc_mac<WIDE>(m0, k0, v0);
+    acc_mac<WIDE>(m1, k0, v1);
+    acc_mac<WIDE>(m1, k1, v0);
+    acc_mac<WIDE>(m2, k1, v1);
+    r0 = add_mod(r0, acc_reduce<WIDE>(m0, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+    r1 = add_mod(r1, acc_reduce<WIDE>(m1, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+    r2 = add_mod(r2, acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+    uint64_t* o = a.out + ((uint64_t)t * a.n_grp + g) * 3 * lim + off;
+    o[0] = r0;
+    o[lim] = r1;
+    o[2 * lim] = r2;
+  }
+}
+
+template <bool WIDE>
+__global__ __launch_bounds__(256) void mix_kernel(MixArgs a) {
+  const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
+  const int i = blockIdx.y, b = blockIdx.z;
+  const int row = a.first + b, g = row / a.n_q;
+  const RedConst pc = red_const((ConstPrime)a.prime, i);
+  const uint64_t off = ((uint64_t)i << a.log_n) + c, lim = (uint64_t)a.nl << a.log_n;
+  uint64_t r0 = 0, r1 = 0, r2 = 0, e0 = 0, e1 = 0;
+  for (int j = 0; j < a.n_k; ++j) {
+    const uint64_t* x = a.a + ((uint64_t)row * a.n_k + j) * 2 * lim + off;
+    const uint64_t* v = a.v + ((uint64_t)g * a.n_k + j) * 2 * lim + off;
+    uint64_t a0 = x[0], a1 = x[lim];
+    if (a.m) {
+      const Split<WIDE> m = split_word<WIDE>(a.m[((uint64_t)(g % a.n_row) * a.n_k + j) * lim + off]);
+      a0 = mul_red<WIDE>(m, split_word<WIDE>(a0), pc);
+      a1 = mul_red<WIDE>(m, split_word<WIDE>(a1), pc);
+    }
+    e0 = add_mod(e0, a0, pc.q);
+    e1 = add_mod(e1, a1, pc.q);
+    const Split<WIDE> s0 = split_word<WIDE>(a0), s1 = split_word<WIDE>(a1);
+    const Split<WIDE> v0 = split_word<WIDE>(v[0]), v1 = split_word<WIDE>(v[lim]);
+    AccT<WIDE> m0{}, m1{}, m2{};
+    acc_mac<WIDE>(m0, s0, v0);
+    acc_mac<WIDE>(m1, s0, v1);
+    acc_mac<WIDE>(m1, s1, v0);
+    acc_mac<WIDE>(m2, s1, v1);
+    r0 = add_mod(r0, acc_reduce<WIDE>(m0, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+    r1 = add_mod(r1, acc_reduce<WIDE>(m1, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+    r2 = add_mod(r2, acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+  }
+  uint64_t* o = a.num + (uint64_t)b * 3 * lim + off;
+  o[0] = r0;
+  o[lim] = r1;
+  o[2 * lim] = r2;
+  if (a.den) {
+    uint64_t* e = a.den + (uint64_t)b * 2 * lim + off;
+    e[0] = e0;
+    e[lim] = e1;
+  }
+}
+
+}  // namespace
+
+#define ATTN_LAUNCH(kern, batch)                                                                             \
+  hipLaunchKernelGGL(c->wide ? kern<true> : kern<false>, dim3(c->N / 256, a.nl, batch), dim3(256), 0, s, a); \
+  CKKS_HIP_CHECK(hipGetLastError());                                                                         \
+  return CKKS_OK
+
+int launch_plain_mul(Ctx* c, hipStream_t s, const PlainMulArgs& a, int batch) {
+  TraceScope ts(c, s, "attn_mac", (double)batch * a.nl * 4 * c->N);
+  ATTN_LAUNCH(plain_mul_kernel, batch);
+}
+
+int launch_pair(Ctx* c, hipStream_t s, const PairArgs& a, int batch) {
+  TraceScope ts(c, s, "attn_mac", (double)batch * a.nl * (a.decay ? 9 : 7) * c->N);
+  ATTN_LAUNCH(pair_kernel, batch);
+}
+
+int launch_scan(Ctx* c, hipStream_t s, const ScanArgs& a) {
+  TraceScope ts(c, s, "attn_mac", (double)a.n_tok * a.n_grp * a.nl * 11 * c->N);
+  ATTN_LAUNCH(scan_kernel, a.n_grp);
+}
+
+int launch_mix(Ctx* c, hipStream_t s, const MixArgs& a, int rows) {
+  TraceScope ts(c, s, "attn_mac", (double)rows * a.n_k * a.nl * 11 * c->N);
+  ATTN_LAUNCH(mix_kernel, rows);
+}
+
+}  // namespace ckks

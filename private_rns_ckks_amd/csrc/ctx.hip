@@ -19,8 +19,16 @@ int set_error(int code, const std::string& msg) {
 
 // Grows a context-owned device buffer; the device is synchronised before the
 // old buffer is freed, since queued work may still use it.
-static int grow(uint64_t*& buf, size_t& have, size_t words, const char* what) {
+static int grow(Ctx* c, uint64_t*& buf, size_t& have, size_t words, const char* what) {
   if (words <= have) return CKKS_OK;
+  if (c->capturing)
+    return set_error(CKKS_EHIP, std::string("the ") + what + " would grow while the stream is being captured: run a "
+                                "call of this size first");
+  if (buf && c->captured) {
+    c->retired.push_back(buf);
+    buf = nullptr;
+    have = 0;
+  }
   if (buf) {
     CKKS_HIP_CHECK(hipDeviceSynchronize());
     CKKS_HIP_CHECK(hipFree(buf));
@@ -35,8 +43,8 @@ static int grow(uint64_t*& buf, size_t& have, size_t words, const char* what) {
   return CKKS_OK;
 }
 
-int ensure_workspace(Ctx* c, size_t words) { return grow(c->ws, c->ws_words, words, "workspace"); }
-int ensure_aux(Ctx* c, size_t words) { return grow(c->aux, c->aux_words, words, "operand buffer"); }
+int ensure_workspace(Ctx* c, size_t words) { return grow(c, c->ws, c->ws_words, words, "workspace"); }
+int ensure_aux(Ctx* c, size_t words) { return grow(c, c->aux, c->aux_words, words, "operand buffer"); }
 
 TraceScope::TraceScope(Ctx* c, hipStream_t s, const char* family, double units)
     : c_(c), s_(s), on_(!c->no_alloc && !c->trace.name.empty() && c->trace.name == family) {
@@ -101,6 +109,9 @@ static int upload(void** dst, const void* src, size_t bytes) {
 
 int ensure_lanes(Ctx* c) {
   if (c->lane[0]) return CKKS_OK;
+  if (c->capturing)
+    return set_error(CKKS_EHIP, "the internal streams would be created while the stream is being captured: run a call "
+                                "of this size first");
   for (int i = 0; i < Ctx::kMaxLanes; ++i) {
     CKKS_HIP_CHECK(hipStreamCreateWithFlags(&c->lane[i], hipStreamNonBlocking));
     CKKS_HIP_CHECK(hipEventCreateWithFlags(&c->join_ev[i], hipEventDisableTiming));
@@ -121,6 +132,7 @@ static void destroy(Ctx* c) {
   void* bufs[] = {c->d_prime, c->d_tw_fwd, c->d_tw_inv, c->d_modup, c->d_moddown, c->d_rescale, c->ws, c->aux};
   for (void* b : bufs)
     if (b) (void)hipFree(b);
+  for (uint64_t* b : c->retired) (void)hipFree(b);
   delete c;
 }
 

@@ -73,6 +73,11 @@ struct Ctx {
   size_t ws_words = 0;
   uint64_t* aux = nullptr;        // intermediate operands of composite calls (BSGS matvec)
   size_t aux_words = 0;
+  // A stream capture has recorded the buffers above: growing keeps the old
+  // ones (a graph may replay on them) until the context is destroyed.
+  bool captured = false;
+  bool capturing = false;          // the running call's stream is being captured: growing is an error
+  std::vector<uint64_t*> retired;
   TraceState trace;
   // Set while an allocation-free call runs: tracing records no events then
   // (creating them could allocate).

@@ -11,6 +11,7 @@
 
 #include "host_math.h"
 #include "kernels.h"
+#include "ops.h"
 
 namespace ckks {
 
@@ -42,6 +43,8 @@ uint32_t inv_mod_2n(uint32_t g, uint32_t two_n) {
   return x & (two_n - 1);
 }
 
+}  // namespace
+
 int check_level(const Ctx* c, int level) {
   if (level < 0 || level >= (int)c->L) return set_error(CKKS_ERANGE, "level out of range");
   return CKKS_OK;
@@ -55,8 +58,7 @@ int check_galois(const Ctx* c, uint32_t g) {
 // Rescale of `batch` items: in [2][level+1][N] at in + b*in_stride -> out
 // [2][level][N], plus acc (same layout as out, may equal it) when given.
 int rescale_batch(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
-                  int batch, int level, uint64_t* ws, uint64_t ws_words, const uint64_t* add0 = nullptr,
-                  const uint64_t* acc = nullptr) {
+                  int batch, int level, uint64_t* ws, uint64_t ws_words, const uint64_t* add0, const uint64_t* acc) {
   const uint32_t N = c->N;
   const uint64_t per = (uint64_t)N * (2 + 2 * level);
   const int chunk = (int)std::max<uint64_t>(1, std::min<uint64_t>(kMaxChunk, ws_words / per));
@@ -75,6 +77,8 @@ int rescale_batch(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride,
   }
   return CKKS_OK;
 }
+
+namespace {
 
 // Chunks of a batch on `lanes` internal streams: fork_lanes makes them wait
 // for the work already on s; join_lanes makes s wait for them (also after a
@@ -340,25 +344,6 @@ int rotate_hoisted(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride
 }  // namespace ckks
 
 using namespace ckks;
-
-// device buffers are read and written with 16-byte vector accesses
-static bool misaligned(const void* p) { return ((uintptr_t)p & 15) != 0; }
-
-// True when the word ranges [a, a + a_words) and [b, b + b_words) share a
-// byte.  Outputs are written by some workgroups while other workgroups still
-// read (and gather) the inputs, so an output that overlaps an input or a key
-// would race; such calls are rejected before any launch.
-static bool overlap(const void* a, uint64_t a_words, const void* b, uint64_t b_words) {
-  if (!a || !b || !a_words || !b_words) return false;
-  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-  return a0 < b0 + b_words * 8 && b0 < a0 + a_words * 8;
-}
-#define REJECT_OVERLAP(a, an, b, bn, what) \
-  if (overlap((a), (an), (b), (bn))) return set_error(CKKS_EINVAL, "output overlaps " what)
-
-#define CTX_OR_FAIL(ctx)                                             \
-  if (!(ctx)) return set_error(CKKS_EINVAL, "ctx is NULL");         \
-  if (hipSetDevice((ctx)->device) != hipSuccess) return set_error(CKKS_EHIP, "hipSetDevice failed")
 
 extern "C" {
 
@@ -911,10 +896,12 @@ int ckks_ptmatvec(ckks_ctx* ctx, const uint64_t* d_x, int n_in, const uint64_t* 
 
 }  // extern "C"
 
+namespace ckks {
+
 // Relinearisation of `batch` three-part ciphertexts T (item b at
 // T + b*t_stride, [3][l+1][N]) into out (item b at out + b*out_stride,
 // [2][l+1][N]): (T0, T1) + KS_{s^2 -> s}(T2), in chunks over the lanes.
-static int relin_batch(Ctx* c, hipStream_t s, const uint64_t* T, uint64_t t_stride, uint64_t* out,
+int relin_batch(Ctx* c, hipStream_t s, const uint64_t* T, uint64_t t_stride, uint64_t* out,
                        uint64_t out_stride, int batch, int level, const uint64_t* rlk) {
   const int nq = level + 1;
   const uint64_t limb = (uint64_t)nq * c->N;
@@ -944,6 +931,8 @@ static int relin_batch(Ctx* c, hipStream_t s, const uint64_t* T, uint64_t t_stri
   }
   return join_lanes(c, s, lanes, rc);
 }
+
+}  // namespace ckks
 
 extern "C" {
 

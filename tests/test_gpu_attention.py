@@ -1,0 +1,598 @@
+"""Bit-exact parity of the attention calls (ckks_rotate_sum, ckks_attn_scores,
+ckks_attn_mix, ckks_linattn_chunk, ckks_linattn_step) against the CPU oracle,
+through the C interface: every output word must be equal, so there are no
+tolerances.  Words are uniform residues (what encryption makes them), the top
+of the residue range where lazy arithmetic comes closest to overflowing, or
+real encryptions."""
+import numpy as np
+import pytest
+
+import ckks_synth as S
+from gpu_util import announce, config_pair, empty_dev, make_pair, misaligned_dev, to_dev, to_host, torch_cuda
+from helpers import encrypt_slots, galois_key, relin_key, secret
+
+pytestmark = pytest.mark.gpu
+
+# (log_n, L, q_bits, K, p_bits, dnum)
+SETS = {
+    "tiny": (12, 4, 30, 1, 60, 4),
+    "small": (10, 6, 40, 2, 60, 3),
+    "c3": (12, 24, 54, 8, 60, 3),
+    "one_digit": (11, 12, 50, 12, 60, 1),
+    "many_digits": (10, 9, 54, 1, 60, 9),
+    "q57": (13, 6, 57, 3, 60, 2),
+    "wide": (12, 6, 62, 2, 61, 3),
+    "wide61": (11, 8, 61, 4, 62, 2),
+}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    torch_cuda()
+    import private_rns_ckks_amd as L
+
+    return L
+
+
+@pytest.fixture(scope="module")
+def sets(lib, orc):
+    made = {}
+
+    def get(name):
+        if name not in made:
+            made[name] = make_pair(lib, orc, *SETS[name])
+        return made[name]
+
+    return get
+
+
+def words(P, seed, tag, limbs, lead, top=False):
+    fn = S.top_limbs if top else S.uniform_limbs
+    return fn(S.stream(seed, "attn/" + tag), P.q[:limbs], P.N, lead=lead)
+
+
+def key(P, seed, tag, top=False):
+    fn = S.top_limbs if top else S.uniform_limbs
+    return fn(S.stream(seed, "attn/key/" + tag), P.mods, P.N, lead=(P.dnum, 2))
+
+
+def steps(lib, P, radices, seed=0, top=False, stride=1):
+    """(library stages, (galois, keys) for the oracle)."""
+    gal, host = [], []
+    for s, r in enumerate(radices):
+        gal.append([P.galois(stride * k) for k in range(1, r)])
+        host.append([key(P, seed, "%d.%d" % (s, k), top) for k in range(1, r)])
+        stride = stride * r % (P.N // 2) or 1
+    return lib.RotateSum(gal, [[to_dev(k) for k in ks] for ks in host]), (gal, host)
+
+
+def same(got, ref, what=""):
+    got = to_host(got)
+    assert got.shape == ref.shape
+    assert np.array_equal(got, ref), "%s: %d words differ" % (what, int((got != ref).sum()))
+
+
+# ---------------------------------------------------------------- rotate_sum
+
+SUMS = [
+    ("tiny", 3, 1, [2]), ("tiny", 0, 3, [3, 2]), ("small", 5, 1, [4, 8]), ("small", 2, 9, [5]), ("small", 0, 2, [7]),
+    ("c3", 23, 2, [8, 2]), ("c3", 16, 3, [3]), ("c3", 7, 1, [4]), ("one_digit", 11, 2, [6]), ("one_digit", 4, 1, [2, 2]),
+    ("many_digits", 8, 2, [9]), ("many_digits", 3, 17, [2]), ("q57", 5, 3, [8]), ("wide", 5, 2, [8]), ("wide", 1, 1, [3]),
+    ("wide61", 7, 2, [5, 3]), ("small", 3, 1, [32]), ("tiny", 2, 8, [4]),
+]
+
+
+@pytest.mark.parametrize("name,level,batch,radices", SUMS, ids=lambda v: str(v).replace(" ", ""))
+def test_rotate_sum_parity(lib, orc, sets, name, level, batch, radices):
+    ctx, P = sets(name)
+    announce("rotate_sum %s level=%d batch=%d radices=%s" % (name, level, batch, radices))
+    st, (gal, keys) = steps(lib, P, radices)
+    x = words(P, level, "sum", level + 1, (batch, 2))
+    out = empty_dev(x.shape)
+    lib.ckks_rotate_sum(ctx, to_dev(x), out, batch, level, st)
+    same(out, np.stack([orc.rotate_sum(P, level, c, gal, keys) for c in x]))
+
+
+@pytest.mark.parametrize("name,level,radices", [("c3", 23, [8]), ("q57", 5, [32]), ("many_digits", 8, [16]),
+                                                 ("wide", 5, [16]), ("wide61", 7, [8]), ("one_digit", 11, [8])])
+def test_rotate_sum_top_of_range(lib, orc, sets, name, level, radices):
+    ctx, P = sets(name)
+    announce("rotate_sum top of range %s" % name)
+    st, (gal, keys) = steps(lib, P, radices, top=True)
+    x = words(P, 1, "top", level + 1, (1, 2), top=True)
+    x[0, 0, 0, :] = np.uint64(P.q[0] - 1)
+    out = empty_dev(x.shape)
+    lib.ckks_rotate_sum(ctx, to_dev(x), out, 1, level, st)
+    same(out[0], orc.rotate_sum(P, level, x[0], gal, keys))
+
+
+def test_rotate_sum_elements_twice_and_conjugation(lib, orc, sets):
+    """The same element twice in a stage, and elements outside the powers of 5."""
+    ctx, P = sets("small")
+    announce("rotate_sum repeated elements")
+    g = P.galois(3)
+    gal = [[g, g, 2 * P.N - 1, 3]]
+    host = [[key(P, 4, str(i)) for i in (0, 0, 1, 2)]]
+    x = words(P, 4, "twice", 6, (1, 2))
+    dev = [[to_dev(k) for k in host[0]]]
+    dev[0][1] = dev[0][0]  # one key buffer, used twice
+    out = empty_dev(x.shape)
+    lib.ckks_rotate_sum(ctx, to_dev(x), out, 1, 5, lib.RotateSum(gal, dev))
+    same(out[0], orc.rotate_sum(P, 5, x[0], gal, host))
+
+
+def test_rotate_sum_encrypted(lib, orc, sets):
+    """An encrypted vector summed over 16 slots at stride 4 decrypts to the sums (2^-12, as the tiny
+    single-rotation set's other tests: 30-bit primes, scale 2^25)."""
+    ctx, P = sets("tiny")
+    announce("rotate_sum encrypted")
+    s, s_ntt = secret(orc, P, 6, 64)
+    gal = [[P.galois(4 * k) for k in range(1, 4)], [P.galois(16 * k) for k in range(1, 4)]]
+    keys = [[to_dev(galois_key(orc, P, s_ntt, g, 6, "g%d" % g)) for g in gs] for gs in gal]
+    z = S.uniform_slots(S.stream(6, "z"), P.N // 2)
+    ct = encrypt_slots(orc, P, s_ntt, z, 2.0 ** 25, 3, 6, "ct")
+    out = empty_dev((1,) + ct.shape)
+    lib.ckks_rotate_sum(ctx, to_dev(ct[None]), out, 1, 3, lib.RotateSum(gal, keys))
+    got = orc.decrypt(P, 3, to_host(out)[0], s_ntt, 2.0 ** 25)
+    ref = sum(np.roll(z, -4 * k) for k in range(16))
+    assert np.max(np.abs(got - ref)) / np.max(np.abs(ref)) < 2.0 ** -12
+
+
+# ---------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("name,level,G,nq,nk,radices", [
+    ("tiny", 3, 1, 1, 1, [2]), ("tiny", 1, 1, 2, 3, []), ("small", 5, 2, 3, 2, [4]), ("c3", 23, 1, 1, 2, [3]),
+    ("c3", 12, 2, 1, 1, [2, 2]), ("wide", 5, 1, 2, 1, [3]), ("one_digit", 11, 1, 1, 1, [2]), ("small", 2, 1, 7, 5, [2])])
+def test_attn_scores_parity(lib, orc, sets, name, level, G, nq, nk, radices):
+    ctx, P = sets(name)
+    announce("attn_scores %s level=%d %dx%dx%d" % (name, level, G, nq, nk))
+    st, ref_st = steps(lib, P, radices)
+    q, k = words(P, level, "q", level + 1, (G, nq, 2)), words(P, level, "k", level + 1, (G, nk, 2))
+    rlk = key(P, 0, "rlk")
+    out = empty_dev((G, nq, nk, 2, level, P.N))
+    lib.ckks_attn_scores(ctx, to_dev(q), nq, to_dev(k), nk, G, level, to_dev(rlk), st if radices else None, out)
+    same(out, orc.attn_scores(P, level, q, k, rlk, *ref_st))
+
+
+@pytest.mark.parametrize("name,level,G,nq,nk,M,radices", [
+    ("tiny", 3, 1, 1, 1, 1, [2]), ("tiny", 2, 2, 2, 3, 1, []), ("tiny", 1, 1, 1, 2, 0, [2]), ("small", 5, 3, 2, 2, 2, [4]),
+    ("small", 4, 2, 1, 9, 0, [2, 2]), ("c3", 12, 1, 2, 3, 1, [3]), ("wide", 5, 2, 1, 2, 2, [2]),
+    ("wide61", 7, 1, 1, 9, 1, []), ("small", 3, 1, 11, 1, 1, [2])])
+@pytest.mark.parametrize("top", [False, True])
+def test_attn_mix_parity(lib, orc, sets, name, level, G, nq, nk, M, radices, top):
+    ctx, P = sets(name)
+    announce("attn_mix %s level=%d %dx%dx%d mask=%d top=%d" % (name, level, G, nq, nk, M, top))
+    st, ref_st = steps(lib, P, radices)
+    a, v = words(P, level, "a", level + 1, (G, nq, nk, 2), top), words(P, level, "v", level + 1, (G, nk, 2), top)
+    m = words(P, level, "m", level + 1, (M, nk), top) if M else None
+    rlk = key(P, 0, "rlk", top)
+    low = 2 if M else 1
+    num, den = empty_dev((G, nq, 2, level + 1 - low, P.N)), empty_dev((G, nq, 2, level + 2 - low, P.N))
+    args = (ctx, to_dev(a), nq, to_dev(v), nk, G, to_dev(m) if M else None, M, level, to_dev(rlk),
+            st if radices else None)
+    lib.ckks_attn_mix(*args, num, den)
+    ref = orc.attn_mix(P, level, a, v, m, rlk, *ref_st)
+    same(num, ref[0], "num")
+    same(den, ref[1], "den")
+    num.zero_()
+    lib.ckks_attn_mix(*args, num)  # without the normaliser
+    same(num, ref[0], "num alone")
+
+
+def test_attn_mix_mask_that_leaves_nothing(lib, orc, sets):
+    """A group whose mask rows are all zero: the trivial zero ciphertext through every step."""
+    ctx, P = sets("small")
+    announce("attn_mix empty group")
+    a, v = words(P, 3, "ea", 6, (2, 1, 2, 2)), words(P, 3, "ev", 6, (2, 2, 2))
+    m = words(P, 3, "em", 6, (2, 2))
+    m[1] = 0
+    st, ref_st = steps(lib, P, [4])
+    rlk = key(P, 0, "rlk")
+    num, den = empty_dev((2, 1, 2, 4, P.N)), empty_dev((2, 1, 2, 5, P.N))
+    lib.ckks_attn_mix(ctx, to_dev(a), 1, to_dev(v), 2, 2, to_dev(m), 2, 5, to_dev(rlk), st, num, den)
+    ref = orc.attn_mix(P, 5, a, v, m, rlk, *ref_st)
+    same(num, ref[0])
+    same(den, ref[1])
+    assert not to_host(num)[1].any() and not to_host(den)[1].any()
+
+
+CHUNKS = [
+    # name, level, T, G, rows, read, carry, state, radices
+    ("tiny", 3, 1, 1, 1, True, True, True, [2]), ("tiny", 3, 4, 1, 1, False, False, False, []),
+    ("small", 5, 3, 2, 2, True, True, True, [4]), ("small", 5, 5, 3, 2, True, False, True, [2]),
+    ("small", 4, 2, 2, 1, False, True, False, [2, 2]), ("c3", 23, 2, 1, 1, True, True, True, [3]),
+    ("wide", 5, 3, 1, 1, True, True, True, [2]), ("wide61", 7, 2, 2, 1, True, False, False, [3]),
+    ("one_digit", 11, 2, 1, 1, True, True, True, [2]), ("small", 3, 13, 1, 1, True, True, True, [2]),
+]
+
+
+def chunk_case(P, level, T, G, R, read, carry, state, seed, top=False):
+    d = {x: words(P, seed, x, level + 1, (T, G, 2), top) for x in "qkv"}
+    d["w"] = words(P, seed, "w", level + 1, (T, R), top)
+    d["r"] = words(P, seed, "r", level + 1, (T, R), top) if read else None
+    d["carry"] = words(P, seed, "carry", level - 1, (R,), top) if carry else None
+    d["state"] = words(P, seed, "state", level - 1, (G, 2), top) if state else None
+    return d
+
+
+def dev(x):
+    return None if x is None else to_dev(x)
+
+
+def run_chunk(lib, ctx, P, d, level, T, G, R, rlk, st):
+    y = empty_dev((T, G, 2, level - 2, P.N))
+    out = empty_dev((G, 2, level - 1 if d["carry"] is None else level - 2, P.N))
+    lib.ckks_linattn_chunk(ctx, dev(d["q"]), dev(d["k"]), dev(d["v"]), T, G, dev(d["w"]), dev(d["r"]), dev(d["carry"]),
+                           R, dev(d["state"]), level, to_dev(rlk), st, y, out)
+    return y, out
+
+
+@pytest.mark.parametrize("name,level,T,G,R,read,carry,state,radices", CHUNKS)
+@pytest.mark.parametrize("top", [False, True])
+def test_linattn_chunk_parity(lib, orc, sets, name, level, T, G, R, read, carry, state, radices, top):
+    ctx, P = sets(name)
+    announce("linattn_chunk %s level=%d T=%d G=%d R=%d read=%d carry=%d state=%d top=%d"
+             % (name, level, T, G, R, read, carry, state, top))
+    st, ref_st = steps(lib, P, radices)
+    d = chunk_case(P, level, T, G, R, read, carry, state, level + T, top)
+    d["w"][-1, 0] = 0  # a padded token
+    rlk = key(P, 0, "rlk", top)
+    y, out = run_chunk(lib, ctx, P, d, level, T, G, R, rlk, st if radices else None)
+    ref = orc.linattn_chunk(P, level, d["q"], d["k"], d["v"], d["w"], d["r"], d["carry"], d["state"], rlk, *ref_st)
+    same(y, ref[0], "y")
+    same(out, ref[1], "state")
+
+
+@pytest.mark.parametrize("name,level,G,R,state,radices", [
+    ("tiny", 3, 1, 1, True, [2]), ("tiny", 2, 1, 0, True, [3]), ("tiny", 3, 2, 1, False, []), ("small", 5, 3, 2, True, [4]),
+    ("small", 4, 11, 11, True, [2]), ("small", 2, 2, 0, False, [2, 2]), ("c3", 23, 2, 1, True, [3]),
+    ("c3", 12, 1, 0, True, [8]), ("wide", 5, 2, 1, True, [2]), ("wide61", 7, 1, 0, True, [2]),
+    ("many_digits", 8, 1, 1, True, [2]), ("one_digit", 6, 1, 1, True, [2])])
+@pytest.mark.parametrize("top", [False, True])
+def test_linattn_step_parity(lib, orc, sets, name, level, G, R, state, radices, top):
+    ctx, P = sets(name)
+    announce("linattn_step %s level=%d G=%d R=%d state=%d top=%d" % (name, level, G, R, state, top))
+    st, ref_st = steps(lib, P, radices)
+    q, k, v = (words(P, level, x, level + 1, (G, 2), top) for x in "qkv")
+    dec = words(P, level, "dec", level + 1, (R,), top) if R else None
+    s_in = words(P, level, "st", level + (1 if R else 0), (G, 2), top) if state else None
+    rlk = key(P, 0, "rlk", top)
+    y, out = empty_dev((G, 2, level - 1, P.N)), empty_dev((G, 2, level, P.N))
+    lib.ckks_linattn_step(ctx, to_dev(q), to_dev(k), to_dev(v), G, dev(dec), R, dev(s_in), level, to_dev(rlk),
+                          st if radices else None, y, out)
+    ref = orc.linattn_step(P, level, q, k, v, dec, s_in, rlk, *ref_st)
+    same(y, ref[0], "y")
+    same(out, ref[1], "state")
+
+
+def test_prompt_then_tokens_then_cross_attention(lib, orc, sets):
+    """The calls as a decoder layer runs them: a prompt's chunk, single tokens on its state, scores of the
+    outputs against an encoder's keys, the polynomial weights, the mix; one stream, nothing in between."""
+    ctx, P = sets("c3")
+    announce("prompt, tokens, cross attention")
+    st, ref_st = steps(lib, P, [4])
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    T, G, R, lv = 3, 2, 1, 23
+    d = chunk_case(P, lv, T, G, R, True, True, True, 77)
+    y, state = run_chunk(lib, ctx, P, d, lv, T, G, R, rlk, st)
+    ref_y, ref_s = orc.linattn_chunk(P, lv, d["q"], d["k"], d["v"], d["w"], d["r"], d["carry"], d["state"], rlk, *ref_st)
+    lv = 20
+    for i in range(2):
+        q, k, v = (words(P, 80 + i, x, lv + 1, (G, 2)) for x in "qkv")
+        dec = words(P, 80 + i, "dec", lv + 1, (R,))
+        ny, ns = empty_dev((G, 2, lv - 1, P.N)), empty_dev((G, 2, lv, P.N))
+        lib.ckks_linattn_step(ctx, to_dev(q), to_dev(k), to_dev(v), G, to_dev(dec), R, state, lv, d_rlk, st, ny, ns)
+        ref_ny, ref_s = orc.linattn_step(P, lv, q, k, v, dec, ref_s, rlk, *ref_st)
+        state, lv = ns, lv - 1
+    lq = lv - 1  # the last step's output level
+    keys_ = words(P, 90, "ek", lq + 1, (G, 2, 2))
+    vals = words(P, 90, "ev", lq - 2, (G, 2, 2))
+    s = empty_dev((G, 1, 2, 2, lq, P.N))
+    lib.ckks_attn_scores(ctx, ny, 1, to_dev(keys_), 2, G, lq, d_rlk, st, s)
+    ref_sc = orc.attn_scores(P, lq, ref_ny[:, None], keys_, rlk, *ref_st)
+    p = empty_dev((G * 2, 2, lq - 2, P.N))
+    lib.ckks_poly_eval_tree(ctx, s, G * 2, lq - 1, 2.0 ** 54, [1.0, 1.0, 0.5], d_rlk, p)
+    ref_p, _ = orc.poly_eval_tree(P, lq - 1, ref_sc.reshape((-1,) + ref_sc.shape[3:]), 2.0 ** 54, [1.0, 1.0, 0.5], rlk)
+    la = lq - 3
+    mask = words(P, 90, "em", la + 1, (1, 2))
+    num, den = empty_dev((G, 1, 2, la - 1, P.N)), empty_dev((G, 1, 2, la, P.N))
+    lib.ckks_attn_mix(ctx, p, 1, to_dev(vals), 2, G, to_dev(mask), 1, la, d_rlk, st, num, den)
+    ref = orc.attn_mix(P, la, ref_p.reshape((G, 1, 2) + ref_p.shape[1:]), vals, mask, rlk, *ref_st)
+    same(y, ref_y)
+    same(num, ref[0])
+    same(den, ref[1])
+
+
+# ---------------------------------------------------------------- use
+
+def test_bytes_outside_the_outputs_stay(lib, orc, sets):
+    """Outputs inside a larger buffer: the words before and behind them are left as they were."""
+    torch = torch_cuda()
+    ctx, P = sets("small")
+    announce("guard words")
+    st, _ = steps(lib, P, [3])
+    rlk = to_dev(key(P, 0, "rlk"))
+    lv, G, N = 5, 3, P.N
+    q, k, v = (to_dev(words(P, 1, x, lv + 1, (2, G, 2))) for x in "qkv")
+    w = to_dev(words(P, 1, "w", lv + 1, (2, 1)))
+    ny, ns = 2 * G * 2 * (lv - 2) * N, G * 2 * (lv - 1) * N
+    buf = torch.full((ny + ns + 6 * N,), -7, dtype=torch.int64, device="cuda")
+    y, s = buf[2 * N:2 * N + ny], buf[4 * N + ny:4 * N + ny + ns]
+    lib.ckks_linattn_chunk(ctx, q, k, v, 2, G, w, None, None, 1, None, lv, rlk, st, y, s)
+    h = to_host(buf).view(np.int64)
+    for part in (h[:2 * N], h[2 * N + ny:4 * N + ny], h[4 * N + ny + ns:]):
+        assert (part == -7).all()
+    assert (h[2 * N:2 * N + ny] != -7).all() and (h[4 * N + ny:4 * N + ny + ns] != -7).all()
+
+
+def test_blocks_of_items_and_tokens(lib, orc, sets):
+    """More tokens, groups and items than one launch of a stage takes; repeated calls give the same words."""
+    torch = torch_cuda()
+    ctx, P = sets("small")
+    announce("many items")
+    st, ref_st = steps(lib, P, [2])
+    rlk = key(P, 0, "rlk")
+    T, G = 21, 2
+    d = chunk_case(P, 3, T, G, 1, True, False, True, 5)
+    y, out = run_chunk(lib, ctx, P, d, 3, T, G, 1, rlk, st)
+    first = y.clone()
+    ref = orc.linattn_chunk(P, 3, d["q"], d["k"], d["v"], d["w"], d["r"], None, d["state"], rlk, *ref_st)
+    same(y, ref[0])
+    same(out, ref[1])
+    y2, _ = run_chunk(lib, ctx, P, d, 3, T, G, 1, rlk, st)
+    assert torch.equal(first, y2)
+
+
+def test_on_another_stream(lib, orc, sets):
+    """A side stream, while the default stream is busy: the call waits for nothing but its own stream."""
+    torch = torch_cuda()
+    ctx, P = sets("small")
+    announce("side stream")
+    st, (gal, keys) = steps(lib, P, [4])
+    x = words(P, 2, "stream", 6, (2, 2))
+    dx, out = to_dev(x), empty_dev(x.shape)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        lib.ckks_rotate_sum(ctx, dx, out, 2, 5, st)  # the current stream
+    side.synchronize()
+    ref = np.stack([orc.rotate_sum(P, 5, c, gal, keys) for c in x])
+    same(out, ref)
+    out.zero_()
+    torch.cuda.synchronize()
+    lib.ckks_rotate_sum(ctx, dx, out, 2, 5, st, stream=side)
+    side.synchronize()
+    same(out, ref)
+
+
+def test_captured_step_replays(lib, orc):
+    """A step captured into a graph after one eager call: every replay equals the eager words, with new
+    inputs, with eager work of the same context between the replays, and after a larger call has grown the
+    context's buffers."""
+    torch = torch_cuda()
+    ctx, P = make_pair(lib, orc, *SETS["small"])
+    announce("captured step")
+    st, ref_st = steps(lib, P, [2, 2])
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    lv, G = 5, 6  # two chunks of the relinearisation: the internal streams join the capture
+
+    def inputs(seed):
+        return [words(P, seed, x, lv + 1, (G, 2)) for x in "qkv"] + [words(P, seed, "dec", lv + 1, (1,)),
+                                                                     words(P, seed, "st", lv + 1, (G, 2))]
+
+    bufs = [to_dev(x) for x in inputs(0)]
+    y, out = empty_dev((G, 2, lv - 1, P.N)), empty_dev((G, 2, lv, P.N))
+
+    def call():
+        lib.ckks_linattn_step(ctx, bufs[0], bufs[1], bufs[2], G, bufs[3], 1, bufs[4], lv, d_rlk, st, y, out)
+
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        call()  # sizes the context's buffers
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for i in range(4):
+        host = inputs(10 + i)
+        for b, h in zip(bufs, host):
+            b.copy_(to_dev(h))
+        y.zero_()
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        q, k, v, dec, s_in = host
+        ref = orc.linattn_step(P, lv, q, k, v, dec, s_in, rlk, *ref_st)
+        same(y, ref[0], "replay %d" % i)
+        same(out, ref[1], "replay %d" % i)
+        if i == 1:  # a larger eager call grows the buffers the graph was captured on
+            big = words(P, 50, "big", 6, (40, 2))
+            o = empty_dev(big.shape)
+            lib.ckks_rotate_sum(ctx, to_dev(big), o, 40, 5, st)
+            same(o[39], orc.rotate_sum(P, 5, big[39], *ref_st))
+        call()
+        torch.cuda.synchronize()
+        same(y, ref[0], "eager after replay %d" % i)
+    del graph
+    ctx.close()
+
+
+def test_capture_of_a_first_call_is_refused(lib, orc):
+    """A call that would have to grow the context's buffers during a capture raises and leaves the capture
+    usable."""
+    torch = torch_cuda()
+    ctx, P = make_pair(lib, orc, *SETS["small"])
+    announce("capture without a first call")
+    st, _ = steps(lib, P, [2])
+    x, out = to_dev(words(P, 2, "cap", 6, (1, 2))), empty_dev((1, 2, 6, P.N))
+    marker = torch.zeros(8, device="cuda")
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        with pytest.raises(lib.CKKSError) as e:
+            lib.ckks_rotate_sum(ctx, x, out, 1, 5, st)
+        marker.add_(1.0)
+    assert e.value.code == lib.CKKS_EHIP and "captured" in str(e.value)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert marker.tolist() == [1.0] * 8
+    lib.ckks_rotate_sum(ctx, x, out, 1, 5, st)
+    torch.cuda.synchronize()
+    ctx.close()
+
+
+# ---------------------------------------------------------------- refusals
+
+def refused(lib, code, fn, text=None):
+    with pytest.raises(lib.CKKSError) as e:
+        fn()
+    assert e.value.code == code, str(e.value)
+    if text:
+        assert text in str(e.value)
+
+
+def test_refusals(lib, orc, sets):
+    torch = torch_cuda()
+    ctx, P = sets("tiny")
+    announce("refusals")
+    N = P.N
+    st, _ = steps(lib, P, [2])
+    rlk = to_dev(key(P, 0, "rlk"))
+    x = to_dev(words(P, 1, "x", 4, (2, 2)))
+    pt = to_dev(words(P, 1, "pt", 4, (2,)))
+    out = torch.full((2, 2, 4, N), 5, dtype=torch.int64, device="cuda")
+    out2 = torch.full((2, 2, 4, N), 5, dtype=torch.int64, device="cuda")
+    k1 = st.keys[0]
+
+    def rs(steps_, batch=1, level=3, o=out, i=x):
+        return lambda: lib.ckks_rotate_sum(ctx, i, o, batch, level, steps_)
+
+    refused(lib, lib.CKKS_EINVAL, rs(lib.RotateSum([], [])), "at least one stage")
+    refused(lib, lib.CKKS_EINVAL, rs(None), "at least one stage")
+    refused(lib, lib.CKKS_EINVAL, rs(lib.RotateSum([[]], [[]])), "radix")
+    refused(lib, lib.CKKS_EINVAL, rs(lib.RotateSum([[5] * 32], [[k1] * 32])), "radix")
+    refused(lib, lib.CKKS_EINVAL, rs(lib.RotateSum([[5]] * 17, [[k1]] * 17)), "number of sum stages")
+    refused(lib, lib.CKKS_EINVAL, rs(lib.RotateSum([[4]], [[k1]])), "odd")
+    refused(lib, lib.CKKS_EINVAL, rs(lib.RotateSum([[2 * N + 1]], [[k1]])), "odd")
+    refused(lib, lib.CKKS_EINVAL, rs(lib.RotateSum([[1]], [[k1]])), "identity")
+    refused(lib, lib.CKKS_ERANGE, rs(st, level=4))
+    refused(lib, lib.CKKS_ERANGE, rs(st, level=-1))
+    refused(lib, lib.CKKS_EINVAL, rs(st, batch=-1))
+    refused(lib, lib.CKKS_EINVAL, rs(st, o=x), "overlaps")
+    refused(lib, lib.CKKS_EINVAL, rs(st, o=k1.view(-1)[: 2 * 4 * N]), "overlaps")
+    mis = misaligned_dev((1, 2, 4, N))
+    refused(lib, lib.CKKS_EINVAL, rs(st, o=mis), "aligned")
+    refused(lib, lib.CKKS_EINVAL, rs(lib.RotateSum([[5]], [[misaligned_dev(tuple(k1.shape))]])), "aligned")
+    with pytest.raises(lib.ArgumentError):
+        rs(lib.RotateSum([[5]], [[None]]))()
+    with pytest.raises(lib.ArgumentError):
+        rs(st, batch=3)()
+    with pytest.raises(lib.ArgumentError):
+        rs(lib.RotateSum([[5]], [[x]]))()  # too short for a key
+
+    sc = lambda nq=1, nk=1, G=1, lv=3, o=out, r=rlk: lambda: lib.ckks_attn_scores(ctx, x, nq, x, nk, G, lv, r, st, o)
+    refused(lib, lib.CKKS_ERANGE, sc(lv=0))
+    refused(lib, lib.CKKS_ERANGE, sc(lv=9))
+    refused(lib, lib.CKKS_EINVAL, sc(nq=-1))
+    refused(lib, lib.CKKS_EINVAL, sc(o=x), "overlaps")
+    rc = lib.lib().ckks_attn_scores(ctx.handle, x.data_ptr(), 5000, x.data_ptr(), 0, 5000, 3, rlk.data_ptr(), None,
+                                    out.data_ptr(), None)
+    assert rc == lib.CKKS_EINVAL and "too many" in lib.ckks_last_error()
+
+    def mx(nq=1, nk=1, G=1, m=pt, M=1, lv=3, o=out, e=out2):
+        return lambda: lib.ckks_attn_mix(ctx, x, nq, x, nk, G, m, M, lv, rlk, st, o, e)
+
+    refused(lib, lib.CKKS_EINVAL, mx(nk=0))
+    refused(lib, lib.CKKS_EINVAL, mx(M=0), "mask")
+    refused(lib, lib.CKKS_EINVAL, mx(M=2), "mask")
+    refused(lib, lib.CKKS_EINVAL, mx(m=None, M=1), "mask")
+    refused(lib, lib.CKKS_ERANGE, mx(lv=1))
+    refused(lib, lib.CKKS_ERANGE, mx(m=None, M=0, lv=0))
+    refused(lib, lib.CKKS_EINVAL, mx(e=out), "overlaps")
+    refused(lib, lib.CKKS_EINVAL, mx(o=x), "overlaps")
+
+    def ch(T=1, G=1, R=1, lv=3, o=out, so=out2, carry=None, state=None):
+        return lambda: lib.ckks_linattn_chunk(ctx, x, x, x, T, G, pt, None, carry, R, state, lv, rlk, st, o, so)
+
+    refused(lib, lib.CKKS_EINVAL, ch(T=0))
+    refused(lib, lib.CKKS_EINVAL, ch(G=-1))
+    refused(lib, lib.CKKS_EINVAL, ch(R=0), "rows")
+    refused(lib, lib.CKKS_EINVAL, ch(R=2), "rows")
+    refused(lib, lib.CKKS_ERANGE, ch(lv=2))
+    refused(lib, lib.CKKS_EINVAL, ch(so=out), "overlaps")
+    refused(lib, lib.CKKS_EINVAL, ch(state=out2), "overlaps")
+
+    def sp(G=1, dec=pt, R=1, state=None, lv=3, o=out, so=out2):
+        return lambda: lib.ckks_linattn_step(ctx, x, x, x, G, dec, R, state, lv, rlk, st, o, so)
+
+    refused(lib, lib.CKKS_EINVAL, sp(R=0), "rows")
+    refused(lib, lib.CKKS_EINVAL, sp(dec=None, R=1), "rows")
+    refused(lib, lib.CKKS_EINVAL, sp(G=-2))
+    refused(lib, lib.CKKS_ERANGE, sp(lv=1))
+    refused(lib, lib.CKKS_EINVAL, sp(state=out2), "overlaps")
+    with pytest.raises(lib.ArgumentError):
+        sp(G=2, R=2, lv=3, o=out.view(-1)[: 8 * N - 2])()
+    torch.cuda.synchronize()
+    assert (out == 5).all() and (out2 == 5).all()  # a refused call writes nothing
+
+
+def test_no_special_primes_is_refused(lib, orc):
+    announce("no special primes")
+    q = lib.ckks_find_primes(10, 40, 4)
+    ctx = lib.Context(10, q, [], 2)
+    x = to_dev(np.zeros((1, 2, 4, 1024), dtype=np.uint64))
+    k = to_dev(np.zeros((2, 2, 4, 1024), dtype=np.uint64))
+    st = lib.RotateSum([[5]], [[k]])
+    o, o2 = empty_dev((1, 2, 4, 1024)), empty_dev((1, 2, 4, 1024))
+    pt = to_dev(np.zeros((1, 4, 1024), dtype=np.uint64))
+    refused(lib, lib.CKKS_EPARAM, lambda: lib.ckks_rotate_sum(ctx, x, o, 1, 3, st))
+    refused(lib, lib.CKKS_EPARAM, lambda: lib.ckks_attn_scores(ctx, x, 1, x, 1, 1, 3, k, st, o))
+    refused(lib, lib.CKKS_EPARAM, lambda: lib.ckks_attn_mix(ctx, x, 1, x, 1, 1, None, 0, 3, k, st, o))
+    refused(lib, lib.CKKS_EPARAM, lambda: lib.ckks_linattn_chunk(ctx, x, x, x, 1, 1, pt, None, None, 1, None, 3, k, st, o,
+                                                                 o2))
+    refused(lib, lib.CKKS_EPARAM, lambda: lib.ckks_linattn_step(ctx, x, x, x, 1, None, 0, None, 3, k, st, o, o2))
+    ctx.close()
+
+
+def test_nothing_to_do(lib, orc, sets):
+    ctx, P = sets("tiny")
+    announce("empty calls")
+    st, _ = steps(lib, P, [2])
+    rlk = to_dev(key(P, 0, "rlk"))
+    x, pt = to_dev(words(P, 1, "x", 4, (1, 2))), to_dev(words(P, 1, "pt", 4, (1,)))
+    torch = torch_cuda()
+    o, o2 = (torch.full((1, 2, 4, P.N), 5, dtype=torch.int64, device="cuda") for _ in range(2))
+    lib.ckks_rotate_sum(ctx, x, o, 0, 3, st)
+    lib.ckks_attn_scores(ctx, x, 0, x, 1, 1, 3, rlk, st, o)
+    lib.ckks_attn_scores(ctx, x, 1, x, 0, 1, 3, rlk, st, o)
+    lib.ckks_attn_mix(ctx, x, 0, x, 1, 1, pt, 1, 3, rlk, st, o, o2)
+    lib.ckks_linattn_chunk(ctx, x, x, x, 1, 0, pt, None, None, 1, None, 3, rlk, st, o, o2)
+    lib.ckks_linattn_step(ctx, x, x, x, 0, pt, 1, None, 3, rlk, st, o, o2)
+    torch.cuda.synchronize()
+    assert (o == 5).all() and (o2 == 5).all()
+
+
+@pytest.mark.parametrize("op", ["sum", "step"])
+def test_full_size(lib, orc, op):
+    """N = 2^16, 24 + 8 primes at the top level: one ciphertext against the oracle, word for word."""
+    ctx, P = config_pair(lib, orc, "C3")
+    announce("full size %s" % op)
+    st, ref_st = steps(lib, P, [3])
+    if op == "sum":
+        x = words(P, 1, "full", 24, (1, 2))
+        out = empty_dev(x.shape)
+        lib.ckks_rotate_sum(ctx, to_dev(x), out, 1, 23, st)
+        same(out[0], orc.rotate_sum(P, 23, x[0], *ref_st))
+    else:
+        q, k, v, s_in = (words(P, 1, t, 13, (1, 2)) for t in ("q", "k", "v", "s"))
+        dec, rlk = words(P, 1, "dec", 13, (1,)), key(P, 0, "rlk")
+        y, out = empty_dev((1, 2, 11, P.N)), empty_dev((1, 2, 12, P.N))
+        lib.ckks_linattn_step(ctx, to_dev(q), to_dev(k), to_dev(v), 1, to_dev(dec), 1, to_dev(s_in), 12, to_dev(rlk), st,
+                              y, out)
+        ref = orc.linattn_step(P, 12, q, k, v, dec, s_in, rlk, *ref_st)
+        same(y, ref[0])
+        same(out, ref[1])
+    ctx.close()
