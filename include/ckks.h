@@ -135,9 +135,8 @@ typedef struct {
  * rotations), "automorph", "modup",
  * "moddown_conv", "rescale", "tensor", "ptmac", "ctmac", "add",
  * "const_mul", "term_mac" (polynomial evaluation's constant multiples),
- * "ip_gather", "sum_ip" and "sum_combine" (inner product and last step of a
- * stage of ckks_rotate_sum), "attn_mac" (slotwise products of the attention
- * calls).  NULL or "" stops tracing.
+ * "ip_gather", "sum_ip" (inner product of a stage of ckks_rotate_sum),
+ * "attn_mac" (slotwise products of the attention calls).  NULL or "" stops tracing.
  * Tracing adds two event records per traced launch and nothing else. */
 int ckks_trace_begin(ckks_ctx* ctx, const char* kernel);
 /* Waits for the recorded events, returns the totals and stops tracing. */

@@ -12,9 +12,9 @@ constexpr int kSumItems = 8;                        // items of one launch of a 
 size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage);
 
 // `batch` ciphertexts (item b at in + b*in_stride) through every stage of the
-// checked plan; item b's sum goes to out[b].  ws holds sum_ws_words.
-int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* const* out, int batch,
-               int level, const ckks_sum_steps& st, uint64_t* ws);
+// checked plan into out + b*out_stride.  ws holds sum_ws_words.
+int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
+               int batch, int level, const ckks_sum_steps& st, uint64_t* ws);
 
 // out[b] = p[(first + b) % n_row] * in[b] on both components, limbs 0..nl-1.
 struct PlainMulArgs {

@@ -103,24 +103,17 @@ struct Tail {
     if (rc) return rc;
     return rescale_batch(c, s, R, 2 * limb(level), Z, 2 * limb(level - 1), n, level, c->ws, c->ws_words, nullptr, acc);
   }
-  int sum(const uint64_t* Z, uint64_t* const* out, int n, int level) const {
+  int sum(const uint64_t* Z, uint64_t* out, int n, int level) const {
     const uint64_t ct = 2 * limb(level);
     if (st.n_stage == 0) {
-      for (int b = 0; b < n; ++b)
-        CKKS_HIP_CHECK(hipMemcpyAsync(out[b], Z + b * ct, ct * 8, hipMemcpyDeviceToDevice, s));
+      CKKS_HIP_CHECK(hipMemcpyAsync(out, Z, ct * n * 8, hipMemcpyDeviceToDevice, s));
       return CKKS_OK;
     }
     int rc = ensure_workspace(c, sum_ws_words(c, level, n, st.n_stage));
     if (rc) return rc;
-    return sum_stages(c, s, Z, ct, out, n, level, st, c->ws);
+    return sum_stages(c, s, Z, ct, out, ct, n, level, st, c->ws);
   }
 };
-
-std::vector<uint64_t*> item_pointers(uint64_t* base, uint64_t stride, int n) {
-  std::vector<uint64_t*> p(n);
-  for (int b = 0; b < n; ++b) p[b] = base + b * stride;
-  return p;
-}
 
 int rotate_sum(Ctx* c, const uint64_t* in, uint64_t* out, int batch, int level, const ckks_sum_steps* steps,
                hipStream_t s) {
@@ -136,7 +129,7 @@ int rotate_sum(Ctx* c, const uint64_t* in, uint64_t* out, int batch, int level, 
   if (t.st.n_stage == 0) return set_error(CKKS_EINVAL, "a sum needs at least one stage");
   if (batch == 0) return CKKS_OK;
   CaptureScope cap(c, s);
-  return t.sum(in, item_pointers(out, ct, batch).data(), batch, level);
+  return t.sum(in, out, batch, level);
 }
 
 int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, int n_grp, int level,
@@ -181,7 +174,7 @@ int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, 
     uint64_t* dst = out + b0 * zct;
     if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin(X, R, n, l))) return rc;
     if ((rc = t.rescale(R, t.st.n_stage ? Z : dst, n, l))) return rc;
-    if (t.st.n_stage && (rc = t.sum(Z, item_pointers(dst, zct, n).data(), n, l - 1))) return rc;
+    if (t.st.n_stage && (rc = t.sum(Z, dst, n, l - 1))) return rc;
   }
   return CKKS_OK;
 }
@@ -232,18 +225,18 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
     m.n_k = n_k;
     m.n_row = mask ? n_mask : 1;
     m.first = b0;
-    const std::vector<uint64_t*> to = item_pointers(num + b0 * nct, nct, n);
+    uint64_t* to = num + b0 * nct;
     if ((rc = launch_mix(c, s, m, n)) || (rc = t.relin(X, R, n, l)) || (rc = t.rescale(R, Z, n, l))) return rc;
     if (mask) {
-      if ((rc = t.rescale(Z, R, n, l - 1)) || (rc = t.sum(R, to.data(), n, l - 2))) return rc;
-    } else if ((rc = t.sum(Z, to.data(), n, l - 1))) {
+      if ((rc = t.rescale(Z, R, n, l - 1)) || (rc = t.sum(R, to, n, l - 2))) return rc;
+    } else if ((rc = t.sum(Z, to, n, l - 1))) {
       return rc;
     }
     if (!den) continue;
-    const std::vector<uint64_t*> de = item_pointers(den + b0 * dct, dct, n);
+    uint64_t* de = den + b0 * dct;
     if (mask) {
-      if ((rc = t.rescale(D, Z, n, l)) || (rc = t.sum(Z, de.data(), n, l - 1))) return rc;
-    } else if ((rc = t.sum(D, de.data(), n, l))) {
+      if ((rc = t.rescale(D, Z, n, l)) || (rc = t.sum(Z, de, n, l - 1))) return rc;
+    } else if ((rc = t.sum(D, de, n, l))) {
       return rc;
     }
   }
@@ -364,9 +357,10 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
         }
       }
       if ((rc = t.relin(X, R, n, l - 2)) || (rc = t.rescale(R, Z, n, l - 2))) return rc;
-      std::vector<uint64_t*> to(n);
-      for (int b = 0; b < n; ++b) to[b] = y + (at + (uint64_t)(b / ng) * n_grp + b % ng) * yct;
-      if ((rc = t.sum(Z, to.data(), n, l - 3))) return rc;
+      // the block's outputs are contiguous when it holds every group
+      for (int i = 0; i < (ng == n_grp ? 1 : nt); ++i)
+        if ((rc = t.sum(Z + (uint64_t)i * ng * yct, y + (at + (uint64_t)i * n_grp) * yct, ng == n_grp ? n : ng, l - 3)))
+          return rc;
       if (t0 + nt < n_tok) continue;
       const uint64_t* last = S + (uint64_t)(nt - 1) * ng * sct;
       if (!carry) {
@@ -447,7 +441,7 @@ int linattn_step(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v
     if ((rc = state_times_q(c, s, S, q + b0 * ct, ct, lim, X, n, l - 1)) || (rc = t.relin(X, R, n, l - 1)) ||
         (rc = t.rescale(R, Z, n, l - 1)))
       return rc;
-    if ((rc = t.sum(Z, item_pointers(y + b0 * yct, yct, n).data(), n, l - 2))) return rc;
+    if ((rc = t.sum(Z, y + b0 * yct, n, l - 2))) return rc;
   }
   return CKKS_OK;
 }

@@ -251,6 +251,14 @@ static int build_tables(Ctx* c) {
     md.push_back(v);
     md.push_back(shoup(v, qi));
   }
+  c->md.pmod = md.size();
+  for (uint32_t i = 0; i < L; ++i) {
+    const uint64_t qi = c->mod[i];
+    uint64_t prod = 1;
+    for (uint32_t k = 0; k < K; ++k) prod = mulmod(prod, c->mod[L + k] % qi, qi);
+    md.push_back(prod);
+    md.push_back(shoup(prod, qi));
+  }
   if ((rc = upload((void**)&c->d_moddown, md.data(), md.size() * 8))) return rc;
   return CKKS_OK;
 }

@@ -41,8 +41,9 @@ struct ModUpEntry {
 //   [2K, 2K + K*L)     : [phat_k * P^-1]_{q_i}, row k, column i
 //   [.., + 2L)         : {[P^-1]_{q_i}, Shoup}
 //   [.., + 2L)         : {[2^64 P^-1]_{q_i}, Shoup} (Montgomery sums times P^-1 in one product)
+//   [.., + 2L)         : {[P]_{q_i}, Shoup}
 struct ModDownLayout {
-  size_t phinv, conv, pinv, pinv64;
+  size_t phinv, conv, pinv, pinv64, pmod;
 };
 
 // Kernel timing trace (see ckks_trace_begin): HIP event pairs recorded on the

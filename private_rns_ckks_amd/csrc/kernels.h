@@ -101,6 +101,13 @@ int ks_decompose(Ctx* c, hipStream_t s, int level, int n_in, const uint64_t* c1,
 int ks_hoisted_chunk(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, const uint64_t* dec,
                      const uint64_t* c1, uint64_t out_stride, uint64_t* ws);
 
+// Last steps of a key switch for n_items accumulators A (item i at A + i*per,
+// [2][next][N], NTT form): out = ModDown(acc) (+ add, gathered through add_g)
+// (+ accum), the ModDown scratch of item i at W + i*per; buffers of it[0] at
+// the given strides.
+int ks_back(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uint64_t* A, uint64_t* W, uint64_t per,
+            uint64_t add_stride, uint64_t accum_stride, uint64_t out_stride, int out_comp_limbs);
+
 int launch_automorph_ntt(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t* out, int npoly, int nl, uint64_t pstride,
                          uint32_t g);
 int launch_automorph_coeff(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t* out, int npoly, int nl,

@@ -783,6 +783,8 @@ int moddown_steps(Ctx* c, hipStream_t s, int level, int n_items, uint64_t* A, ui
   return ntt_pass_only(c, s, W, W, wstride, wstride, n_items, jobs, false, true, 0, nullptr, nullptr);
 }
 
+}  // namespace
+
 // Steps F to I for n_items accumulators A (item i at A + i*per, [2][next][N]
 // NTT form) with W as the ModDown scratch: out = ModDown(acc) (+ add, gathered
 // through add_g) (+ accum).
@@ -856,8 +858,6 @@ int ks_back(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uin
   }
   return CKKS_OK;
 }
-
-}  // namespace
 
 // Workspace of the fused pipeline per item: Y [nq] (inverse row pass of the
 // input), E [beta][next] (raised digits after the forward column pass), A

@@ -5,192 +5,302 @@
 #include "arith.h"
 #include "attention.h"
 #include "automorph.h"
+#include "ntt_core.h"
 
 namespace ckks {
 
 namespace {
 
+using nttc::at_u32;
+
 struct SumIPArgs {
-  const uint64_t* E;  // item b: E + b*E_bstride, [beta][next][N] raised digits
-  const uint64_t* T;  // item b: T + b*T_bstride, c1 [nq][N] (limbs inside their own digit)
-  uint64_t* acc;      // item b: acc + b*acc_bstride, [2][next][N]
-  uint64_t E_bstride, T_bstride, acc_bstride;
+  const uint64_t* E;   // item b: E + b*E_bstride, [beta][next][N] raised digits
+  const uint64_t* ct;  // item b: ct + b*ct_bstride, [2][nq][N]: the stage's input
+  uint64_t* acc;       // item b: acc + b*acc_bstride, [2][next][N]
+  uint64_t E_bstride, ct_bstride, acc_bstride;
   const uint64_t* evk[kMaxSumRot];
   uint32_t g[kMaxSumRot];
   const PrimeConst* prime;
-  int log_n, level, next, beta, alpha, L, K, n_rot;
+  const uint64_t* pmod;  // [L][2]: {[P]_{q_i}, Shoup}
+  int log_n, level, next, beta, alpha, L, K, n_rot, n_items;
 };
 
-// acc_b[t][w] = sum_r sum_j D_j[t][pi_{g_r}(w)] * evk_{r,j}.b[t][w] (and acc_a).
+// Sums of products of two words below 2^(2 SH), split into SH-bit halves, in
+// three columns (weights 1, 2^SH, 2^2SH).  SH = 27 takes words below 2^54 and
+// 256 products between folds, SH = 30 words below 2^60 and 8: column 1 gets
+// two products a term, 2 * 256 * 2^54 = 2^63 and 2 * 8 * (2^30 - 1)^2 + 2^30 <
+// 2^64.  A fold carries columns 0 and 1 upwards and reduces column 2 modulo q,
+// which leaves it below q.
+template <int SH>
+struct Cols {
+  uint64_t a0, a1, a2;
+};
+template <int SH>
+constexpr int kFoldTerms = SH == 27 ? 256 : 8;
+template <int SH>
+__device__ __forceinline__ uint32_t low_half(uint64_t v) {
+  return (uint32_t)v & ((1u << SH) - 1);
+}
+template <int SH>
+__device__ __forceinline__ void cols_mac(Cols<SH>& A, uint32_t xl, uint32_t xh, uint32_t kl, uint32_t kh) {
+  A.a0 = mad64(xl, kl, A.a0);
+  A.a1 = mad64(xl, kh, A.a1);
+  A.a1 = mad64(xh, kl, A.a1);
+  A.a2 = mad64(xh, kh, A.a2);
+}
+template <int SH>
+__device__ __forceinline__ void cols_fold(Cols<SH>& A, uint64_t q, uint64_t inv1) {
+  constexpr uint64_t M = (1ull << SH) - 1;
+  A.a1 += A.a0 >> SH;
+  A.a0 &= M;
+  A.a2 = reduce64(A.a2 + (A.a1 >> SH), q, inv1);
+  A.a1 &= M;
+}
+template <int SH>
+__device__ __forceinline__ uint64_t cols_reduce(const Cols<SH>& A, uint64_t q, uint64_t r64, uint64_t r64p,
+                                                uint64_t inv1) {
+  U128 r;
+  uint64_t t = A.a1 << SH;
+  const uint64_t lo = A.a0 + t;
+  r.hi = (A.a1 >> (64 - SH)) + (lo < t ? 1 : 0);
+  t = A.a2 << (2 * SH);
+  r.lo = lo + t;
+  r.hi += (A.a2 >> (64 - 2 * SH)) + (r.lo < t ? 1 : 0);
+  return reduce128_lazy(r, q, r64, r64p, inv1);
+}
+
+// One (digit, rotation) of the inner product: a key word pair per component
+// and every item's digit words, in flight while the previous one is computed.
+template <int I>
+struct SumTerm {
+  ulonglong2 kb, ka, x[I];
+  bool swap;
+};
+
+// acc[t] = sum_j sum_r tau_{g_r}(D_j)[t] evk_{r,j}[t] for two adjacent words of
+// I items; on ciphertext limbs component 0 also gets P sum_r tau_{g_r}(c0),
+// which ModDown turns into the stage's sum of rotated c0 (P is 0 modulo the
+// special primes, so they are not touched).
+//
+// Each thread holds both words of I items: a key word is loaded once for all
+// of them (the keys are the kernel's HBM traffic: 2 beta limbs per target limb
+// and rotation).  tau_g maps an aligned pair of words of the bit-reversed
+// order onto an aligned pair, perhaps swapped, so a gather is one 16-byte load.
+// Digits are the outer loop: the I limbs of one digit (I * 512 KB at N = 2^16)
+// stay in an XCD's L2 while the rotations gather from them.
+template <int I, int SH>
+__device__ __forceinline__ void sum_ip_narrow(const SumIPArgs& a, const PrimeConst& pc, int t, int keyl, int item0,
+                                              uint32_t w0) {
+  const int log_n = a.log_n;
+  const uint64_t q = pc.q, inv1 = pc.inv1;
+  const uint64_t LKN = (uint64_t)(a.L + a.K) << log_n;
+  const uint64_t koff = (uint64_t)keyl << log_n;
+  int it[I];
+#pragma unroll
+  for (int i = 0; i < I; ++i) it[i] = min(item0 + i, a.n_items - 1);
+  auto load = [&](int j, int r, SumTerm<I>& s) {
+    const uint32_t src = automorph_src(w0, a.g[r], log_n);
+    s.swap = src & 1;
+    const uint64_t* kb = a.evk[r] + (uint64_t)(2 * j) * LKN + koff;
+    s.kb = at_u32(reinterpret_cast<const ulonglong2*>(kb), w0 >> 1);
+    s.ka = at_u32(reinterpret_cast<const ulonglong2*>(kb + LKN), w0 >> 1);
+    const bool own = t >= j * a.alpha && t < (j + 1) * a.alpha && t <= a.level;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const uint64_t* d = own ? a.ct + it[i] * a.ct_bstride + ((uint64_t)(a.level + 1 + t) << log_n)
+                              : a.E + it[i] * a.E_bstride + ((uint64_t)(j * a.next + t) << log_n);
+      s.x[i] = at_u32(reinterpret_cast<const ulonglong2*>(d), src >> 1);
+    }
+  };
+  Cols<SH> A[I][2][2];  // item, component, word
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) A[i][e >> 1][e & 1] = Cols<SH>{0, 0, 0};
+  const int terms = a.beta * a.n_rot;
+  int since = 0, j = 0, r = 0;
+  SumTerm<I> cur;
+  load(0, 0, cur);
+  for (int n = 0; n < terms; ++n) {
+    if (++r == a.n_rot) {
+      r = 0;
+      ++j;
+    }
+    SumTerm<I> next = cur;
+    if (n + 1 < terms) load(j, r, next);
+    const uint32_t bl0 = low_half<SH>(cur.kb.x), bh0 = (uint32_t)(cur.kb.x >> SH);
+    const uint32_t bl1 = low_half<SH>(cur.kb.y), bh1 = (uint32_t)(cur.kb.y >> SH);
+    const uint32_t al0 = low_half<SH>(cur.ka.x), ah0 = (uint32_t)(cur.ka.x >> SH);
+    const uint32_t al1 = low_half<SH>(cur.ka.y), ah1 = (uint32_t)(cur.ka.y >> SH);
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const uint64_t x0 = cur.swap ? cur.x[i].y : cur.x[i].x, x1 = cur.swap ? cur.x[i].x : cur.x[i].y;
+      const uint32_t l0 = low_half<SH>(x0), h0 = (uint32_t)(x0 >> SH);
+      const uint32_t l1 = low_half<SH>(x1), h1 = (uint32_t)(x1 >> SH);
+      cols_mac<SH>(A[i][0][0], l0, h0, bl0, bh0);
+      cols_mac<SH>(A[i][0][1], l1, h1, bl1, bh1);
+      cols_mac<SH>(A[i][1][0], l0, h0, al0, ah0);
+      cols_mac<SH>(A[i][1][1], l1, h1, al1, ah1);
+    }
+    if (++since == kFoldTerms<SH>) {
+      since = 0;
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cols_fold<SH>(A[i][e >> 1][e & 1], q, inv1);
+    }
+    cur = next;
+  }
+  uint64_t s0[I], s1[I];
+#pragma unroll
+  for (int i = 0; i < I; ++i) s0[i] = s1[i] = 0;
+  if (t <= a.level) {
+    for (int k = 0; k < a.n_rot; ++k) {
+      const uint32_t src = automorph_src(w0, a.g[k], log_n);
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const ulonglong2 v = at_u32(
+            reinterpret_cast<const ulonglong2*>(a.ct + it[i] * a.ct_bstride + ((uint64_t)t << log_n)), src >> 1);
+        s0[i] = add_mod(s0[i], src & 1 ? v.y : v.x, q);
+        s1[i] = add_mod(s1[i], src & 1 ? v.x : v.y, q);
+      }
+    }
+    const uint64_t pw = a.pmod[2 * t], pwp = a.pmod[2 * t + 1];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      s0[i] = reduce_4q(mul_shoup_lazy(s0[i], pw, pwp, q), q);
+      s1[i] = reduce_4q(mul_shoup_lazy(s1[i], pw, pwp, q), q);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    if (item0 + i >= a.n_items) break;
+    uint64_t* ob = a.acc + (item0 + i) * a.acc_bstride + ((uint64_t)t << log_n);
+    uint64_t* oa = ob + ((uint64_t)a.next << log_n);
+    ulonglong2 vb, va;
+    vb.x = add_mod(cols_reduce<SH>(A[i][0][0], q, pc.r64, pc.r64p, inv1), s0[i], q);
+    vb.y = add_mod(cols_reduce<SH>(A[i][0][1], q, pc.r64, pc.r64p, inv1), s1[i], q);
+    va.x = cols_reduce<SH>(A[i][1][0], q, pc.r64, pc.r64p, inv1);
+    va.y = cols_reduce<SH>(A[i][1][1], q, pc.r64, pc.r64p, inv1);
+    at_u32(reinterpret_cast<ulonglong2*>(ob), w0 >> 1) = vb;
+    at_u32(reinterpret_cast<ulonglong2*>(oa), w0 >> 1) = va;
+  }
+}
+
+// Primes below 2^60.  The grid is (tiles of 512 words, target limbs, groups of
+// I items), groups fastest: the groups of one tile run together on one XCD
+// and share its key words in L2.
+template <int I>
 __global__ __launch_bounds__(256) void sum_ip_kernel(SumIPArgs a) {
-  constexpr int W = 4;  // consecutive output words per thread
+  const nttc::GridPos gp = nttc::row_grid_pos<true>();
+  const int t = gp.job;
+  const int keyl = t <= a.level ? t : a.L + (t - a.level - 1);
+  const PrimeConst& pc = a.prime[keyl];
+  const uint32_t w0 = (gp.tile * 256 + threadIdx.x) * 2;
+  if (pc.q < (1ull << 54))
+    sum_ip_narrow<I, 27>(a, pc, t, keyl, gp.item * I, w0);
+  else
+    sum_ip_narrow<I, 30>(a, pc, t, keyl, gp.item * I, w0);
+}
+
+// Primes up to 2^62: lazy Montgomery products as in the key switch, one item.
+__global__ __launch_bounds__(256) void sum_ip_wide_kernel(SumIPArgs a) {
   const int t = blockIdx.y, item = blockIdx.z;
   const int keyl = t <= a.level ? t : a.L + (t - a.level - 1);
   const PrimeConst& pc = a.prime[keyl];
   const uint64_t q = pc.q, mp = pc.mprime;
   const int log_n = a.log_n;
-  const uint32_t w0 = (blockIdx.x * blockDim.x + threadIdx.x) * W;
+  const uint32_t w = blockIdx.x * blockDim.x + threadIdx.x;
   const uint64_t LKN = (uint64_t)(a.L + a.K) << log_n;
-  uint64_t accb[W], acca[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) accb[i] = acca[i] = 0;
+  const uint64_t* c0 = a.ct + item * a.ct_bstride + ((uint64_t)t << log_n);
+  uint64_t b = 0, c = 0, rot = 0;
   const int fold = mont_fold(q);
   int since = 0;
   for (int r = 0; r < a.n_rot; ++r) {
-    uint32_t src[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) src[i] = automorph_src(w0 + i, a.g[r], log_n);
-    const uint64_t* evk = a.evk[r] + ((uint64_t)keyl << log_n) + w0;
+    const uint32_t src = automorph_src(w, a.g[r], log_n);
+    const uint64_t* evk = a.evk[r] + ((uint64_t)keyl << log_n) + w;
     for (int j = 0; j < a.beta; ++j) {
-      const bool in_digit = t >= j * a.alpha && t < (j + 1) * a.alpha && t <= a.level;
-      const uint64_t* d = in_digit ? a.T + item * a.T_bstride + ((uint64_t)t << log_n)
-                                   : a.E + item * a.E_bstride + ((uint64_t)(j * a.next + t) << log_n);
-      const uint64_t* kb = evk + (uint64_t)(2 * j) * LKN;
-      const uint64_t* ka = evk + (uint64_t)(2 * j + 1) * LKN;
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const uint64_t x = d[src[i]];
-        accb[i] += mont_mul_lazy(x, kb[i], q, mp);
-        acca[i] += mont_mul_lazy(x, ka[i], q, mp);
-      }
+      const bool own = t >= j * a.alpha && t < (j + 1) * a.alpha && t <= a.level;
+      const uint64_t x = own ? c0[((uint64_t)(a.level + 1) << log_n) + src]
+                             : a.E[item * a.E_bstride + ((uint64_t)(j * a.next + t) << log_n) + src];
+      b += mont_mul_lazy(x, evk[(uint64_t)(2 * j) * LKN], q, mp);
+      c += mont_mul_lazy(x, evk[(uint64_t)(2 * j + 1) * LKN], q, mp);
       if (++since == fold) {  // mont_fold(m) products since the last reduction
         since = 0;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          accb[i] = reduce64(accb[i], q, pc.inv1);
-          acca[i] = reduce64(acca[i], q, pc.inv1);
-        }
+        b = reduce64(b, q, pc.inv1);
+        c = reduce64(c, q, pc.inv1);
       }
     }
+    if (t <= a.level) rot = add_mod(rot, c0[src], q);
   }
-  uint64_t* ob = a.acc + item * a.acc_bstride + ((uint64_t)t << log_n) + w0;
-  uint64_t* oa = ob + ((uint64_t)a.next << log_n);
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    ob[i] = reduce_4q(mul_shoup_lazy(accb[i], pc.r64, pc.r64p, q), q);
-    oa[i] = reduce_4q(mul_shoup_lazy(acca[i], pc.r64, pc.r64p, q), q);
-  }
+  b = reduce_4q(mul_shoup_lazy(b, pc.r64, pc.r64p, q), q);
+  if (t <= a.level) b = add_mod(b, reduce_4q(mul_shoup_lazy(rot, a.pmod[2 * t], a.pmod[2 * t + 1], q), q), q);
+  uint64_t* o = a.acc + item * a.acc_bstride + ((uint64_t)t << log_n) + w;
+  o[0] = b;
+  o[(uint64_t)a.next << log_n] = reduce_4q(mul_shoup_lazy(c, pc.r64, pc.r64p, q), q);
 }
 
-struct SumCombineArgs {
-  const uint64_t* acc;  // [2][next][N] per item
-  const uint64_t* w;    // [2][nq][N] per item: NTT of the ModDown conversion
-  const uint64_t* ct;   // [2][nq][N] per item: the stage's input
-  uint64_t acc_bstride, w_bstride, ct_bstride;
-  uint64_t* out[kSumItems];  // [2][nq][N]
-  const uint64_t* pinv;  // [L][2]
-  const PrimeConst* prime;
-  uint32_t g[kMaxSumRot];
-  int log_n, nq, next, n_rot;
-};
+// Items a thread of the inner product holds: as many as the launch has, up to
+// 4 (24 accumulator registers an item; 4 leave three waves a SIMD).
+constexpr int kSumHeld = 4;
 
-// out_c = acc_c P^-1 - w_c + ct_c (+ sum_r tau_{g_r}(ct_0) for c = 0)
-__global__ __launch_bounds__(256) void sum_combine_kernel(SumCombineArgs a) {
-  const uint32_t j = blockIdx.x * blockDim.x + threadIdx.x;
-  const int comp = blockIdx.y / a.nq, i = blockIdx.y % a.nq, item = blockIdx.z;
-  const uint64_t q = a.prime[i].q;
-  const uint64_t* ct = a.ct + item * a.ct_bstride + ((uint64_t)blockIdx.y << a.log_n);
-  const uint64_t v = a.acc[item * a.acc_bstride + ((uint64_t)(comp * a.next + i) << a.log_n) + j];
-  const uint64_t w = a.w[item * a.w_bstride + ((uint64_t)blockIdx.y << a.log_n) + j];
-  uint64_t r = sub_mod(reduce_4q(mul_shoup_lazy(v, a.pinv[2 * i], a.pinv[2 * i + 1], q), q), w, q);
-  r = add_mod(r, ct[j], q);
-  if (comp == 0)
-    for (int k = 0; k < a.n_rot; ++k) r = add_mod(r, ct[automorph_src(j, a.g[k], a.log_n)], q);
-  a.out[item][((uint64_t)blockIdx.y << a.log_n) + j] = r;
+int launch_sum_ip(Ctx* c, hipStream_t s, const SumIPArgs& a) {
+  TraceScope ts(c, s, "sum_ip", (double)a.n_items * a.next * c->N * (2.0 * a.beta * a.n_rot + 2));
+  if (c->wide) {
+    hipLaunchKernelGGL(sum_ip_wide_kernel, dim3(c->N / 256, a.next, a.n_items), dim3(256), 0, s, a);
+  } else {
+    const int groups = (a.n_items + kSumHeld - 1) / kSumHeld, held = (a.n_items + groups - 1) / groups;
+    auto fn = held == 1 ? sum_ip_kernel<1> : held == 2 ? sum_ip_kernel<2> : held == 3 ? sum_ip_kernel<3>
+                                                                                      : sum_ip_kernel<4>;
+    hipLaunchKernelGGL(fn, dim3(c->N / 512, a.next, (a.n_items + held - 1) / held), dim3(256), 0, s, a);
+  }
+  CKKS_HIP_CHECK(hipGetLastError());
+  return CKKS_OK;
 }
 
 // Words per item: decomposition, accumulators, ModDown conversion.
 size_t stage_words(const Ctx* c, int level) { return ks_dec_words(c, level) + ks_back_words(c, level); }
 
-// One stage on n items (n <= kSumItems).
-int sum_stage(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* const* out, int n, int level,
-              int n_rot, const uint32_t* g, const uint64_t* const* evk, uint64_t* ws) {
+// One stage on n items (n <= kSumItems): decomposition, inner product, and
+// the ModDown of a key switch, whose last pass adds the stage's input.
+int sum_stage(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride, int n,
+              int level, int n_rot, const uint32_t* g, const uint64_t* const* evk, uint64_t* ws) {
   const uint32_t N = c->N;
-  const int nq = level + 1, next = nq + (int)c->K, K = (int)c->K;
+  const int nq = level + 1, next = nq + (int)c->K;
   const uint64_t dec_per = ks_dec_words(c, level), per = ks_back_words(c, level);
   uint64_t* dec = ws;
   uint64_t* A = ws + dec_per * n;
-  uint64_t* W = A + 2ull * next * N;
-  const uint64_t* c1 = in + (uint64_t)nq * N;
-  int rc = ks_decompose(c, s, level, n, c1, in_stride, dec, dec_per);
+  int rc = ks_decompose(c, s, level, n, in + (uint64_t)nq * N, in_stride, dec, dec_per);
   if (rc) return rc;
-  {
-    SumIPArgs a;
-    memset(&a, 0, sizeof(a));
-    a.E = dec + (uint64_t)nq * N;
-    a.E_bstride = dec_per;
-    a.T = c1;
-    a.T_bstride = in_stride;
-    a.acc = A;
-    a.acc_bstride = per;
-    for (int r = 0; r < n_rot; ++r) {
-      a.evk[r] = evk[r];
-      a.g[r] = g[r];
-    }
-    a.prime = c->d_prime;
-    a.log_n = (int)c->log_n;
-    a.level = level;
-    a.next = next;
-    a.beta = c->beta(level);
-    a.alpha = (int)c->alpha;
-    a.L = (int)c->L;
-    a.K = K;
-    a.n_rot = n_rot;
-    TraceScope ts(c, s, "sum_ip", (double)n * next * N * (2.0 * a.beta * n_rot + 2));
-    hipLaunchKernelGGL(sum_ip_kernel, dim3(N / 1024, next, n), dim3(256), 0, s, a);
-    CKKS_HIP_CHECK(hipGetLastError());
-  }
-  {
-    NttJobs jobs;
-    uint32_t off[kMaxJobs];
-    for (int comp = 0; comp < 2; ++comp)
-      for (int k = 0; k < K; ++k) {
-        off[jobs.n] = (uint32_t)(c->md.phinv + 2 * k);
-        jobs.add(comp * next + nq + k, comp * next + nq + k, (int)c->L + k);
-      }
-    if ((rc = ntt_run_scaled(c, s, A, A, per, per, n, jobs, true, 2, c->d_moddown, off))) return rc;
-  }
-  {
-    ModDownArgs md;
-    memset(&md, 0, sizeof(md));
-    md.acc = A;
-    md.w = W;
-    md.acc_bstride = per;
-    md.w_bstride = per;
-    md.conv = c->d_moddown + c->md.conv;
-    md.prime = c->d_prime;
-    md.n = N;
-    md.level = level;
-    md.acc_comp_limbs = next;
-    md.acc_k0 = nq;
-    md.L = (int)c->L;
-    md.K = K;
-    if ((rc = launch_moddown_conv(c, s, md, n))) return rc;
-    NttJobs jobs;
-    for (int i = 0; i < 2 * nq; ++i) jobs.add(i, i, i % nq);
-    if ((rc = ntt_pass_only(c, s, W, W, per, per, n, jobs, false, true, 0, nullptr, nullptr))) return rc;
-    if ((rc = ntt_pass_only(c, s, W, W, per, per, n, jobs, false, false, 0, nullptr, nullptr))) return rc;
-  }
-  SumCombineArgs a;
+  SumIPArgs a;
   memset(&a, 0, sizeof(a));
-  a.acc = A;
-  a.w = W;
+  a.E = dec + (uint64_t)nq * N;
+  a.E_bstride = dec_per;
   a.ct = in;
-  a.acc_bstride = per;
-  a.w_bstride = per;
   a.ct_bstride = in_stride;
-  for (int b = 0; b < n; ++b) a.out[b] = out[b];
-  a.pinv = c->d_moddown + c->md.pinv;
+  a.acc = A;
+  a.acc_bstride = per;
+  for (int r = 0; r < n_rot; ++r) {
+    a.evk[r] = evk[r];
+    a.g[r] = g[r];
+  }
   a.prime = c->d_prime;
-  for (int r = 0; r < n_rot; ++r) a.g[r] = g[r];
+  a.pmod = c->d_moddown + c->md.pmod;
   a.log_n = (int)c->log_n;
-  a.nq = nq;
+  a.level = level;
   a.next = next;
+  a.beta = c->beta(level);
+  a.alpha = (int)c->alpha;
+  a.L = (int)c->L;
+  a.K = (int)c->K;
   a.n_rot = n_rot;
-  TraceScope ts(c, s, "sum_combine", (double)n * 2 * nq * N);
-  hipLaunchKernelGGL(sum_combine_kernel, dim3(N / 256, 2 * nq, n), dim3(256), 0, s, a);
-  CKKS_HIP_CHECK(hipGetLastError());
-  return CKKS_OK;
+  a.n_items = n;
+  if ((rc = launch_sum_ip(c, s, a))) return rc;
+  KSItem it[kSumItems];
+  memset(it, 0, sizeof(it));
+  it[0].accum = in;
+  it[0].out = out;
+  return ks_back(c, s, level, n, it, A, A + 2ull * next * N, per, 0, in_stride, out_stride, nq);
 }
 
 }  // namespace
@@ -201,8 +311,8 @@ size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage) {
   return n * (stage_words(c, level) + (n_stage > 1 ? 2 * ct : 0));
 }
 
-int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* const* out, int batch,
-               int level, const ckks_sum_steps& st, uint64_t* ws) {
+int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
+               int batch, int level, const ckks_sum_steps& st, uint64_t* ws) {
   const uint64_t ct = 2ull * (level + 1) * c->N;
   for (int b0 = 0; b0 < batch; b0 += kSumItems) {
     const int n = batch - b0 < kSumItems ? batch - b0 : kSumItems;
@@ -212,9 +322,9 @@ int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, ui
     uint64_t src_stride = in_stride;
     int at = 0;
     for (int k = 0; k < st.n_stage; ++k) {
-      uint64_t* dst[kSumItems];
-      for (int b = 0; b < n; ++b) dst[b] = k == st.n_stage - 1 ? out[b0 + b] : half[k & 1] + b * ct;
-      int rc = sum_stage(c, s, src, src_stride, dst, n, level, st.radix[k] - 1, st.galois_elts + at, st.d_evks + at, ws);
+      const bool last = k == st.n_stage - 1;
+      int rc = sum_stage(c, s, src, src_stride, last ? out + b0 * out_stride : half[k & 1], last ? out_stride : ct, n,
+                         level, st.radix[k] - 1, st.galois_elts + at, st.d_evks + at, ws);
       if (rc) return rc;
       at += st.radix[k] - 1;
       src = half[k & 1];
