@@ -6,7 +6,6 @@
 namespace ckks {
 
 constexpr int kMaxSumRot = CKKS_SUM_MAX_RADIX - 1;  // rotations of one stage
-constexpr int kSumItems = 8;                        // items of one launch of a stage
 
 // Words of workspace sum_stages needs for `batch` items at `level`.
 size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage);

@@ -2,6 +2,8 @@
 // and one ModDown per stage (see ckks_sum_steps in include/ckks.h).
 #include <string.h>
 
+#include <algorithm>
+
 #include "arith.h"
 #include "attention.h"
 #include "automorph.h"
@@ -30,7 +32,8 @@ struct SumIPArgs {
 // 256 products between folds, SH = 30 words below 2^60 and 8: column 1 gets
 // two products a term, 2 * 256 * 2^54 = 2^63 and 2 * 8 * (2^30 - 1)^2 + 2^30 <
 // 2^64.  A fold carries columns 0 and 1 upwards and reduces column 2 modulo q,
-// which leaves it below q.
+// which leaves it below 2.5 q (reduce_hi; primes that split at 30 bits are
+// above 2^54) or below q.
 template <int SH>
 struct Cols {
   uint64_t a0, a1, a2;
@@ -53,9 +56,11 @@ __device__ __forceinline__ void cols_fold(Cols<SH>& A, uint64_t q, uint64_t inv1
   constexpr uint64_t M = (1ull << SH) - 1;
   A.a1 += A.a0 >> SH;
   A.a0 &= M;
-  A.a2 = reduce64(A.a2 + (A.a1 >> SH), q, inv1);
+  const uint64_t v = A.a2 + (A.a1 >> SH);
+  A.a2 = SH == 30 ? reduce_hi(v, q, (uint32_t)inv1) : reduce64(v, q, inv1);
   A.a1 &= M;
 }
+// The sum modulo q, congruent, in [0, 6q).
 template <int SH>
 __device__ __forceinline__ uint64_t cols_reduce(const Cols<SH>& A, uint64_t q, uint64_t r64, uint64_t r64p,
                                                 uint64_t inv1) {
@@ -66,7 +71,7 @@ __device__ __forceinline__ uint64_t cols_reduce(const Cols<SH>& A, uint64_t q, u
   t = A.a2 << (2 * SH);
   r.lo = lo + t;
   r.hi += (A.a2 >> (64 - 2 * SH)) + (r.lo < t ? 1 : 0);
-  return reduce128_lazy(r, q, r64, r64p, inv1);
+  return reduce128_6q(r, q, r64, r64p, inv1);
 }
 
 // One (digit, rotation) of the inner product: a key word pair per component
@@ -151,39 +156,46 @@ __device__ __forceinline__ void sum_ip_narrow(const SumIPArgs& a, const PrimeCon
     }
     cur = next;
   }
+  // Ciphertext limbs leave the kernel congruent, below 10 q < 2^64: the last
+  // pass multiplies them by P^-1 with a product that takes any 64-bit word.
+  // Special limbs go to inverse butterflies, which take words below 4q.
   uint64_t s0[I], s1[I];
 #pragma unroll
   for (int i = 0; i < I; ++i) s0[i] = s1[i] = 0;
-  if (t <= a.level) {
+  const bool low = t <= a.level;
+  if (low) {
     for (int k = 0; k < a.n_rot; ++k) {
       const uint32_t src = automorph_src(w0, a.g[k], log_n);
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         const ulonglong2 v = at_u32(
             reinterpret_cast<const ulonglong2*>(a.ct + it[i] * a.ct_bstride + ((uint64_t)t << log_n)), src >> 1);
-        s0[i] = add_mod(s0[i], src & 1 ? v.y : v.x, q);
-        s1[i] = add_mod(s1[i], src & 1 ? v.x : v.y, q);
+        const uint64_t x0 = src & 1 ? v.y : v.x, x1 = src & 1 ? v.x : v.y;
+        s0[i] = SH == 27 ? s0[i] + x0 : add_mod(s0[i], x0, q);  // at most 31 words below 2^54
+        s1[i] = SH == 27 ? s1[i] + x1 : add_mod(s1[i], x1, q);
       }
     }
     const uint64_t pw = a.pmod[2 * t], pwp = a.pmod[2 * t + 1];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      s0[i] = reduce_4q(mul_shoup_lazy(s0[i], pw, pwp, q), q);
-      s1[i] = reduce_4q(mul_shoup_lazy(s1[i], pw, pwp, q), q);
+      s0[i] = mul_shoup_lazy(s0[i], pw, pwp, q);  // [0, 4q)
+      s1[i] = mul_shoup_lazy(s1[i], pw, pwp, q);
     }
   }
+  const uint64_t cut = low ? ~0ull : 4 * q;
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     if (item0 + i >= a.n_items) break;
     uint64_t* ob = a.acc + (item0 + i) * a.acc_bstride + ((uint64_t)t << log_n);
     uint64_t* oa = ob + ((uint64_t)a.next << log_n);
-    ulonglong2 vb, va;
-    vb.x = add_mod(cols_reduce<SH>(A[i][0][0], q, pc.r64, pc.r64p, inv1), s0[i], q);
-    vb.y = add_mod(cols_reduce<SH>(A[i][0][1], q, pc.r64, pc.r64p, inv1), s1[i], q);
-    va.x = cols_reduce<SH>(A[i][1][0], q, pc.r64, pc.r64p, inv1);
-    va.y = cols_reduce<SH>(A[i][1][1], q, pc.r64, pc.r64p, inv1);
-    at_u32(reinterpret_cast<ulonglong2*>(ob), w0 >> 1) = vb;
-    at_u32(reinterpret_cast<ulonglong2*>(oa), w0 >> 1) = va;
+    uint64_t v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = cols_reduce<SH>(A[i][e >> 1][e & 1], q, pc.r64, pc.r64p, inv1);
+      if (v[e] >= cut) v[e] -= 4 * q;
+    }
+    at_u32(reinterpret_cast<ulonglong2*>(ob), w0 >> 1) = make_ulonglong2(v[0] + s0[i], v[1] + s1[i]);
+    at_u32(reinterpret_cast<ulonglong2*>(oa), w0 >> 1) = make_ulonglong2(v[2], v[3]);
   }
 }
 
@@ -261,7 +273,7 @@ int launch_sum_ip(Ctx* c, hipStream_t s, const SumIPArgs& a) {
 // Words per item: decomposition, accumulators, ModDown conversion.
 size_t stage_words(const Ctx* c, int level) { return ks_dec_words(c, level) + ks_back_words(c, level); }
 
-// One stage on n items (n <= kSumItems): decomposition, inner product, and
+// One stage on n items (n <= kMaxChunk): decomposition, inner product, and
 // the ModDown of a key switch, whose last pass adds the stage's input.
 int sum_stage(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride, int n,
               int level, int n_rot, const uint32_t* g, const uint64_t* const* evk, uint64_t* ws) {
@@ -296,7 +308,7 @@ int sum_stage(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uin
   a.n_rot = n_rot;
   a.n_items = n;
   if ((rc = launch_sum_ip(c, s, a))) return rc;
-  KSItem it[kSumItems];
+  KSItem it[kMaxChunk];
   memset(it, 0, sizeof(it));
   it[0].accum = in;
   it[0].out = out;
@@ -305,17 +317,30 @@ int sum_stage(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uin
 
 }  // namespace
 
+// Words of a group of items that goes through the stages together, with the
+// two buffers between stages.
+static size_t group_words(const Ctx* c, int level, int n, int n_stage) {
+  return n * (stage_words(c, level) + (n_stage > 1 ? 4 * (size_t)(level + 1) * c->N : 0));
+}
+
+// Items of a group: the launches' limit, or what 2 GiB hold (17 at N = 2^16
+// and 24 + 8 limbs).  Large groups share each key word among more items; two
+// half groups on two streams measured 0-14 % slower (keys are read twice).
+static int sum_group(const Ctx* c, int level, int batch, int n_stage) {
+  const size_t fit = (1ull << 28) / group_words(c, level, 1, n_stage);
+  return (int)std::max<size_t>(1, std::min<size_t>({fit, (size_t)kMaxChunk, (size_t)batch}));
+}
+
 size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage) {
-  const size_t n = (size_t)(batch < kSumItems ? batch : kSumItems);
-  const size_t ct = 2 * (size_t)(level + 1) * c->N;
-  return n * (stage_words(c, level) + (n_stage > 1 ? 2 * ct : 0));
+  return group_words(c, level, sum_group(c, level, batch, n_stage), n_stage);
 }
 
 int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
                int batch, int level, const ckks_sum_steps& st, uint64_t* ws) {
   const uint64_t ct = 2ull * (level + 1) * c->N;
-  for (int b0 = 0; b0 < batch; b0 += kSumItems) {
-    const int n = batch - b0 < kSumItems ? batch - b0 : kSumItems;
+  const int group = sum_group(c, level, batch, st.n_stage);
+  for (int b0 = 0; b0 < batch; b0 += group) {
+    const int n = std::min(group, batch - b0);
     // the stages between the first and the last alternate between two buffers
     uint64_t* half[2] = {ws + n * stage_words(c, level), ws + n * (stage_words(c, level) + ct)};
     const uint64_t* src = in + b0 * in_stride;
