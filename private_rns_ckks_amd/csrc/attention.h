@@ -15,52 +15,71 @@ size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage);
 int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
                int batch, int level, const ckks_sum_steps& st, uint64_t* ws);
 
-// out[b] = p[(first + b) % n_row] * in[b] on both components, limbs 0..nl-1.
+// out[b] = p[row] * in[b] on both components, limbs 0..nl-1; b = t * ng +
+// g reads in + (t * n_grp + g)*in_bstride and
+// row t * n_row + (g0 + g) % n_row.
 struct PlainMulArgs {
-  const uint64_t* in;  // item b at + b*in_bstride, component stride in_comp
+  const uint64_t* in;  // component stride in_comp
   const uint64_t* p;   // [..][nl][N]
   uint64_t* out;       // item b at + b*out_bstride, [2][nl][N]
   uint64_t in_bstride, in_comp, out_bstride;
   const PrimeConst* prime;
-  int log_n, nl, n_row, first;
+  int log_n, nl, ng, n_grp, n_row, g0;
 };
 int launch_plain_mul(Ctx* c, hipStream_t s, const PlainMulArgs& a, int batch);
 
-// Tensor products of paired ciphertexts: out[b] = a[b] x b[b] at limbs
-// 0..nl-1, item b of `a` at a + ia(b)*a_bstride with ia(b) = b / n_k and of
-// `b` at (b / n_qk) * n_k + b % n_k (pairs [group][i][j]); with n_qk = 0 both
-// are item b.  decay (optional): parts 0 and 1 get decay[row] * state[b] added,
-// row = b % n_row (state [2][nl][N] per item, b_bstride apart).
+// What the products below do to their output for ks_rescale: parts 0 and 1 of
+// the limbs that stay after `drop` rescales are multiplied by the inverses of
+// the dropped primes and get `add` added (item's words [2][nl - drop][N], or
+// NULL).  rescale: the context's table.
+struct DropOut {
+  const uint64_t* rescale;
+  int L, drop;
+};
+
+// Tensor products of paired ciphertexts at limbs 0..nl-1: out[b] = a[ia] x
+// b[ib] for p = first + b.  With n_k > 0 the pairs are [group][i][j] (n_qk of
+// them a group): ia = p / n_k, ib = (p / n_qk) * n_k + p % n_k.  Otherwise ia
+// = p and ib = (p / ng) * n_grp + p % ng.  decay (optional): parts 0 and 1 get
+// decay[p % n_row] * state[p] added ([2][nl][N], state_bstride apart).
 struct PairArgs {
   const uint64_t *a, *b;
   uint64_t* out;  // [3][nl][N] per item
-  uint64_t a_bstride, a_comp, b_bstride, b_comp, out_bstride;
+  uint64_t a_bstride, a_comp, b_bstride, b_comp;
   const uint64_t *decay, *state;
   uint64_t state_bstride;
+  DropOut drop;
+  const uint64_t* add;  // item p's at + p*add_bstride
+  uint64_t add_bstride;
   const PrimeConst* prime;
-  int log_n, nl, n_k, n_qk, n_row, first;  // first: index of item 0 in the pair order
+  int log_n, nl, n_k, n_qk, ng, n_grp, n_row, first;
 };
 int launch_pair(Ctx* c, hipStream_t s, const PairArgs& a, int batch);
 
-// Weighted prefix sums over tokens of one block: out[t][g] = init[g] +
-// sum_{u <= t} w[u][g % n_row] * (k[u][g] x v[u][g]), three parts; k, v at
-// token stride tok_stride; init may be NULL (zero).
+// Weighted prefix sums over tokens of one block: X[t][g] = init[g] +
+// sum_{u <= t} w[u][(g0 + g) % n_row] * (k[u][g] x v[u][g]), three parts; k, v
+// at token stride tok_stride; init may be NULL (zero).  last (optional)
+// receives the last token's sums.
 struct ScanArgs {
   const uint64_t *k, *v, *w;
   const uint64_t* init;  // [n_grp][3][nl][N]
-  uint64_t* out;         // [n_tok][n_grp][3][nl][N]
+  uint64_t* out;         // [n_tok][n_grp][3][nl][N], as DropOut says
+  uint64_t* last;        // [n_grp][3][nl][N], may be init
   uint64_t tok_stride;
+  DropOut drop;
+  const uint64_t* add;   // group g's at + g * 2 * (nl - drop) * N
   const PrimeConst* prime;
-  int log_n, nl, n_tok, n_grp, n_row, g0;  // g0: the block's first group (its row offset)
+  int log_n, nl, n_tok, n_grp, n_row, g0;
 };
 int launch_scan(Ctx* c, hipStream_t s, const ScanArgs& a);
 
 // Masked weighted sums: for row b = (g, i), num[b] = sum_j m[g % n_row][j] *
-// (a[b][j] x v[g][j]) (three parts) and, when den is given, den[b] = sum_j
-// m[g % n_row][j] * a[b][j]; m NULL: no mask.
+// (a[b][j] x v[g][j]) (three parts, as DropOut says) and, when den is given,
+// den[b] = sum_j m[g % n_row][j] * a[b][j]; m NULL: no mask.
 struct MixArgs {
   const uint64_t *a, *v, *m;
   uint64_t *num, *den;
+  DropOut drop;
   const PrimeConst* prime;
   int log_n, nl, n_q, n_k, n_row, first;  // first: index of row 0
 };

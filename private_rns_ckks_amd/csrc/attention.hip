@@ -83,9 +83,7 @@ int check_count(uint64_t items) {
   return items > (1u << 24) ? set_error(CKKS_EINVAL, "too many ciphertexts in one call") : CKKS_OK;
 }
 
-// Tail of every product: relinearise n three-part items X ([3][level+1][N]
-// each, contiguous) into R, rescale into Z, and sum Z into out; without stages
-// the rescale writes Z and the copies go to out.
+// The steps after a product: relinearisation with its rescales, the sum.
 struct Tail {
   Ctx* c;
   hipStream_t s;
@@ -93,15 +91,25 @@ struct Tail {
   ckks_sum_steps st;
 
   uint64_t limb(int l) const { return (uint64_t)(l + 1) * c->N; }
+  DropOut drop_out(int drop) const { return DropOut{c->d_rescale, (int)c->L, drop}; }
 
-  int relin(const uint64_t* X, uint64_t* R, int n, int level) const {
-    return relin_batch(c, s, X, 3 * limb(level), R, 2 * limb(level), n, level, rlk);
+  // n three-part items X ([3][level+1][N] each, written with drop_out(drop))
+  // into out ([2][level+1-drop][N] each), in launches of as many items as 2 GiB
+  // of workspace hold: the items of a launch share the key.
+  int relin_rescale(const uint64_t* X, uint64_t* out, int n, int level, int drop) const {
+    const uint64_t per = ks_rescale_ws_words(c, level, drop);
+    const int chunk = (int)std::max<uint64_t>(1, std::min<uint64_t>({(1ull << 28) / per, (uint64_t)kMaxChunk, (uint64_t)n}));
+    int rc = ensure_workspace(c, per * chunk);
+    for (int b0 = 0; b0 < n && rc == CKKS_OK; b0 += chunk)
+      rc = ks_rescale(c, s, level, drop, std::min(chunk, n - b0), X + b0 * 3 * limb(level), 3 * limb(level), rlk,
+                      out + b0 * 2 * limb(level - drop), 2 * limb(level - drop), c->ws);
+    return rc;
   }
-  int rescale(const uint64_t* R, uint64_t* Z, int n, int level, const uint64_t* acc = nullptr) const {
+  int rescale(const uint64_t* R, uint64_t* Z, int n, int level) const {
     const uint64_t per = (uint64_t)c->N * (2 + 2 * level);
     int rc = ensure_workspace(c, per * std::min(n, kMaxChunk));
     if (rc) return rc;
-    return rescale_batch(c, s, R, 2 * limb(level), Z, 2 * limb(level - 1), n, level, c->ws, c->ws_words, nullptr, acc);
+    return rescale_batch(c, s, R, 2 * limb(level), Z, 2 * limb(level - 1), n, level, c->ws, c->ws_words);
   }
   int sum(const uint64_t* Z, uint64_t* out, int n, int level) const {
     const uint64_t ct = 2 * limb(level);
@@ -150,10 +158,10 @@ int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, 
   if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges({{out, zct * items}}, ins))) return rc;
   if (items == 0) return CKKS_OK;
   CaptureScope cap(c, s);
-  const uint64_t per = 3 * lim + 2 * lim + zct;
+  const uint64_t per = 3 * lim + zct;
   const int block = block_items(per, items);
   if ((rc = ensure_aux(c, per * block))) return rc;
-  uint64_t *X = c->aux, *R = X + 3 * lim * block, *Z = R + 2 * lim * block;
+  uint64_t *X = c->aux, *Z = X + 3 * lim * block;
   for (int b0 = 0; b0 < items; b0 += block) {
     const int n = std::min(block, items - b0);
     PairArgs a;
@@ -163,7 +171,7 @@ int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, 
     a.out = X;
     a.a_bstride = a.b_bstride = 2 * lim;
     a.a_comp = a.b_comp = lim;
-    a.out_bstride = 3 * lim;
+    a.drop = t.drop_out(1);
     a.prime = c->d_prime;
     a.log_n = (int)c->log_n;
     a.nl = l + 1;
@@ -172,8 +180,7 @@ int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, 
     a.n_row = 1;
     a.first = b0;
     uint64_t* dst = out + b0 * zct;
-    if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin(X, R, n, l))) return rc;
-    if ((rc = t.rescale(R, t.st.n_stage ? Z : dst, n, l))) return rc;
+    if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin_rescale(X, t.st.n_stage ? Z : dst, n, l, 1))) return rc;
     if (t.st.n_stage && (rc = t.sum(Z, dst, n, l - 1))) return rc;
   }
   return CKKS_OK;
@@ -205,10 +212,10 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
   if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges(outs, ins))) return rc;
   if (rows == 0) return CKKS_OK;
   CaptureScope cap(c, s);
-  const uint64_t per = 3 * lim + 2 * lim + 2 * lim + mid;
+  const uint64_t per = 3 * lim + 2 * lim + mid;
   const int block = block_items(per, rows);
   if ((rc = ensure_aux(c, per * block))) return rc;
-  uint64_t *X = c->aux, *D = X + 3 * lim * block, *R = D + 2 * lim * block, *Z = R + 2 * lim * block;
+  uint64_t *X = c->aux, *D = X + 3 * lim * block, *Z = D + 2 * lim * block;
   for (int b0 = 0; b0 < rows; b0 += block) {
     const int n = std::min(block, rows - b0);
     MixArgs m;
@@ -218,6 +225,7 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
     m.m = mask;
     m.num = X;
     m.den = den ? D : nullptr;
+    m.drop = t.drop_out(drop);
     m.prime = c->d_prime;
     m.log_n = (int)c->log_n;
     m.nl = l + 1;
@@ -226,12 +234,8 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
     m.n_row = mask ? n_mask : 1;
     m.first = b0;
     uint64_t* to = num + b0 * nct;
-    if ((rc = launch_mix(c, s, m, n)) || (rc = t.relin(X, R, n, l)) || (rc = t.rescale(R, Z, n, l))) return rc;
-    if (mask) {
-      if ((rc = t.rescale(Z, R, n, l - 1)) || (rc = t.sum(R, to, n, l - 2))) return rc;
-    } else if ((rc = t.sum(Z, to, n, l - 1))) {
+    if ((rc = launch_mix(c, s, m, n)) || (rc = t.relin_rescale(X, Z, n, l, drop)) || (rc = t.sum(Z, to, n, l - drop)))
       return rc;
-    }
     if (!den) continue;
     uint64_t* de = den + b0 * dct;
     if (mask) {
@@ -243,26 +247,28 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
   return CKKS_OK;
 }
 
-// X (three parts) = state x q at `level`, both components of q read at its
-// first level+1 limbs (q's components q_comp apart).
-int state_times_q(Ctx* c, hipStream_t s, const uint64_t* state, const uint64_t* q, uint64_t q_bstride,
-                  uint64_t q_comp, uint64_t* X, int n, int level) {
-  const uint64_t lim = (uint64_t)(level + 1) * c->N;
+// X (three parts, one rescale to come) = state x q at `level`, n items in rows
+// of ng: q's item (t, g) at q + (t * n_grp + g)*q_bstride, read at its first
+// level+1 limbs (components q_comp apart).
+int state_times_q(const Tail& t, const uint64_t* state, const uint64_t* q, uint64_t q_bstride, uint64_t q_comp, int ng,
+                  int n_grp, uint64_t* X, int n, int level) {
   PairArgs a;
   memset(&a, 0, sizeof(a));
   a.a = state;
   a.b = q;
   a.out = X;
-  a.a_bstride = 2 * lim;
-  a.a_comp = lim;
+  a.a_bstride = 2 * t.limb(level);
+  a.a_comp = t.limb(level);
   a.b_bstride = q_bstride;
   a.b_comp = q_comp;
-  a.out_bstride = 3 * lim;
-  a.prime = c->d_prime;
-  a.log_n = (int)c->log_n;
+  a.drop = t.drop_out(1);
+  a.prime = t.c->d_prime;
+  a.log_n = (int)t.c->log_n;
   a.nl = level + 1;
+  a.ng = ng;
+  a.n_grp = n_grp;
   a.n_row = 1;
-  return launch_pair(c, s, a, n);
+  return launch_pair(t.c, t.s, a, n);
 }
 
 int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v, int n_tok, int n_grp,
@@ -291,20 +297,21 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
     return rc;
   if (n_grp == 0) return CKKS_OK;
   CaptureScope cap(c, s);
-  // per (token, group): X / the state's product, R, C, S, Z; per group: the
-  // prefix sums carried from one block of tokens to the next
-  const uint64_t mid = 2ull * l * N, per = 3 * lim + ct + mid + sct + yct;
-  const int gb = block_items(per + 3 * lim, n_grp);
+  // per (token, group): X (then the state's product), R = r q and C its
+  // rescale, S the states, Z the outputs before the sum; per group: the prefix
+  // sums carried from one block of tokens to the next
+  const uint64_t mid = 2ull * l * N, per = 3 * lim + (r ? ct + mid : 0) + sct + yct;
+  const int gb = block_items(per + 3 * lim + sct, n_grp);
   const int tb = block_items((per + 3 * lim) * gb, n_tok);
   const uint64_t nb = (uint64_t)gb * tb;
-  if ((rc = ensure_aux(c, per * nb + 3 * lim * gb))) return rc;
-  uint64_t *X = c->aux, *R = X + 3 * lim * nb, *C = R + ct * nb, *S = C + mid * nb, *Z = S + sct * nb,
-           *P = Z + yct * nb;
+  if ((rc = ensure_aux(c, per * nb + (3 * lim + sct) * gb))) return rc;
+  uint64_t *X = c->aux, *S = X + 3 * lim * nb, *Z = S + sct * nb, *R = Z + yct * nb, *C = R + (r ? ct * nb : 0),
+           *P = C + (r ? mid * nb : 0), *V = P + 3 * lim * gb;
   for (int g0 = 0; g0 < n_grp; g0 += gb) {
     const int ng = std::min(gb, n_grp - g0);
     for (int t0 = 0; t0 < n_tok; t0 += tb) {
       const int nt = std::min(tb, n_tok - t0), n = nt * ng;
-      const uint64_t at = ((uint64_t)t0 * n_grp + g0);
+      const uint64_t at = (uint64_t)t0 * n_grp + g0;
       ScanArgs sc;
       memset(&sc, 0, sizeof(sc));
       sc.k = k + at * ct;
@@ -312,7 +319,10 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
       sc.w = w + (uint64_t)t0 * n_row * lim;
       sc.init = t0 ? P : nullptr;
       sc.out = X;
+      sc.last = t0 + nt < n_tok ? P : nullptr;
       sc.tok_stride = (uint64_t)n_grp * ct;
+      sc.drop = t.drop_out(2);
+      sc.add = state_in ? state_in + g0 * sct : nullptr;
       sc.prime = c->d_prime;
       sc.log_n = (int)c->log_n;
       sc.nl = l + 1;
@@ -320,43 +330,30 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
       sc.n_grp = ng;
       sc.n_row = n_row;
       sc.g0 = g0;
-      if ((rc = launch_scan(c, s, sc))) return rc;
-      if (t0 + nt < n_tok)
-        CKKS_HIP_CHECK(hipMemcpyAsync(P, X + (uint64_t)(nt - 1) * ng * 3 * lim, 3 * lim * ng * 8,
-                                      hipMemcpyDeviceToDevice, s));
-      if ((rc = t.relin(X, R, n, l)) || (rc = t.rescale(R, C, n, l))) return rc;
-      if (state_in) {
-        for (int i = 0; i < nt; ++i)
-          if ((rc = t.rescale(C + (uint64_t)i * ng * mid, S + (uint64_t)i * ng * sct, ng, l - 1, state_in + g0 * sct)))
-            return rc;
-      } else if ((rc = t.rescale(C, S, n, l - 1))) {
+      if ((rc = launch_scan(c, s, sc)) || (rc = t.relin_rescale(X, S, n, l, 2))) return rc;
+      const uint64_t* qt = q + at * ct;
+      if (r) {
+        PlainMulArgs pm;
+        memset(&pm, 0, sizeof(pm));
+        pm.in = qt;
+        pm.in_bstride = ct;
+        pm.in_comp = lim;
+        pm.p = r + (uint64_t)t0 * n_row * lim;
+        pm.out = R;
+        pm.out_bstride = ct;
+        pm.prime = c->d_prime;
+        pm.log_n = (int)c->log_n;
+        pm.nl = l + 1;
+        pm.ng = ng;
+        pm.n_grp = n_grp;
+        pm.n_row = n_row;
+        pm.g0 = g0;
+        if ((rc = launch_plain_mul(c, s, pm, n)) || (rc = t.rescale(R, C, n, l))) return rc;
+        if ((rc = state_times_q(t, S, C, mid, mid / 2, 1, 1, X, n, l - 2))) return rc;
+      } else if ((rc = state_times_q(t, S, qt, ct, lim, ng, n_grp, X, n, l - 2))) {
         return rc;
       }
-      for (int i = 0; i < nt; ++i) {
-        const uint64_t* qt = q + (at + (uint64_t)i * n_grp) * ct;
-        uint64_t* xt = X + (uint64_t)i * ng * 3 * sct / 2;
-        const uint64_t* st = S + (uint64_t)i * ng * sct;
-        if (r) {
-          PlainMulArgs pm;
-          memset(&pm, 0, sizeof(pm));
-          pm.in = qt;
-          pm.in_bstride = ct;
-          pm.in_comp = lim;
-          pm.p = r + (uint64_t)(t0 + i) * n_row * lim;
-          pm.out = R;
-          pm.out_bstride = ct;
-          pm.prime = c->d_prime;
-          pm.log_n = (int)c->log_n;
-          pm.nl = l + 1;
-              pm.n_row = n_row;
-          pm.first = g0;
-          if ((rc = launch_plain_mul(c, s, pm, ng)) || (rc = t.rescale(R, C, ng, l))) return rc;
-          if ((rc = state_times_q(c, s, st, C, mid, mid / 2, xt, ng, l - 2))) return rc;
-        } else if ((rc = state_times_q(c, s, st, qt, ct, lim, xt, ng, l - 2))) {
-          return rc;
-        }
-      }
-      if ((rc = t.relin(X, R, n, l - 2)) || (rc = t.rescale(R, Z, n, l - 2))) return rc;
+      if ((rc = t.relin_rescale(X, Z, n, l - 2, 1))) return rc;
       // the block's outputs are contiguous when it holds every group
       for (int i = 0; i < (ng == n_grp ? 1 : nt); ++i)
         if ((rc = t.sum(Z + (uint64_t)i * ng * yct, y + (at + (uint64_t)i * n_grp) * yct, ng == n_grp ? n : ng, l - 3)))
@@ -373,14 +370,15 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
       pm.in_bstride = sct;
       pm.in_comp = sct / 2;
       pm.p = carry;
-      pm.out = R;
+      pm.out = V;
       pm.out_bstride = sct;
       pm.prime = c->d_prime;
       pm.log_n = (int)c->log_n;
       pm.nl = l - 1;
+      pm.ng = pm.n_grp = ng;
       pm.n_row = n_row;
-      pm.first = g0;
-      if ((rc = launch_plain_mul(c, s, pm, ng)) || (rc = t.rescale(R, state_out + g0 * yct, ng, l - 2))) return rc;
+      pm.g0 = g0;
+      if ((rc = launch_plain_mul(c, s, pm, ng)) || (rc = t.rescale(V, state_out + g0 * yct, ng, l - 2))) return rc;
     }
   }
   return CKKS_OK;
@@ -410,10 +408,10 @@ int linattn_step(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v
     return rc;
   if (n_grp == 0) return CKKS_OK;
   CaptureScope cap(c, s);
-  const uint64_t per = 3 * lim + ct + yct;
+  const uint64_t per = 3 * lim + yct;
   const int block = block_items(per, n_grp);
   if ((rc = ensure_aux(c, per * block))) return rc;
-  uint64_t *X = c->aux, *R = X + 3 * lim * block, *Z = R + ct * block;
+  uint64_t *X = c->aux, *Z = X + 3 * lim * block;
   for (int b0 = 0; b0 < n_grp; b0 += block) {
     const int n = std::min(block, n_grp - b0);
     PairArgs a;
@@ -423,23 +421,24 @@ int linattn_step(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v
     a.out = X;
     a.a_bstride = a.b_bstride = ct;
     a.a_comp = a.b_comp = lim;
-    a.out_bstride = 3 * lim;
     if (state_in && decay) {
       a.decay = decay;
       a.state = state_in;
       a.state_bstride = ct;
+    } else if (state_in) {
+      a.add = state_in;
+      a.add_bstride = sct;
     }
+    a.drop = t.drop_out(1);
     a.prime = c->d_prime;
     a.log_n = (int)c->log_n;
     a.nl = l + 1;
+    a.ng = a.n_grp = 1;
     a.n_row = decay ? n_row : 1;
     a.first = b0;
     uint64_t* S = state_out + b0 * sct;
-    if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin(X, R, n, l)) ||
-        (rc = t.rescale(R, S, n, l, state_in && !decay ? state_in + b0 * sct : nullptr)))
-      return rc;
-    if ((rc = state_times_q(c, s, S, q + b0 * ct, ct, lim, X, n, l - 1)) || (rc = t.relin(X, R, n, l - 1)) ||
-        (rc = t.rescale(R, Z, n, l - 1)))
+    if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin_rescale(X, S, n, l, 1))) return rc;
+    if ((rc = state_times_q(t, S, q + b0 * ct, ct, lim, 1, 1, X, n, l - 1)) || (rc = t.relin_rescale(X, Z, n, l - 1, 1)))
       return rc;
     if ((rc = t.sum(Z, y + b0 * yct, n, l - 2))) return rc;
   }

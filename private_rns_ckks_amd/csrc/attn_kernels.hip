@@ -16,15 +16,28 @@ __device__ __forceinline__ uint64_t mul_red(const Split<WIDE>& x, const Split<WI
   return acc_reduce<WIDE>(m, pc.q, pc.r64, pc.r64p, pc.inv1);
 }
 
+// Part 0 or 1 (component comp) of limb i as DropOut says.
+__device__ __forceinline__ uint64_t drop_out(uint64_t x, const DropOut& d, int nl, int i, const uint64_t* add,
+                                             uint64_t add_off, uint64_t q) {
+  if (i >= nl - d.drop) return x;
+  for (int k = 0; k < d.drop; ++k) {
+    const ConstU64 rs = (ConstU64)(d.rescale + ((uint64_t)(nl - 1 - k) * d.L + i) * 4);
+    x = mul_shoup_lazy(x, rs[0], rs[1], q);
+  }
+  x = reduce_4q(x, q);
+  return add ? add_mod(x, add[add_off], q) : x;
+}
+
 template <bool WIDE>
 __global__ __launch_bounds__(256) void plain_mul_kernel(PlainMulArgs a) {
   const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
   const int i = blockIdx.y, b = blockIdx.z;
   const RedConst pc = red_const((ConstPrime)a.prime, i);
   const uint64_t off = ((uint64_t)i << a.log_n) + c, lim = (uint64_t)a.nl << a.log_n;
-  const uint64_t row = (uint64_t)((a.first + b) % a.n_row);
+  const int t = b / a.ng, g = b % a.ng;
+  const uint64_t row = (uint64_t)t * a.n_row + (a.g0 + g) % a.n_row;
   const Split<WIDE> p = split_word<WIDE>(a.p[row * lim + off]);
-  const uint64_t* x = a.in + b * a.in_bstride + off;
+  const uint64_t* x = a.in + ((uint64_t)t * a.n_grp + g) * a.in_bstride + off;
   uint64_t* o = a.out + b * a.out_bstride + off;
   o[0] = mul_red<WIDE>(p, split_word<WIDE>(x[0]), pc);
   o[lim] = mul_red<WIDE>(p, split_word<WIDE>(x[a.in_comp]), pc);
@@ -35,13 +48,13 @@ __global__ __launch_bounds__(256) void pair_kernel(PairArgs a) {
   const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
   const int i = blockIdx.y;
   const int item = blockIdx.z, p = a.first + item;
-  const int ia = a.n_qk ? p / a.n_k : p;
-  const int ib = a.n_qk ? (p / a.n_qk) * a.n_k + p % a.n_k : p;
+  const int ia = a.n_k ? p / a.n_k : p;
+  const int ib = a.n_k ? (p / a.n_qk) * a.n_k + p % a.n_k : (p / a.ng) * a.n_grp + p % a.ng;
   const RedConst pc = red_const((ConstPrime)a.prime, i);
   const uint64_t off = ((uint64_t)i << a.log_n) + c, lim = (uint64_t)a.nl << a.log_n;
   const uint64_t* x = a.a + ia * a.a_bstride + off;
   const uint64_t* y = a.b + ib * a.b_bstride + off;
-  uint64_t* d = a.out + item * a.out_bstride + off;
+  uint64_t* d = a.out + (uint64_t)item * 3 * lim + off;
   const Split<WIDE> x0 = split_word<WIDE>(x[0]), x1 = split_word<WIDE>(x[a.a_comp]);
   const Split<WIDE> y0 = split_word<WIDE>(y[0]), y1 = split_word<WIDE>(y[a.b_comp]);
   AccT<WIDE> m0{}, m1{}, m2{};
@@ -55,8 +68,10 @@ __global__ __launch_bounds__(256) void pair_kernel(PairArgs a) {
     acc_mac<WIDE>(m0, g, split_word<WIDE>(st[0]));
     acc_mac<WIDE>(m1, g, split_word<WIDE>(st[lim]));
   }
-  d[0] = acc_reduce<WIDE>(m0, pc.q, pc.r64, pc.r64p, pc.inv1);
-  d[lim] = acc_reduce<WIDE>(m1, pc.q, pc.r64, pc.r64p, pc.inv1);
+  const uint64_t low = (uint64_t)(a.nl - a.drop.drop) << a.log_n;
+  const uint64_t* add = a.add ? a.add + p * a.add_bstride : nullptr;
+  d[0] = drop_out(acc_reduce<WIDE>(m0, pc.q, pc.r64, pc.r64p, pc.inv1), a.drop, a.nl, i, add, off, pc.q);
+  d[lim] = drop_out(acc_reduce<WIDE>(m1, pc.q, pc.r64, pc.r64p, pc.inv1), a.drop, a.nl, i, add, low + off, pc.q);
   d[2 * lim] = acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1);
 }
 
@@ -74,6 +89,8 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a) {
     r1 = x[lim];
     r2 = x[2 * lim];
   }
+  const uint64_t low = (uint64_t)(a.nl - a.drop.drop) << a.log_n;
+  const uint64_t* add = a.add ? a.add + (uint64_t)g * 2 * low : nullptr;
   for (int t = 0; t < a.n_tok; ++t) {
     const uint64_t* k = a.k + t * a.tok_stride + (uint64_t)g * 2 * lim + off;
     const uint64_t* v = a.v + t * a.tok_stride + (uint64_t)g * 2 * lim + off;
@@ -90,6 +107,12 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a) {
     r1 = add_mod(r1, acc_reduce<WIDE>(m1, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
     r2 = add_mod(r2, acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
     uint64_t* o = a.out + ((uint64_t)t * a.n_grp + g) * 3 * lim + off;
+    o[0] = drop_out(r0, a.drop, a.nl, i, add, off, pc.q);
+    o[lim] = drop_out(r1, a.drop, a.nl, i, add, low + off, pc.q);
+    o[2 * lim] = r2;
+  }
+  if (a.last) {
+    uint64_t* o = a.last + (uint64_t)g * 3 * lim + off;
     o[0] = r0;
     o[lim] = r1;
     o[2 * lim] = r2;
@@ -127,8 +150,8 @@ __global__ __launch_bounds__(256) void mix_kernel(MixArgs a) {
     r2 = add_mod(r2, acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
   }
   uint64_t* o = a.num + (uint64_t)b * 3 * lim + off;
-  o[0] = r0;
-  o[lim] = r1;
+  o[0] = drop_out(r0, a.drop, a.nl, i, nullptr, 0, pc.q);
+  o[lim] = drop_out(r1, a.drop, a.nl, i, nullptr, 0, pc.q);
   o[2 * lim] = r2;
   if (a.den) {
     uint64_t* e = a.den + (uint64_t)b * 2 * lim + off;

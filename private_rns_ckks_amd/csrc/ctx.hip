@@ -129,7 +129,7 @@ static void destroy(Ctx* c) {
     if (c->join_ev[i]) (void)hipEventDestroy(c->join_ev[i]);
   }
   if (c->fork_ev) (void)hipEventDestroy(c->fork_ev);
-  void* bufs[] = {c->d_prime, c->d_tw_fwd, c->d_tw_inv, c->d_modup, c->d_moddown, c->d_rescale, c->ws, c->aux};
+  void* bufs[] = {c->d_prime, c->d_tw_fwd, c->d_tw_inv, c->d_modup, c->d_moddown, c->d_rescale, c->d_drop, c->ws, c->aux};
   for (void* b : bufs)
     if (b) (void)hipFree(b);
   for (uint64_t* b : c->retired) (void)hipFree(b);
@@ -259,6 +259,24 @@ static int build_tables(Ctx* c) {
     md.push_back(prod);
     md.push_back(shoup(prod, qi));
   }
+  c->md.pinvn = md.size();
+  for (uint32_t i = 0; i < L; ++i) {
+    const uint64_t qi = c->mod[i], v = mulmod(md[c->md.pinv + 2 * i], invmod(N % qi, qi), qi);
+    md.push_back(v);
+    md.push_back(shoup(v, qi));
+  }
+  std::vector<uint64_t> drop((size_t)L * 2 * L * 2, 0);
+  for (uint32_t l = 0; l < L; ++l)
+    for (uint32_t d = 1; d <= 2 && d <= l; ++d)
+      for (uint32_t i = 0; i + d <= l; ++i) {
+        const uint64_t qi = c->mod[i];
+        uint64_t v = md[c->md.pinv64 + 2 * i];
+        for (uint32_t y = l - d + 1; y <= l; ++y) v = mulmod(v, invmod(c->mod[y] % qi, qi), qi);
+        uint64_t* o = &drop[(((size_t)l * 2 + d - 1) * L + i) * 2];
+        o[0] = v;
+        o[1] = shoup(v, qi);
+      }
+  if ((rc = upload((void**)&c->d_drop, drop.data(), drop.size() * 8))) return rc;
   if ((rc = upload((void**)&c->d_moddown, md.data(), md.size() * 8))) return rc;
   return CKKS_OK;
 }

@@ -42,8 +42,9 @@ struct ModUpEntry {
 //   [.., + 2L)         : {[P^-1]_{q_i}, Shoup}
 //   [.., + 2L)         : {[2^64 P^-1]_{q_i}, Shoup} (Montgomery sums times P^-1 in one product)
 //   [.., + 2L)         : {[P]_{q_i}, Shoup}
+//   [.., + 2L)         : {[P^-1 * N^-1]_{q_i}, Shoup}
 struct ModDownLayout {
-  size_t phinv, conv, pinv, pinv64, pmod;
+  size_t phinv, conv, pinv, pinv64, pmod, pinvn;
 };
 
 // Kernel timing trace (see ckks_trace_begin): HIP event pairs recorded on the
@@ -70,6 +71,9 @@ struct Ctx {
   uint64_t* d_moddown = nullptr;
   ModDownLayout md{};
   uint64_t* d_rescale = nullptr;  // [L][L][4]: for level l, limb i < l: {ql^-1, Shoup, ql mod q_i, 0}
+  // [L][2][L][2]: for level l, d = 1 or 2 dropped limbs, limb i <= l - d:
+  // {[2^64 P^-1 (q_l .. q_(l-d+1))^-1]_{q_i}, Shoup}
+  uint64_t* d_drop = nullptr;
   uint64_t* ws = nullptr;         // workspace
   size_t ws_words = 0;
   uint64_t* aux = nullptr;        // intermediate operands of composite calls (BSGS matvec)

@@ -87,6 +87,21 @@ size_t ks_ws_words(const Ctx* c, int level);
 int ks_chunk(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uint64_t d_stride,
              uint64_t add_stride, uint64_t accum_stride, uint64_t out_stride, int out_comp_limbs, uint64_t* ws);
 
+// Relinearisation and `drop` (1 or 2) rescales of up to kMaxChunk three-part
+// items X ([3][level+1][N] at X + b*x_stride) into out ([2][level+1-drop][N]),
+// the same words as the key switch followed by the rescales.  On the limbs
+// that stay, parts 0 and 1 of X hold d * (q_l .. q_(l-drop+1))^-1 plus
+// whatever is to be added to the result; the dropped limbs hold d.
+size_t ks_rescale_ws_words(const Ctx* c, int level, int drop);  // per item
+int ks_rescale(Ctx* c, hipStream_t s, int level, int drop, int n_items, const uint64_t* X, uint64_t x_stride,
+               const uint64_t* rlk, uint64_t* out, uint64_t out_stride, uint64_t* ws);
+// Its step in rescale.hip: from the dropped limbs' coefficients (A item b at A
+// + b*per, [2][comp_limbs][N], the dropped limbs first, without their ModDown
+// term) and the ModDown conversion W ([2][level+1][N]), the forward column
+// pass of (w + v) q_l^-1 (once more for drop 2) on the limbs that stay, in W.
+int drop_col_pass(Ctx* c, hipStream_t s, uint64_t* A, uint64_t* W, uint64_t per, int n_items, int level, int drop,
+                  int comp_limbs);
+
 // Hoisted rotations of several inputs that share one decomposition each:
 // ks_decompose raises the digits of c1 (input i at c1 + i*c1_stride, NTT form)
 // to the extended basis and transforms them, into dec (input i at

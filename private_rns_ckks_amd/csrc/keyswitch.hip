@@ -28,6 +28,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <string>
 #include <vector>
@@ -277,15 +278,25 @@ __device__ __forceinline__ void ip_inverse_row_store(uint64_t (&x)[W], uint64_t*
   ip_inv_rounds_up<LOGB, AR, W, G::RW>(lds, tile, log_n, s0, twi, q, inv1, dst);
 }
 
-// acc: item b at acc + b*acc_bstride, [2][K][N] (special limbs only).
-template <int LOGB, int LOGN, int W = 8>
+// With TOP the targets begin at the ciphertext limbs t0..l that a rescale
+// drops after the switch (ks_rescale): their accumulators get P * add (so that
+// P^-1 times the sum is the switched polynomial before its ModDown term) and
+// take the same inverse row pass.
+struct TopArgs {
+  const uint64_t* add[2];  // component c's additive term, item b at + b*add_bstride, [nq][N]
+  uint64_t add_bstride;
+  const uint64_t* pmod;    // [L][2]: {[P]_{q_i}, Shoup}
+};
+
+// acc: item b at acc + b*acc_bstride, [2][targets][N].
+template <int LOGB, int LOGN, int W = 8, bool TOP = false>
 __global__ __launch_bounds__((IPRounds<LOGB, W>::THREADS)) __attribute__((amdgpu_waves_per_eu(W == 8 ? 2 : (LOGN ? 4 : 3)))) void ip_special_kernel(
-    RowIPArgs a, const uint64_t* twi) {
+    RowIPArgs a, const uint64_t* twi, TopArgs top) {
   __shared__ uint64_t lds[(1 << LOGB) * IPRounds<LOGB, W>::KC];
   __shared__ ulonglong2 twl[IPRounds<LOGB, W>::KC * ((1 << LOGB) - 1)];
   const GridPos g0 = a.shared_key ? row_grid_pos<true>() : row_grid_pos<false>();
-  const int t = g0.job + a.t0;  // a special limb
-  const int keyl = a.L + (t - a.level - 1);
+  const int t = g0.job + a.t0;  // a special limb (TOP: or a ciphertext limb)
+  const int keyl = TOP && t <= a.level ? t : a.L + (t - a.level - 1);
   const PrimeConst& pc = a.prime[keyl];
   const int log_n = LOGN ? LOGN : a.log_n;
   const uint32_t s0 = (uint32_t)logb_col(log_n);
@@ -320,8 +331,32 @@ __global__ __launch_bounds__((IPRounds<LOGB, W>::THREADS)) __attribute__((amdgpu
         acca[i] = acca[i] >= two_q ? acca[i] - two_q : acca[i];
       }
     }
-    uint64_t* ob = a.acc + gp.item * a.acc_bstride + ((uint64_t)(t - a.level - 1) << log_n);
-    uint64_t* oa = ob + ((uint64_t)a.K << log_n);
+    if (TOP && t <= a.level) {
+      int col, base;
+      ip_item<IPRounds<LOGB, W>::RW, LOGB, W>(0, 0, col, base);
+      const uint32_t h0 = ip_word<LOGB, W>(gp.tile, base, col) >> 1;
+      const uint64_t pw = top.pmod[2 * t], pwp = top.pmod[2 * t + 1];
+      const uint64_t bound = iar == AR_STRICT ? 2 * pc.q : 4 * pc.q;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const ulonglong2* ad =
+            reinterpret_cast<const ulonglong2*>(top.add[c] + gp.item * top.add_bstride + ((uint64_t)t << log_n));
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+          const ulonglong2 v = at_u32(ad, h0 + i);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint64_t& x = c ? acca[2 * i + e] : accb[2 * i + e];
+            uint64_t p = mul_shoup_lazy(e ? v.y : v.x, pw, pwp, pc.q);
+            if (iar == AR_STRICT && p >= bound) p -= bound;  // 4q < 2^64, but 8q is not
+            x += p;
+            x = x >= bound ? x - bound : x;
+          }
+        }
+      }
+    }
+    uint64_t* ob = a.acc + gp.item * a.acc_bstride + ((uint64_t)(t - a.t0) << log_n);
+    uint64_t* oa = ob + ((uint64_t)(TOP ? gridDim.y : a.K) << log_n);
     if (iar == AR_LAZY) {
       ip_inverse_row_store<LOGB, AR_LAZY, W>(accb, lds, gp.tile, log_n, tw_i, pc.q, pc.inv1, ob);
       ip_inverse_row_store<LOGB, AR_LAZY, W>(acca, lds, gp.tile, log_n, tw_i, pc.q, pc.inv1, oa);
@@ -335,20 +370,21 @@ __global__ __launch_bounds__((IPRounds<LOGB, W>::THREADS)) __attribute__((amdgpu
   }
 }
 
-typedef void (*IPSpecialFn)(RowIPArgs, const uint64_t*);
+typedef void (*IPSpecialFn)(RowIPArgs, const uint64_t*, TopArgs);
 
 // Words per thread of the special-limb inner product (IPRounds): 8 measured
 // faster than 4 here (the extra inverse round and its twiddle loads cost more
 // than the added waves gain).
 constexpr int kSpecialW = 8;
 
+template <bool TOP>
 IPSpecialFn pick_ip_special(int log_n, int logb) {
-  if (log_n == 16 && logb == 8) return ip_special_kernel<8, 16, kSpecialW>;
+  if (log_n == 16 && logb == 8) return ip_special_kernel<8, 16, kSpecialW, TOP>;
   switch (logb) {
-    case 5: return ip_special_kernel<5, 0, kSpecialW>;
-    case 6: return ip_special_kernel<6, 0, kSpecialW>;
-    case 7: return ip_special_kernel<7, 0, kSpecialW>;
-    case 8: return ip_special_kernel<8, 0, kSpecialW>;
+    case 5: return ip_special_kernel<5, 0, kSpecialW, TOP>;
+    case 6: return ip_special_kernel<6, 0, kSpecialW, TOP>;
+    case 7: return ip_special_kernel<7, 0, kSpecialW, TOP>;
+    case 8: return ip_special_kernel<8, 0, kSpecialW, TOP>;
   }
   return nullptr;
 }
@@ -985,28 +1021,12 @@ int ks_hoisted_chunk(Ctx* c, hipStream_t s, int level, int n_items, const KSItem
   return ks_back(c, s, level, n_items, it, A, W, per, 0, 0, out_stride, nq);
 }
 
-// The fused pipeline (digits and special primes of at most 8 limbs):
-//   intt_row_gather   inverse row pass of tau_g(c1)                 -> Y
-//   modup pass        inverse column pass of each digit, ModUp,
-//                     forward column pass of every target limb      -> E
-//   ip_special        forward row pass + inner product of the K
-//                     special limbs, inverse row pass               -> A
-//   moddown pass      inverse column pass of A, centred ModDown,
-//                     forward column pass of every ciphertext limb  -> W
-//   comb_ip           forward row pass + inner product of the
-//                     ciphertext limbs, forward row pass of W,
-//                     acc*P^-1 - NTT(w) (+ add) (+ accum)           -> out
-int ks_chunk_fused(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uint64_t d_stride,
-                   uint64_t add_stride, uint64_t accum_stride, uint64_t out_stride, int out_comp_limbs, uint64_t* ws) {
-  const uint32_t N = c->N;
+// Steps A to C of the fused pipeline: the raised digits E (forward column pass
+// done) of the items' inputs, and the arguments of the inner products on them.
+static int ks_raise(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uint64_t d_stride, uint64_t* Y,
+                    uint64_t* E, uint64_t per, RowIPArgs* ip) {
   const int log_n = (int)c->log_n;
-  const int nq = level + 1, next = nq + (int)c->K, beta = c->beta(level), K = (int)c->K;
-  const uint64_t per = fused_ws_words(c, level);
-  uint64_t* Y = ws;
-  uint64_t* E = Y + (uint64_t)nq * N;
-  uint64_t* A = E + (uint64_t)beta * next * N;
-  uint64_t* W = A + (uint64_t)2 * K * N;
-  const int lr = logb_row(log_n);
+  const int nq = level + 1;
   int rc;
   {
     const char* dump = getenv("CKKS_DEBUG_DUMP");
@@ -1026,77 +1046,188 @@ int ks_chunk_fused(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* 
     if ((rc = launch_gather(c, s, ga, nq, n_items))) return rc;
   }
   if ((rc = modup_steps(c, s, level, n_items, Y, per, E, per))) return rc;
-  RowIPArgs ip;
-  memset(&ip, 0, sizeof(ip));
-  ip.E = E;
-  ip.E_bstride = per;
-  ip.T = it[0].d;
-  ip.T_bstride = d_stride;
-  for (int i = 0; i < n_items; ++i) ip.g[i] = it[i].g;
-  ip.shared_key = 1;
+  memset(ip, 0, sizeof(*ip));
+  ip->E = E;
+  ip->E_bstride = per;
+  ip->T = it[0].d;
+  ip->T_bstride = d_stride;
+  for (int i = 0; i < n_items; ++i) ip->g[i] = it[i].g;
+  ip->shared_key = 1;
   for (int i = 0; i < n_items; ++i) {
-    ip.evk[i] = it[i].evk;
-    if (it[i].evk != it[0].evk) ip.shared_key = 0;
+    ip->evk[i] = it[i].evk;
+    if (it[i].evk != it[0].evk) ip->shared_key = 0;
   }
-  ip.tw = c->d_tw_fwd;
-  ip.prime = c->d_prime;
-  ip.log_n = log_n;
-  ip.level = level;
-  ip.next = next;
-  ip.beta = beta;
-  ip.alpha = (int)c->alpha;
-  ip.L = (int)c->L;
-  ip.K = K;
-  ip.n_items = n_items;
-  {
-    RowIPArgs sp = ip;
-    sp.acc = A;
-    sp.acc_bstride = per;
-    sp.t0 = nq;
-    sp.items_per_wg = 2;
-    IPSpecialFn fn = pick_ip_special(log_n, lr);
-    if (!fn) return set_error(CKKS_EINTERNAL, "unsupported NTT pass size");
-    const double units = (double)K * ((double)beta * (N / 2) * lr + N * (2.0 * beta + 2) + 2.0 * (N / 2) * lr);
-    TraceScope ts(c, s, "ip_special", units * n_items);
-    const int logkc = ip_logkc(lr, kSpecialW);
-    hipLaunchKernelGGL(fn, dim3(N >> (lr + logkc), K, (n_items + 1) / 2), dim3((1u << (lr + logkc)) / kSpecialW), 0, s,
-                       sp, c->d_tw_inv);
-    CKKS_HIP_CHECK(hipGetLastError());
-  }
-  if ((rc = moddown_steps(c, s, level, n_items, A, per, W, per))) return rc;
-  {
-    CombIPArgs ca;
-    memset(&ca, 0, sizeof(ca));
-    ca.ip = ip;
-    ca.ip.t0 = 0;
-    ca.ip.items_per_wg = 2;
-    ca.W = W;
-    ca.W_bstride = per;
-    ca.add[0] = it[0].add[0];
-    ca.add[1] = it[0].add[1];
-    ca.add_bstride = add_stride;
-    for (int i = 0; i < n_items; ++i) ca.add_g[i] = it[i].add_g;
-    ca.accum = it[0].accum;
-    ca.accum_bstride = accum_stride;
-    ca.out = it[0].out;
-    ca.out_bstride = out_stride;
-    ca.out_comp_limbs = out_comp_limbs;
-    ca.pinv64 = c->d_moddown + c->md.pinv64;
-    CombIPFn fn = pick_comb_ip(log_n, lr);
-    if (!fn) return set_error(CKKS_EINTERNAL, "unsupported NTT pass size");
-    double units = 0;
-    for (int j = 0; j < beta; ++j) {
-      const int na = c->modup[level][j].hi - c->modup[level][j].lo;
-      units += (double)(nq - na) * (N / 2) * lr;  // row passes of the converted ciphertext limbs
-    }
-    units += (double)nq * (N * (2.0 * beta + 2) + 2.0 * ((N / 2) * lr + N));
-    TraceScope ts(c, s, "comb_ip", units * n_items);
-    const int logkc = ip_logkc(lr, kCombW);
-    hipLaunchKernelGGL(fn, dim3(N >> (lr + logkc), nq, (n_items + 1) / 2), dim3((1u << (lr + logkc)) / kCombW), 0,
-                       s, ca);
-    CKKS_HIP_CHECK(hipGetLastError());
-  }
+  ip->tw = c->d_tw_fwd;
+  ip->prime = c->d_prime;
+  ip->log_n = log_n;
+  ip->level = level;
+  ip->next = nq + (int)c->K;
+  ip->beta = c->beta(level);
+  ip->alpha = (int)c->alpha;
+  ip->L = (int)c->L;
+  ip->K = (int)c->K;
+  ip->items_per_wg = 2;
+  ip->n_items = n_items;
   return CKKS_OK;
+}
+
+// Step D on the special limbs and, with `drop` > 0, the ciphertext limbs
+// l-drop+1..l before them, into A ([2][drop + K][N] per item).
+static int launch_ip_special(Ctx* c, hipStream_t s, const RowIPArgs& ip, uint64_t* A, uint64_t per, int drop,
+                             const TopArgs& top) {
+  const uint32_t N = c->N;
+  const int log_n = (int)c->log_n, lr = logb_row(log_n), targets = (int)c->K + drop;
+  RowIPArgs sp = ip;
+  sp.acc = A;
+  sp.acc_bstride = per;
+  sp.t0 = ip.level + 1 - drop;
+  IPSpecialFn fn = drop ? pick_ip_special<true>(log_n, lr) : pick_ip_special<false>(log_n, lr);
+  if (!fn) return set_error(CKKS_EINTERNAL, "unsupported NTT pass size");
+  const double units = (double)targets * ((double)ip.beta * (N / 2) * lr + N * (2.0 * ip.beta + 2) + 2.0 * (N / 2) * lr);
+  TraceScope ts(c, s, "ip_special", units * ip.n_items);
+  const int logkc = ip_logkc(lr, kSpecialW);
+  hipLaunchKernelGGL(fn, dim3(N >> (lr + logkc), targets, (ip.n_items + 1) / 2), dim3((1u << (lr + logkc)) / kSpecialW),
+                     0, s, sp, c->d_tw_inv, top);
+  CKKS_HIP_CHECK(hipGetLastError());
+  return CKKS_OK;
+}
+
+// Step I on the ciphertext limbs 0..n_limb-1.
+static int launch_comb_ip(Ctx* c, hipStream_t s, const CombIPArgs& ca, int n_limb) {
+  const uint32_t N = c->N;
+  const int log_n = (int)c->log_n, lr = logb_row(log_n), level = ca.ip.level;
+  CombIPFn fn = pick_comb_ip(log_n, lr);
+  if (!fn) return set_error(CKKS_EINTERNAL, "unsupported NTT pass size");
+  double units = 0;
+  for (int j = 0; j < ca.ip.beta; ++j) {
+    const int na = c->modup[level][j].hi - c->modup[level][j].lo;
+    units += (double)std::max(0, n_limb - na) * (N / 2) * lr;  // row passes of the converted ciphertext limbs
+  }
+  units += (double)n_limb * (N * (2.0 * ca.ip.beta + 2) + 2.0 * ((N / 2) * lr + N));
+  TraceScope ts(c, s, "comb_ip", units * ca.ip.n_items);
+  const int logkc = ip_logkc(lr, kCombW);
+  hipLaunchKernelGGL(fn, dim3(N >> (lr + logkc), n_limb, (ca.ip.n_items + 1) / 2), dim3((1u << (lr + logkc)) / kCombW),
+                     0, s, ca);
+  CKKS_HIP_CHECK(hipGetLastError());
+  return CKKS_OK;
+}
+
+// The fused pipeline (digits and special primes of at most 8 limbs):
+//   intt_row_gather   inverse row pass of tau_g(c1)                 -> Y
+//   modup pass        inverse column pass of each digit, ModUp,
+//                     forward column pass of every target limb      -> E
+//   ip_special        forward row pass + inner product of the K
+//                     special limbs, inverse row pass               -> A
+//   moddown pass      inverse column pass of A, centred ModDown,
+//                     forward column pass of every ciphertext limb  -> W
+//   comb_ip           forward row pass + inner product of the
+//                     ciphertext limbs, forward row pass of W,
+//                     acc*P^-1 - NTT(w) (+ add) (+ accum)           -> out
+int ks_chunk_fused(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uint64_t d_stride,
+                   uint64_t add_stride, uint64_t accum_stride, uint64_t out_stride, int out_comp_limbs, uint64_t* ws) {
+  const uint32_t N = c->N;
+  const int nq = level + 1, next = nq + (int)c->K, beta = c->beta(level), K = (int)c->K;
+  const uint64_t per = fused_ws_words(c, level);
+  uint64_t* Y = ws;
+  uint64_t* E = Y + (uint64_t)nq * N;
+  uint64_t* A = E + (uint64_t)beta * next * N;
+  uint64_t* W = A + (uint64_t)2 * K * N;
+  int rc;
+  CombIPArgs ca;
+  memset(&ca, 0, sizeof(ca));
+  if ((rc = ks_raise(c, s, level, n_items, it, d_stride, Y, E, per, &ca.ip))) return rc;
+  if ((rc = launch_ip_special(c, s, ca.ip, A, per, 0, TopArgs{}))) return rc;
+  if ((rc = moddown_steps(c, s, level, n_items, A, per, W, per))) return rc;
+  ca.W = W;
+  ca.W_bstride = per;
+  ca.add[0] = it[0].add[0];
+  ca.add[1] = it[0].add[1];
+  ca.add_bstride = add_stride;
+  for (int i = 0; i < n_items; ++i) ca.add_g[i] = it[i].add_g;
+  ca.accum = it[0].accum;
+  ca.accum_bstride = accum_stride;
+  ca.out = it[0].out;
+  ca.out_bstride = out_stride;
+  ca.out_comp_limbs = out_comp_limbs;
+  ca.pinv64 = c->d_moddown + c->md.pinv64;
+  return launch_comb_ip(c, s, ca, nq);
+}
+
+size_t ks_rescale_ws_words(const Ctx* c, int level, int drop) {
+  return fused_ws_words(c, level) + (size_t)2 * drop * c->N;
+}
+
+// Relinearisation and `drop` rescales in one (see kernels.h).  With w the
+// ModDown conversion, R = acc P^-1 - NTT(w) + d the relinearised ciphertext
+// and v the centred inverse transform of its limb l, the rescale is
+//   (R - NTT(v)) q_l^-1 = acc (P q_l)^-1 + d q_l^-1 - NTT((w + v) q_l^-1),
+// so the conversion and the rescale share one forward transform, R is never
+// written, and only limb l of R is formed, in coefficient form: ip_special
+// takes it along with the special limbs.  A second rescale needs limb l-1 as
+// well, v' = (iNTT(R)_{l-1} - v) q_l^-1, and one more constant per limb.
+int ks_rescale(Ctx* c, hipStream_t s, int level, int drop, int n_items, const uint64_t* X, uint64_t x_stride,
+               const uint64_t* rlk, uint64_t* out, uint64_t out_stride, uint64_t* ws) {
+  const uint32_t N = c->N;
+  const int nq = level + 1, next = nq + (int)c->K, beta = c->beta(level), K = (int)c->K, low = nq - drop;
+  if (n_items > kMaxChunk || drop < 1 || drop > 2 || low < 1) return set_error(CKKS_EINTERNAL, "bad rescale chunk");
+  const uint64_t per = ks_rescale_ws_words(c, level, drop);
+  uint64_t* Y = ws;
+  uint64_t* E = Y + (uint64_t)nq * N;
+  uint64_t* A = E + (uint64_t)beta * next * N;  // [2][drop + K][N]
+  uint64_t* W = A + (uint64_t)2 * (K + drop) * N;
+  KSItem it[kMaxChunk];
+  memset(it, 0, sizeof(it));
+  for (int i = 0; i < n_items; ++i) {
+    it[i].d = X + i * x_stride + 2ull * nq * N;
+    it[i].evk = rlk;
+  }
+  int rc;
+  CombIPArgs ca;
+  memset(&ca, 0, sizeof(ca));
+  if ((rc = ks_raise(c, s, level, n_items, it, x_stride, Y, E, per, &ca.ip))) return rc;
+  TopArgs top;
+  top.add[0] = X;
+  top.add[1] = X + (uint64_t)nq * N;
+  top.add_bstride = x_stride;
+  top.pmod = c->d_moddown + c->md.pmod;
+  if ((rc = launch_ip_special(c, s, ca.ip, A, per, drop, top))) return rc;
+  {
+    NttJobs jobs;
+    uint32_t off[kMaxJobs];
+    for (int comp = 0; comp < 2; ++comp)
+      for (int k = 0; k < drop + K; ++k) {
+        const int limb = comp * (drop + K) + k;
+        off[jobs.n] = (uint32_t)(k < drop ? c->md.pinvn + 2 * (low + k) : c->md.phinv + 2 * (k - drop));
+        jobs.add(limb, limb, k < drop ? low + k : (int)c->L + k - drop);
+      }
+    if ((rc = ntt_pass_only(c, s, A, A, per, per, n_items, jobs, true, false, 2, c->d_moddown, off))) return rc;
+  }
+  ModDownArgs md;
+  memset(&md, 0, sizeof(md));
+  md.acc = A;
+  md.w = W;
+  md.acc_bstride = per;
+  md.w_bstride = per;
+  md.conv = c->d_moddown + c->md.conv;
+  md.prime = c->d_prime;
+  md.n = N;
+  md.level = level;
+  md.acc_comp_limbs = drop + K;
+  md.acc_k0 = drop;
+  md.L = (int)c->L;
+  md.K = K;
+  if ((rc = launch_moddown_conv(c, s, md, n_items))) return rc;
+  if ((rc = drop_col_pass(c, s, A, W, per, n_items, level, drop, drop + K))) return rc;
+  ca.W = W;
+  ca.W_bstride = per;
+  ca.add[0] = X;
+  ca.add[1] = X + (uint64_t)nq * N;
+  ca.add_bstride = x_stride;
+  ca.out = out;
+  ca.out_bstride = out_stride;
+  ca.out_comp_limbs = low;
+  ca.pinv64 = c->d_drop + ((uint64_t)level * 2 + drop - 1) * c->L * 2;
+  return launch_comb_ip(c, s, ca, low);
 }
 
 int ks_chunk(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uint64_t d_stride,

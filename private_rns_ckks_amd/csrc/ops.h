@@ -16,10 +16,6 @@ int rescale_batch(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride,
                   int batch, int level, uint64_t* ws, uint64_t ws_words, const uint64_t* add0 = nullptr,
                   const uint64_t* acc = nullptr);
 
-// Relinearisation of `batch` three-part ciphertexts (see ops.hip).
-int relin_batch(Ctx* c, hipStream_t s, const uint64_t* T, uint64_t t_stride, uint64_t* out, uint64_t out_stride,
-                int batch, int level, const uint64_t* rlk);
-
 // device buffers are read and written with 16-byte vector accesses
 inline bool misaligned(const void* p) { return ((uintptr_t)p & 15) != 0; }
 

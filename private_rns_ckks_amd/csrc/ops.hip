@@ -896,12 +896,10 @@ int ckks_ptmatvec(ckks_ctx* ctx, const uint64_t* d_x, int n_in, const uint64_t* 
 
 }  // extern "C"
 
-namespace ckks {
-
 // Relinearisation of `batch` three-part ciphertexts T (item b at
 // T + b*t_stride, [3][l+1][N]) into out (item b at out + b*out_stride,
 // [2][l+1][N]): (T0, T1) + KS_{s^2 -> s}(T2), in chunks over the lanes.
-int relin_batch(Ctx* c, hipStream_t s, const uint64_t* T, uint64_t t_stride, uint64_t* out,
+static int relin_batch(Ctx* c, hipStream_t s, const uint64_t* T, uint64_t t_stride, uint64_t* out,
                        uint64_t out_stride, int batch, int level, const uint64_t* rlk) {
   const int nq = level + 1;
   const uint64_t limb = (uint64_t)nq * c->N;
@@ -931,8 +929,6 @@ int relin_batch(Ctx* c, hipStream_t s, const uint64_t* T, uint64_t t_stride, uin
   }
   return join_lanes(c, s, lanes, rc);
 }
-
-}  // namespace ckks
 
 extern "C" {
 

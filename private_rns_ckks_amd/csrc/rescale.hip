@@ -115,7 +115,119 @@ __global__ __launch_bounds__(kThreads) void rescale_row_kernel(RescalePassArgs a
   run_pass<RA, RB, false, false, LOGN>(io, lds, gp.tile, a.log_n, a.tw + ((uint64_t)i << (a.log_n + 1)), pc.q, fin);
 }
 
+// ---------------------------------------------------------------------------
+// The rescales of a key switch (ks_rescale).
+struct DropArgs {
+  uint64_t* A;  // item b: A + b*per, [2][comp_limbs][N]: dropped limbs q_(l-drop+1)..q_l first
+  uint64_t* W;  // item b: W + b*per, [2][l+1][N]
+  uint64_t per;
+  const uint64_t* tab;  // as RescalePassArgs
+  const PrimeConst* prime;
+  const uint64_t* tw;
+  int log_n, level, L, drop, comp_limbs;
+};
+
+// The centred lift of x mod the dropped prime ql, modulo q.
+__device__ __forceinline__ uint64_t lift_mod(uint64_t x, uint64_t half, uint64_t qlmod, uint64_t q, uint64_t inv1) {
+  const uint64_t t = x >= q ? reduce64(x, q, inv1) : x;
+  return x > half ? sub_mod(t, qlmod, q) : t;
+}
+
+// The values dropped, canonical, in place: v = iNTT(R)_l = A_l - w_l and, for
+// a second rescale, v' = (A_(l-1) - w_(l-1) - v) q_l^-1 mod q_(l-1).
+__global__ __launch_bounds__(256) void drop_values_kernel(DropArgs a) {
+  const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
+  const int comp = blockIdx.y, l = a.level;
+  uint64_t* v = a.A + blockIdx.z * a.per + ((uint64_t)(comp * a.comp_limbs) << a.log_n) + c;
+  const uint64_t* w = a.W + blockIdx.z * a.per + ((uint64_t)(comp * (l + 1)) << a.log_n) + c;
+  const uint64_t N = 1ull << a.log_n;
+  const PrimeConst& pl = a.prime[l];
+  const uint64_t x = sub_mod(v[(a.drop - 1) * N], reduce64(w[l * N], pl.q, pl.inv1), pl.q);
+  v[(a.drop - 1) * N] = x;
+  if (a.drop == 1) return;
+  const PrimeConst& p = a.prime[l - 1];
+  const uint64_t* rs = a.tab + ((uint64_t)l * a.L + l - 1) * 4;
+  uint64_t u = sub_mod(v[0], reduce64(w[(l - 1) * N], p.q, p.inv1), p.q);
+  u = sub_mod(u, lift_mod(x, (pl.q - 1) / 2, rs[2], p.q, p.inv1), p.q);
+  v[0] = reduce_2q(mul_shoup(u, rs[0], rs[1], p.q), p.q);
+}
+
+// Column-pass input: (w + v) q_l^-1 computed on load, for DROP 2 then
+// (that + v') q_(l-1)^-1.  w is congruent, below 6q (below q for primes above
+// 2^60), so the sums stay below 2^63.
+template <int DROP>
+struct DropIO {
+  typedef NoOps Ops;
+  uint64_t* w;
+  const uint64_t* v[DROP];
+  uint64_t q, inv1, qinv[DROP], qinvp[DROP], qlmod[DROP], half[DROP];
+  __device__ __forceinline__ uint64_t load(uint32_t j) const {
+    uint64_t x = w[j];
+#pragma unroll
+    for (int d = 0; d < DROP; ++d)
+      x = mul_shoup(x + lift_mod(v[d][j], half[d], qlmod[d], q, inv1), qinv[d], qinvp[d], q);
+    return reduce_2q(x, q);
+  }
+  __device__ __forceinline__ void after_load(uint32_t, uint64_t) const {}
+  __device__ __forceinline__ Ops fetch(uint32_t) const { return Ops(); }
+  __device__ __forceinline__ void store(uint32_t j, uint64_t x, const Ops&) const { w[j] = x; }
+};
+
+template <int RA, int RB, int LOGN, int DROP>
+__global__ __launch_bounds__(kThreads) void drop_col_kernel(DropArgs a) {
+  constexpr int ROWS = 1 << (RA + RB);
+  __shared__ uint64_t lds[lds_words<true, RB, ROWS>()];
+  const int low = a.level + 1 - DROP;
+  const int comp = blockIdx.y / low, i = blockIdx.y % low;
+  const PrimeConst& pc = a.prime[i];
+  DropIO<DROP> io;
+  io.w = a.W + blockIdx.z * a.per + ((uint64_t)(comp * (a.level + 1) + i) << a.log_n);
+#pragma unroll
+  for (int d = 0; d < DROP; ++d) {  // q_l first
+    const uint64_t* rs = a.tab + ((uint64_t)(a.level - d) * a.L + i) * 4;
+    io.v[d] = a.A + blockIdx.z * a.per + ((uint64_t)(comp * a.comp_limbs + DROP - 1 - d) << a.log_n);
+    io.qinv[d] = rs[0];
+    io.qinvp[d] = rs[1];
+    io.qlmod[d] = rs[2];
+    io.half[d] = (a.prime[a.level - d].q - 1) / 2;
+  }
+  io.q = pc.q;
+  io.inv1 = pc.inv1;
+  Finish fin{0, 0, 0, pc.inv1};
+  run_pass<RA, RB, false, true, LOGN>(io, lds, blockIdx.x, a.log_n, a.tw + ((uint64_t)i << (a.log_n + 1)), pc.q,
+                                      fin);
+}
+
 }  // namespace
+
+int drop_col_pass(Ctx* c, hipStream_t s, uint64_t* A, uint64_t* W, uint64_t per, int n_items, int level, int drop,
+                  int comp_limbs) {
+  const uint32_t N = c->N;
+  const int log_n = (int)c->log_n, lc = logb_col(log_n), low = level + 1 - drop;
+  DropArgs a;
+  a.A = A;
+  a.W = W;
+  a.per = per;
+  a.tab = c->d_rescale;
+  a.prime = c->d_prime;
+  a.tw = c->d_tw_fwd;
+  a.log_n = log_n;
+  a.level = level;
+  a.L = (int)c->L;
+  a.drop = drop;
+  a.comp_limbs = comp_limbs;
+  {
+    TraceScope ts(c, s, "rescale", (double)n_items * 2 * drop * N);
+    hipLaunchKernelGGL(drop_values_kernel, dim3(N / 256, 2, n_items), dim3(256), 0, s, a);
+    CKKS_HIP_CHECK(hipGetLastError());
+  }
+  auto fn = drop == 1 ? CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 1) : CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 2);
+  if (!fn) return set_error(CKKS_EINTERNAL, "unsupported N");
+  TraceScope ts(c, s, "rescale", (double)n_items * 2 * low * ((double)(N / 2) * lc + drop * N));
+  hipLaunchKernelGGL(fn, dim3(pass_tiles(N, lc), 2 * low, n_items), dim3(kThreads), 0, s, a);
+  CKKS_HIP_CHECK(hipGetLastError());
+  return CKKS_OK;
+}
 
 int rescale_fused(Ctx* c, hipStream_t s, const uint64_t* ct, uint64_t ct_bstride, const uint64_t* v, uint64_t v_bstride,
                   uint64_t* w, uint64_t w_bstride, uint64_t* out, uint64_t out_bstride, int batch, int level,
