@@ -1,7 +1,8 @@
 // Entry points of the attention calls: argument checks, and the composition of
 // slotwise products (attn_kernels.hip), relinearisation and rescale (ops.hip)
 // and the sum over a packed axis (sumrot.hip).  Items go in blocks whose
-// intermediates fit kBlockWords.
+// intermediates fit block_words().
+#include <stdlib.h>
 #include <string.h>
 
 #include <algorithm>
@@ -13,12 +14,17 @@ namespace ckks {
 
 namespace {
 
-// Words of intermediates a call holds at once (4 GiB of the card's 288): at
-// N = 2^16 and 24 limbs some 25 items, enough to fill the chip many times.
-constexpr uint64_t kBlockWords = 1ull << 29;
+// Words of intermediates a call holds at once: CKKS_BLOCK_MB of memory, by
+// default 4 GiB of the card's 288 (some 40 items at N = 2^16 and 24 limbs,
+// enough to fill the chip many times).
+uint64_t block_words() {
+  const char* e = getenv("CKKS_BLOCK_MB");
+  const long mb = e ? atol(e) : 0;
+  return (uint64_t)(mb > 0 ? mb : 4096) << 17;
+}
 
 int block_items(uint64_t per_item, uint64_t items) {
-  return (int)std::max<uint64_t>(1, std::min<uint64_t>({items, kBlockWords / per_item, 1024}));
+  return (int)std::max<uint64_t>(1, std::min<uint64_t>({items, block_words() / per_item, 1024}));
 }
 
 // Tells the context's buffers that this call's stream is being captured:

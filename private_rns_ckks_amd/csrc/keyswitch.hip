@@ -411,9 +411,14 @@ struct CombIPArgs {
   uint64_t out_bstride;
   int out_comp_limbs;
   const uint64_t* pinv64;  // [L][2]: {[2^64 P^-1]_{q_i}, Shoup}
+  // Instead of the inner product: stored accumulators (any 64-bit words), item
+  // b at + b*acc_bstride, [2][acc_comp_limbs][N]; pinv64 then holds [P^-1].
+  const uint64_t* acc;
+  uint64_t acc_bstride;
+  int acc_comp_limbs;
 };
 
-template <int LOGB, int LOGN, int AR, int W>
+template <int LOGB, int LOGN, int AR, int W, bool STORED>
 __device__ __forceinline__ void comb_ip_body(const CombIPArgs& a, uint64_t* lds, const ulonglong2* twl,
                                              const PrimeConst& pc, int i, const GridPos& gp) {
   constexpr int H = W / 2;
@@ -421,7 +426,24 @@ __device__ __forceinline__ void comb_ip_body(const CombIPArgs& a, uint64_t* lds,
   const int item = gp.item;
   const uint64_t q = pc.q;
   uint64_t acc[2][W];
-  ip_accumulate<LOGB, LOGN, AR, W>(a.ip, lds, twl, pc, i, gp, acc[0], acc[1]);
+  if constexpr (STORED) {
+    int col, base;
+    ip_item<IPRounds<LOGB, W>::RW, LOGB, W>(0, 0, col, base);
+    const uint32_t h0 = ip_word<LOGB, W>(gp.tile, base, col) >> 1;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const ulonglong2* src = reinterpret_cast<const ulonglong2*>(
+          a.acc + item * a.acc_bstride + ((uint64_t)(c * a.acc_comp_limbs + i) << log_n));
+#pragma unroll
+      for (int r = 0; r < H; ++r) {
+        const ulonglong2 v = at_u32(src, h0 + r);
+        acc[c][2 * r] = v.x;
+        acc[c][2 * r + 1] = v.y;
+      }
+    }
+  } else {
+    ip_accumulate<LOGB, LOGN, AR, W>(a.ip, lds, twl, pc, i, gp, acc[0], acc[1]);
+  }
   const uint64_t cw = a.pinv64[2 * i], cwp = a.pinv64[2 * i + 1];
   // Lazy primes in (2^33, 2^56): the row pass leaves NTT(w) below 65q < 2^63,
   // which reduce_hi takes to [0, 2q); with acc*P^-1 in [0, 4q) and canonical
@@ -491,7 +513,9 @@ __device__ __forceinline__ void comb_ip_body(const CombIPArgs& a, uint64_t* lds,
   }
 }
 
-template <int LOGB, int LOGN, int W = 8>
+// STORED: the accumulators come from memory (hoisted rotations and sums, whose
+// inner product gathers across tiles) and the kernel is the last pass alone.
+template <int LOGB, int LOGN, int W = 8, bool STORED = false>
 __global__ __launch_bounds__((IPRounds<LOGB, W>::THREADS)) __attribute__((amdgpu_waves_per_eu(W == 8 ? 2 : (LOGN ? 4 : 3)))) void comb_ip_kernel(
     CombIPArgs a) {
   __shared__ uint64_t lds[(1 << LOGB) * IPRounds<LOGB, W>::KC];
@@ -508,11 +532,11 @@ __global__ __launch_bounds__((IPRounds<LOGB, W>::THREADS)) __attribute__((amdgpu
     if (gp.item >= a.ip.n_items) break;
     const int far = fwd_ar(pc.q);
     if (far == AR_LAZY)
-      comb_ip_body<LOGB, LOGN, AR_LAZY, W>(a, lds, twl, pc, i, gp);
+      comb_ip_body<LOGB, LOGN, AR_LAZY, W, STORED>(a, lds, twl, pc, i, gp);
     else if (far == AR_HARVEY)
-      comb_ip_body<LOGB, LOGN, AR_HARVEY, W>(a, lds, twl, pc, i, gp);
+      comb_ip_body<LOGB, LOGN, AR_HARVEY, W, STORED>(a, lds, twl, pc, i, gp);
     else
-      comb_ip_body<LOGB, LOGN, AR_STRICT, W>(a, lds, twl, pc, i, gp);
+      comb_ip_body<LOGB, LOGN, AR_STRICT, W, STORED>(a, lds, twl, pc, i, gp);
   }
 }
 
@@ -522,86 +546,16 @@ typedef void (*CombIPFn)(CombIPArgs);
 // SIMD for N = 2^16, measured faster than 8 at 2 waves.
 constexpr int kCombW = 4;
 
+template <bool STORED>
 CombIPFn pick_comb_ip(int log_n, int logb) {
-  if (log_n == 16 && logb == 8) return comb_ip_kernel<8, 16, kCombW>;
+  if (log_n == 16 && logb == 8) return comb_ip_kernel<8, 16, kCombW, STORED>;
   switch (logb) {
-    case 5: return comb_ip_kernel<5, 0, kCombW>;
-    case 6: return comb_ip_kernel<6, 0, kCombW>;
-    case 7: return comb_ip_kernel<7, 0, kCombW>;
-    case 8: return comb_ip_kernel<8, 0, kCombW>;
+    case 5: return comb_ip_kernel<5, 0, kCombW, STORED>;
+    case 6: return comb_ip_kernel<6, 0, kCombW, STORED>;
+    case 7: return comb_ip_kernel<7, 0, kCombW, STORED>;
+    case 8: return comb_ip_kernel<8, 0, kCombW, STORED>;
   }
   return nullptr;
-}
-
-// ---------------------------------------------------------------------------
-// I: forward row pass storing acc*P^-1 - v (+ gathered add) (+ accum)
-struct CombineOps {
-  uint64_t acc, add, accum;
-};
-
-struct CombineIO {
-  typedef CombineOps Ops;
-  const uint64_t* w;      // lazy column-pass output
-  const uint64_t* acc;    // accumulator limb (NTT form)
-  const uint64_t* add;    // or NULL
-  const uint64_t* accum;  // or NULL
-  uint64_t* out;
-  uint64_t pinv, pinvp, q;
-  uint32_t g;
-  int log_n;
-  __device__ __forceinline__ uint64_t load(uint32_t j) const { return w[j]; }
-  __device__ __forceinline__ void after_load(uint32_t, uint64_t) const {}
-  __device__ __forceinline__ Ops fetch(uint32_t j) const {
-    Ops o;
-    o.acc = acc[j];
-    o.add = add ? add[g ? automorph_src(j, g, log_n) : j] : 0;
-    o.accum = accum ? accum[j] : 0;
-    return o;
-  }
-  __device__ __forceinline__ void store(uint32_t j, uint64_t v, const Ops& o) const {
-    uint64_t r = sub_mod(reduce_4q(mul_shoup_lazy(o.acc, pinv, pinvp, q), q), v, q);
-    r = add_mod(r, o.add, q);
-    r = add_mod(r, o.accum, q);
-    out[j] = r;
-  }
-};
-
-struct CombinePassArgs {
-  const uint64_t* w;    // item b: w + b*w_bstride, [2][nq][N]
-  const uint64_t* acc;  // item b: acc + b*acc_bstride, [2][next][N]
-  const uint64_t* add[2];
-  const uint64_t* accum;
-  uint64_t* out;
-  uint64_t w_bstride, acc_bstride, add_bstride, accum_bstride, out_bstride;
-  const uint64_t* pinv;  // [L][2]
-  const uint64_t* tw;
-  const PrimeConst* prime;
-  uint32_t g[kMaxChunk];
-  int log_n, nq, next, out_comp_limbs;
-};
-
-template <int RA, int RB, int LOGN>
-__global__ __launch_bounds__(kThreads) void ntt_row_combine_kernel(CombinePassArgs a) {
-  constexpr int ROWS = 1 << (RA + RB);
-  __shared__ uint64_t lds[lds_words<false, RB, ROWS>()];
-  const GridPos gp = row_grid_pos();
-  const int job = gp.job, item = gp.item;  // job = comp * nq + i
-  const int comp = job / a.nq, i = job % a.nq;
-  const PrimeConst& pc = a.prime[i];
-  CombineIO io;
-  io.w = a.w + item * a.w_bstride + ((uint64_t)job << a.log_n);
-  io.acc = a.acc + item * a.acc_bstride + ((uint64_t)(comp * a.next + i) << a.log_n);
-  io.add = a.add[comp] ? a.add[comp] + item * a.add_bstride + ((uint64_t)i << a.log_n) : nullptr;
-  io.accum = a.accum ? a.accum + item * a.accum_bstride + ((uint64_t)job << a.log_n) : nullptr;
-  io.out = a.out + item * a.out_bstride + ((uint64_t)(comp * a.out_comp_limbs + i) << a.log_n);
-  io.pinv = a.pinv[2 * i];
-  io.pinvp = a.pinv[2 * i + 1];
-  io.q = pc.q;
-  io.g = a.g[item];
-  io.log_n = a.log_n;
-  Finish fin{1, 0, 0, pc.inv1};
-  run_pass<RA, RB, false, false, LOGN>(io, lds, gp.tile, a.log_n, a.tw + ((uint64_t)i << (a.log_n + 1)), pc.q,
-                                       fin);
 }
 
 // ---------------------------------------------------------------------------
@@ -821,6 +775,39 @@ int moddown_steps(Ctx* c, hipStream_t s, int level, int n_items, uint64_t* A, ui
 
 }  // namespace
 
+// Items a workgroup of the inner products runs one after another: two share
+// the staged twiddles; one when all of them fit the chip at once (`slots`
+// workgroups): 24 against 36 us for ip_special, 17 against 26 us for comb_ip on
+// 32 items of 7 + 3 limbs at N = 2^12, while 1.5 rounds of single items lose
+// 2 us to one round of pairs on 2 items of 12 limbs at N = 2^16.
+static int ip_items(uint32_t tiles, int limbs, int n_items, uint32_t slots) {
+  return (uint64_t)tiles * limbs * n_items <= slots ? 1 : 2;
+}
+constexpr uint32_t kSpecialSlots = 512, kCombSlots = 1024;  // 2 and 4 workgroups on each of 256 CUs
+
+// Step I on the ciphertext limbs 0..n_limb-1.
+static int launch_comb_ip(Ctx* c, hipStream_t s, CombIPArgs& ca, int n_limb) {
+  const uint32_t N = c->N;
+  const int log_n = (int)c->log_n, lr = logb_row(log_n), level = ca.ip.level;
+  CombIPFn fn = ca.acc ? pick_comb_ip<true>(log_n, lr) : pick_comb_ip<false>(log_n, lr);
+  if (!fn) return set_error(CKKS_EINTERNAL, "unsupported NTT pass size");
+  double units = (double)n_limb * 2 * ((double)(N / 2) * lr + N);
+  if (!ca.acc) {
+    for (int j = 0; j < ca.ip.beta; ++j) {
+      const int na = c->modup[level][j].hi - c->modup[level][j].lo;
+      units += (double)std::max(0, n_limb - na) * (N / 2) * lr;  // row passes of the converted ciphertext limbs
+    }
+    units += (double)n_limb * N * (2.0 * ca.ip.beta + 2);
+  }
+  TraceScope ts(c, s, ca.acc ? "ntt_row_combine" : "comb_ip", units * ca.ip.n_items);
+  const int logkc = ip_logkc(lr, kCombW);
+  const int items = ca.ip.items_per_wg = ip_items(N >> (lr + logkc), n_limb, ca.ip.n_items, kCombSlots);
+  hipLaunchKernelGGL(fn, dim3(N >> (lr + logkc), n_limb, (ca.ip.n_items + items - 1) / items),
+                     dim3((1u << (lr + logkc)) / kCombW), 0, s, ca);
+  CKKS_HIP_CHECK(hipGetLastError());
+  return CKKS_OK;
+}
+
 // Steps F to I for n_items accumulators A (item i at A + i*per, [2][next][N]
 // NTT form) with W as the ModDown scratch: out = ModDown(acc) (+ add, gathered
 // through add_g) (+ accum).
@@ -829,7 +816,6 @@ int ks_back(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uin
   const uint32_t N = c->N;
   const int log_n = (int)c->log_n;
   const int nq = level + 1, next = nq + (int)c->K;
-  const int lr = logb_row(log_n);
   int rc;
   // F, G: inverse NTT of the special limbs, times [phat_k^-1 N^-1]: y_k
   {
@@ -865,34 +851,29 @@ int ks_back(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uin
     if ((rc = ntt_pass_only(c, s, W, W, per, per, n_items, jobs, false, true, 0, nullptr, nullptr))) return rc;
   }
   // I: forward row pass with the final combination
-  {
-    CombinePassArgs ca;
-    memset(&ca, 0, sizeof(ca));
-    ca.w = W;
-    ca.w_bstride = per;
-    ca.acc = A;
-    ca.acc_bstride = per;
-    ca.add[0] = it[0].add[0];
-    ca.add[1] = it[0].add[1];
-    ca.add_bstride = add_stride;
-    ca.accum = it[0].accum;
-    ca.accum_bstride = accum_stride;
-    ca.out = it[0].out;
-    ca.out_bstride = out_stride;
-    ca.pinv = c->d_moddown + c->md.pinv;
-    ca.tw = c->d_tw_fwd;
-    ca.prime = c->d_prime;
-    for (int i = 0; i < n_items; ++i) ca.g[i] = it[i].add_g;
-    ca.log_n = log_n;
-    ca.nq = nq;
-    ca.next = next;
-    ca.out_comp_limbs = out_comp_limbs;
-    auto fn = CKKS_PICK_PASS(ntt_row_combine_kernel, log_n, lr);
-    TraceScope ts(c, s, "ntt_row_combine", (double)n_items * 2 * nq * ((double)(N / 2) * lr + N));
-    hipLaunchKernelGGL(fn, dim3(pass_tiles(N, lr), 2 * nq, n_items), dim3(kThreads), 0, s, ca);
-    CKKS_HIP_CHECK(hipGetLastError());
-  }
-  return CKKS_OK;
+  CombIPArgs ca;
+  memset(&ca, 0, sizeof(ca));
+  ca.ip.tw = c->d_tw_fwd;
+  ca.ip.prime = c->d_prime;
+  ca.ip.log_n = log_n;
+  ca.ip.level = level;
+  ca.ip.n_items = n_items;
+  ca.acc = A;
+  ca.acc_bstride = per;
+  ca.acc_comp_limbs = next;
+  ca.W = W;
+  ca.W_bstride = per;
+  ca.add[0] = it[0].add[0];
+  ca.add[1] = it[0].add[1];
+  ca.add_bstride = add_stride;
+  for (int i = 0; i < n_items; ++i) ca.add_g[i] = it[i].add_g;
+  ca.accum = it[0].accum;
+  ca.accum_bstride = accum_stride;
+  ca.out = it[0].out;
+  ca.out_bstride = out_stride;
+  ca.out_comp_limbs = out_comp_limbs;
+  ca.pinv64 = c->d_moddown + c->md.pinv;
+  return launch_comb_ip(c, s, ca, nq);
 }
 
 // Workspace of the fused pipeline per item: Y [nq] (inverse row pass of the
@@ -1066,7 +1047,6 @@ static int ks_raise(Ctx* c, hipStream_t s, int level, int n_items, const KSItem*
   ip->alpha = (int)c->alpha;
   ip->L = (int)c->L;
   ip->K = (int)c->K;
-  ip->items_per_wg = 2;
   ip->n_items = n_items;
   return CKKS_OK;
 }
@@ -1086,28 +1066,9 @@ static int launch_ip_special(Ctx* c, hipStream_t s, const RowIPArgs& ip, uint64_
   const double units = (double)targets * ((double)ip.beta * (N / 2) * lr + N * (2.0 * ip.beta + 2) + 2.0 * (N / 2) * lr);
   TraceScope ts(c, s, "ip_special", units * ip.n_items);
   const int logkc = ip_logkc(lr, kSpecialW);
-  hipLaunchKernelGGL(fn, dim3(N >> (lr + logkc), targets, (ip.n_items + 1) / 2), dim3((1u << (lr + logkc)) / kSpecialW),
-                     0, s, sp, c->d_tw_inv, top);
-  CKKS_HIP_CHECK(hipGetLastError());
-  return CKKS_OK;
-}
-
-// Step I on the ciphertext limbs 0..n_limb-1.
-static int launch_comb_ip(Ctx* c, hipStream_t s, const CombIPArgs& ca, int n_limb) {
-  const uint32_t N = c->N;
-  const int log_n = (int)c->log_n, lr = logb_row(log_n), level = ca.ip.level;
-  CombIPFn fn = pick_comb_ip(log_n, lr);
-  if (!fn) return set_error(CKKS_EINTERNAL, "unsupported NTT pass size");
-  double units = 0;
-  for (int j = 0; j < ca.ip.beta; ++j) {
-    const int na = c->modup[level][j].hi - c->modup[level][j].lo;
-    units += (double)std::max(0, n_limb - na) * (N / 2) * lr;  // row passes of the converted ciphertext limbs
-  }
-  units += (double)n_limb * (N * (2.0 * ca.ip.beta + 2) + 2.0 * ((N / 2) * lr + N));
-  TraceScope ts(c, s, "comb_ip", units * ca.ip.n_items);
-  const int logkc = ip_logkc(lr, kCombW);
-  hipLaunchKernelGGL(fn, dim3(N >> (lr + logkc), n_limb, (ca.ip.n_items + 1) / 2), dim3((1u << (lr + logkc)) / kCombW),
-                     0, s, ca);
+  sp.items_per_wg = ip_items(N >> (lr + logkc), targets, ip.n_items, kSpecialSlots);
+  hipLaunchKernelGGL(fn, dim3(N >> (lr + logkc), targets, (ip.n_items + sp.items_per_wg - 1) / sp.items_per_wg),
+                     dim3((1u << (lr + logkc)) / kSpecialW), 0, s, sp, c->d_tw_inv, top);
   CKKS_HIP_CHECK(hipGetLastError());
   return CKKS_OK;
 }

@@ -153,20 +153,25 @@ __global__ __launch_bounds__(256) void drop_values_kernel(DropArgs a) {
 }
 
 // Column-pass input: (w + v) q_l^-1 computed on load, for DROP 2 then
-// (that + v') q_(l-1)^-1.  w is congruent, below 6q (below q for primes above
-// 2^60), so the sums stay below 2^63.
+// (that + v') q_(l-1)^-1, v and v' centred: a dropped word above half its prime
+// q_l gets -q_l mod q added and needs no reduction, since the Shoup product
+// takes any 64-bit word.  w is congruent, below 6q (below q for primes above
+// 2^60), a product below 2q, so the sums stay below 8 * 2^60 or 2^64.  The
+// result is left below 2q, as the first butterflies take it.
 template <int DROP>
 struct DropIO {
   typedef NoOps Ops;
   uint64_t* w;
   const uint64_t* v[DROP];
-  uint64_t q, inv1, qinv[DROP], qinvp[DROP], qlmod[DROP], half[DROP];
+  uint64_t q, qinv[DROP], qinvp[DROP], neg[DROP], half[DROP];
   __device__ __forceinline__ uint64_t load(uint32_t j) const {
     uint64_t x = w[j];
 #pragma unroll
-    for (int d = 0; d < DROP; ++d)
-      x = mul_shoup(x + lift_mod(v[d][j], half[d], qlmod[d], q, inv1), qinv[d], qinvp[d], q);
-    return reduce_2q(x, q);
+    for (int d = 0; d < DROP; ++d) {
+      const uint64_t y = v[d][j];
+      x = mul_shoup(x + y + (y > half[d] ? neg[d] : 0), qinv[d], qinvp[d], q);
+    }
+    return x;
   }
   __device__ __forceinline__ void after_load(uint32_t, uint64_t) const {}
   __device__ __forceinline__ Ops fetch(uint32_t) const { return Ops(); }
@@ -188,11 +193,10 @@ __global__ __launch_bounds__(kThreads) void drop_col_kernel(DropArgs a) {
     io.v[d] = a.A + blockIdx.z * a.per + ((uint64_t)(comp * a.comp_limbs + DROP - 1 - d) << a.log_n);
     io.qinv[d] = rs[0];
     io.qinvp[d] = rs[1];
-    io.qlmod[d] = rs[2];
+    io.neg[d] = pc.q - rs[2];
     io.half[d] = (a.prime[a.level - d].q - 1) / 2;
   }
   io.q = pc.q;
-  io.inv1 = pc.inv1;
   Finish fin{0, 0, 0, pc.inv1};
   run_pass<RA, RB, false, true, LOGN>(io, lds, blockIdx.x, a.log_n, a.tw + ((uint64_t)i << (a.log_n + 1)), pc.q,
                                       fin);

@@ -344,6 +344,40 @@ def test_blocks_of_items_and_tokens(lib, orc, sets):
     assert torch.equal(first, y2)
 
 
+def test_small_blocks(lib, orc, sets, monkeypatch):
+    """Intermediates limited to 1 MiB: every call runs in blocks of one or two items, a chunk's tokens in
+    several blocks that carry the prefix sums, its groups in several blocks whose outputs interleave."""
+    monkeypatch.setenv("CKKS_BLOCK_MB", "1")
+    ctx, P = sets("small")
+    announce("small blocks")
+    st, ref_st = steps(lib, P, [2])
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    for T, G, R in [(5, 1, 1), (4, 5, 2), (40, 1, 1)]:
+        d = chunk_case(P, 5, T, G, R, T < 6, False, True, 30 + T)
+        y, out = run_chunk(lib, ctx, P, d, 5, T, G, R, rlk, st)
+        ref = orc.linattn_chunk(P, 5, d["q"], d["k"], d["v"], d["w"], d["r"], None, d["state"], rlk, *ref_st)
+        same(y, ref[0], "y %d %d" % (T, G))
+        same(out, ref[1], "state %d %d" % (T, G))
+    a, v, m = words(P, 8, "a", 6, (2, 3, 2, 2)), words(P, 8, "v", 6, (2, 2, 2)), words(P, 8, "m", 6, (2, 2))
+    num, den = empty_dev((2, 3, 2, 4, P.N)), empty_dev((2, 3, 2, 5, P.N))
+    lib.ckks_attn_mix(ctx, to_dev(a), 3, to_dev(v), 2, 2, to_dev(m), 2, 5, d_rlk, st, num, den)
+    ref = orc.attn_mix(P, 5, a, v, m, rlk, *ref_st)
+    same(num, ref[0])
+    same(den, ref[1])
+    s = empty_dev((2, 3, 2, 2, 5, P.N))
+    lib.ckks_attn_scores(ctx, to_dev(a[:, :, 0]), 3, to_dev(v), 2, 2, 5, d_rlk, st, s)
+    same(s, orc.attn_scores(P, 5, a[:, :, 0], v, rlk, *ref_st))
+    q, k, w = (words(P, 9, x, 6, (7, 2)) for x in "qkv")
+    for R in (0, 3):
+        dec, s_in = (words(P, 9, "dec", 6, (R,)), words(P, 9, "st", 6, (7, 2))) if R else (None, words(P, 9, "st", 5, (7, 2)))
+        y, out = empty_dev((7, 2, 4, P.N)), empty_dev((7, 2, 5, P.N))
+        lib.ckks_linattn_step(ctx, to_dev(q), to_dev(k), to_dev(w), 7, dev(dec), R, to_dev(s_in), 5, d_rlk, st, y, out)
+        ref = orc.linattn_step(P, 5, q, k, w, dec, s_in, rlk, *ref_st)
+        same(y, ref[0])
+        same(out, ref[1])
+
+
 def test_on_another_stream(lib, orc, sets):
     """A side stream, while the default stream is busy: the call waits for nothing but its own stream."""
     torch = torch_cuda()
