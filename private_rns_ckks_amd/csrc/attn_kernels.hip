@@ -9,8 +9,14 @@ namespace ckks {
 
 namespace {
 
-constexpr int kAhead = 4;      // terms of a sum whose words load together
 constexpr int kSegments = 16;  // token segments of the segmented scan
+// The scan runs in segments below this many words (groups x limbs x N) and
+// from kSegments tokens on: one thread a word then leaves most of the chip
+// empty, while the segments' second pass over the output costs a full chip
+// more.  Scan and state product of 96 tokens of 2^14.8 words: 92 us in
+// segments, 206 us without; 32 tokens of 2^16.2: 87 and 98; of 2^17.2: 159 and
+// 141; 16 tokens of 2^20.6: 910 and 563.
+constexpr uint64_t kSegmentWords = 3u << 15;
 
 template <bool WIDE>
 __device__ __forceinline__ uint64_t mul_red(const Split<WIDE>& x, const Split<WIDE>& y, const RedConst& pc) {
@@ -78,12 +84,10 @@ __global__ __launch_bounds__(256) void pair_kernel(PairArgs a) {
   d[2 * lim] = acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1);
 }
 
-// r += (w k) x v, three parts.
+// r += (a0, a1) x (v0, v1), three parts.
 template <bool WIDE>
-__device__ __forceinline__ void weigh_add(const Split<WIDE>& w, uint64_t k0, uint64_t k1, uint64_t v0, uint64_t v1,
-                                          const RedConst& pc, uint64_t& r0, uint64_t& r1, uint64_t& r2) {
-  const Split<WIDE> a0 = split_word<WIDE>(mul_red<WIDE>(w, split_word<WIDE>(k0), pc));
-  const Split<WIDE> a1 = split_word<WIDE>(mul_red<WIDE>(w, split_word<WIDE>(k1), pc));
+__device__ __forceinline__ void tensor_add(const Split<WIDE>& a0, const Split<WIDE>& a1, uint64_t v0, uint64_t v1,
+                                           const RedConst& pc, uint64_t& r0, uint64_t& r1, uint64_t& r2) {
   const Split<WIDE> b0 = split_word<WIDE>(v0), b1 = split_word<WIDE>(v1);
   AccT<WIDE> m0{}, m1{}, m2{};
   acc_mac<WIDE>(m0, a0, b0);
@@ -93,6 +97,14 @@ __device__ __forceinline__ void weigh_add(const Split<WIDE>& w, uint64_t k0, uin
   r0 = add_mod(r0, acc_reduce<WIDE>(m0, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
   r1 = add_mod(r1, acc_reduce<WIDE>(m1, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
   r2 = add_mod(r2, acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+}
+
+// r += (w k) x v.
+template <bool WIDE>
+__device__ __forceinline__ void weigh_add(const Split<WIDE>& w, uint64_t k0, uint64_t k1, uint64_t v0, uint64_t v1,
+                                          const RedConst& pc, uint64_t& r0, uint64_t& r1, uint64_t& r2) {
+  tensor_add<WIDE>(split_word<WIDE>(mul_red<WIDE>(w, split_word<WIDE>(k0), pc)),
+                   split_word<WIDE>(mul_red<WIDE>(w, split_word<WIDE>(k1), pc)), v0, v1, pc, r0, r1, r2);
 }
 
 template <bool WIDE>
@@ -111,30 +123,15 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a) {
   }
   const uint64_t low = (uint64_t)(a.nl - a.drop.drop) << a.log_n;
   const uint64_t* add = a.add ? a.add + (uint64_t)g * 2 * low : nullptr;
-  // the words of kAhead tokens load together: with few groups there are too
-  // few waves to hide a load per token
-  for (int t0 = 0; t0 < a.n_tok; t0 += kAhead) {
-    uint64_t x[kAhead][5];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int t = min(t0 + u, a.n_tok - 1);
-      const uint64_t* k = a.k + t * a.tok_stride + (uint64_t)g * 2 * lim + off;
-      const uint64_t* v = a.v + t * a.tok_stride + (uint64_t)g * 2 * lim + off;
-      x[u][0] = a.w[((uint64_t)t * a.n_row + row) * lim + off];
-      x[u][1] = k[0];
-      x[u][2] = k[lim];
-      x[u][3] = v[0];
-      x[u][4] = v[lim];
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (t0 + u >= a.n_tok) break;
-      weigh_add<WIDE>(split_word<WIDE>(x[u][0]), x[u][1], x[u][2], x[u][3], x[u][4], pc, r0, r1, r2);
-      uint64_t* o = a.out + ((uint64_t)(t0 + u) * a.n_grp + g) * 3 * lim + off;
-      o[0] = drop_out(r0, a.drop, a.nl, i, add, off, pc.q);
-      o[lim] = drop_out(r1, a.drop, a.nl, i, add, low + off, pc.q);
-      o[2 * lim] = r2;
-    }
+  for (int t = 0; t < a.n_tok; ++t) {
+    const uint64_t* k = a.k + t * a.tok_stride + (uint64_t)g * 2 * lim + off;
+    const uint64_t* v = a.v + t * a.tok_stride + (uint64_t)g * 2 * lim + off;
+    const Split<WIDE> w = split_word<WIDE>(a.w[((uint64_t)t * a.n_row + row) * lim + off]);
+    weigh_add<WIDE>(w, k[0], k[lim], v[0], v[lim], pc, r0, r1, r2);
+    uint64_t* o = a.out + ((uint64_t)t * a.n_grp + g) * 3 * lim + off;
+    o[0] = drop_out(r0, a.drop, a.nl, i, add, off, pc.q);
+    o[lim] = drop_out(r1, a.drop, a.nl, i, add, low + off, pc.q);
+    o[2 * lim] = r2;
   }
   if (a.last) {
     uint64_t* o = a.last + (uint64_t)g * 3 * lim + off;
@@ -211,41 +208,18 @@ __global__ __launch_bounds__(256) void mix_kernel(MixArgs a) {
   const RedConst pc = red_const((ConstPrime)a.prime, i);
   const uint64_t off = ((uint64_t)i << a.log_n) + c, lim = (uint64_t)a.nl << a.log_n;
   uint64_t r0 = 0, r1 = 0, r2 = 0, e0 = 0, e1 = 0;
-  for (int j0 = 0; j0 < a.n_k; j0 += kAhead) {
-    uint64_t w[kAhead][5];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int j = min(j0 + u, a.n_k - 1);
-      const uint64_t* x = a.a + ((uint64_t)row * a.n_k + j) * 2 * lim + off;
-      const uint64_t* v = a.v + ((uint64_t)g * a.n_k + j) * 2 * lim + off;
-      w[u][0] = a.m ? a.m[((uint64_t)(g % a.n_row) * a.n_k + j) * lim + off] : 0;
-      w[u][1] = x[0];
-      w[u][2] = x[lim];
-      w[u][3] = v[0];
-      w[u][4] = v[lim];
+  for (int j = 0; j < a.n_k; ++j) {
+    const uint64_t* x = a.a + ((uint64_t)row * a.n_k + j) * 2 * lim + off;
+    const uint64_t* v = a.v + ((uint64_t)g * a.n_k + j) * 2 * lim + off;
+    uint64_t a0 = x[0], a1 = x[lim];
+    if (a.m) {
+      const Split<WIDE> m = split_word<WIDE>(a.m[((uint64_t)(g % a.n_row) * a.n_k + j) * lim + off]);
+      a0 = mul_red<WIDE>(m, split_word<WIDE>(a0), pc);
+      a1 = mul_red<WIDE>(m, split_word<WIDE>(a1), pc);
     }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (j0 + u >= a.n_k) break;
-      uint64_t a0 = w[u][1], a1 = w[u][2];
-      if (a.m) {
-        const Split<WIDE> m = split_word<WIDE>(w[u][0]);
-        a0 = mul_red<WIDE>(m, split_word<WIDE>(a0), pc);
-        a1 = mul_red<WIDE>(m, split_word<WIDE>(a1), pc);
-      }
-      e0 = add_mod(e0, a0, pc.q);
-      e1 = add_mod(e1, a1, pc.q);
-      const Split<WIDE> s0 = split_word<WIDE>(a0), s1 = split_word<WIDE>(a1);
-      const Split<WIDE> v0 = split_word<WIDE>(w[u][3]), v1 = split_word<WIDE>(w[u][4]);
-      AccT<WIDE> m0{}, m1{}, m2{};
-      acc_mac<WIDE>(m0, s0, v0);
-      acc_mac<WIDE>(m1, s0, v1);
-      acc_mac<WIDE>(m1, s1, v0);
-      acc_mac<WIDE>(m2, s1, v1);
-      r0 = add_mod(r0, acc_reduce<WIDE>(m0, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
-      r1 = add_mod(r1, acc_reduce<WIDE>(m1, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
-      r2 = add_mod(r2, acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
-    }
+    e0 = add_mod(e0, a0, pc.q);
+    e1 = add_mod(e1, a1, pc.q);
+    tensor_add<WIDE>(split_word<WIDE>(a0), split_word<WIDE>(a1), v[0], v[lim], pc, r0, r1, r2);
   }
   uint64_t* o = a.num + (uint64_t)b * 3 * lim + off;
   o[0] = drop_out(r0, a.drop, a.nl, i, nullptr, 0, pc.q);
@@ -277,10 +251,7 @@ int launch_pair(Ctx* c, hipStream_t s, const PairArgs& a, int batch) {
 
 int launch_scan(Ctx* c, hipStream_t s, const ScanArgs& a) {
   TraceScope ts(c, s, "attn_mac", (double)a.n_tok * a.n_grp * a.nl * 11 * c->N);
-  // segments when one thread a word fills less than a quarter of the chip
-  // (256 CUs x 2048 threads) and there are tokens for all of them: 96 tokens of
-  // 7 limbs at N = 2^12 take 64 us, 151 us with one thread a word
-  if ((uint64_t)a.n_grp * a.nl * c->N < (1u << 17) && a.n_tok >= kSegments) {
+  if ((uint64_t)a.n_grp * a.nl * c->N < kSegmentWords && a.n_tok >= kSegments) {
     hipLaunchKernelGGL(c->wide ? scan_segments_kernel<true> : scan_segments_kernel<false>, dim3(c->N / 64, a.nl, a.n_grp),
                        dim3(64, kSegments), 0, s, a);
     CKKS_HIP_CHECK(hipGetLastError());

@@ -74,6 +74,24 @@ __device__ __forceinline__ uint64_t cols_reduce(const Cols<SH>& A, uint64_t q, u
   return reduce128_6q(r, q, r64, r64p, inv1);
 }
 
+// 16-byte accesses, NT: non-temporal, so that words used once do not push the
+// digits out of L2.
+typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+template <bool NT>
+__device__ __forceinline__ ulonglong2 load_pair(const uint64_t* limb, uint32_t w0) {
+  if constexpr (NT) {
+    const u64x2 v = __builtin_nontemporal_load(&at_u32(reinterpret_cast<const u64x2*>(limb), w0 >> 1));
+    return make_ulonglong2(v.x, v.y);
+  } else {
+    return at_u32(reinterpret_cast<const ulonglong2*>(limb), w0 >> 1);
+  }
+}
+template <bool NT>
+__device__ __forceinline__ void store_pair(uint64_t* limb, uint32_t w0, uint64_t x, uint64_t y) {
+  if constexpr (NT) __builtin_nontemporal_store((u64x2){x, y}, &at_u32(reinterpret_cast<u64x2*>(limb), w0 >> 1));
+  else at_u32(reinterpret_cast<ulonglong2*>(limb), w0 >> 1) = make_ulonglong2(x, y);
+}
+
 // One (digit, rotation) of the inner product: a key word pair per component
 // and every item's digit words, in flight while the previous one is computed.
 template <int I>
@@ -93,7 +111,7 @@ struct SumTerm {
 // order onto an aligned pair, perhaps swapped, so a gather is one 16-byte load.
 // Digits are the outer loop: the I limbs of one digit (I * 512 KB at N = 2^16)
 // stay in an XCD's L2 while the rotations gather from them.
-template <int I, int SH>
+template <int I, int SH, bool NT>
 __device__ __forceinline__ void sum_ip_narrow(const SumIPArgs& a, const PrimeConst& pc, int t, int keyl, int item0,
                                               uint32_t w0) {
   const int log_n = a.log_n;
@@ -107,8 +125,8 @@ __device__ __forceinline__ void sum_ip_narrow(const SumIPArgs& a, const PrimeCon
     const uint32_t src = automorph_src(w0, a.g[r], log_n);
     s.swap = src & 1;
     const uint64_t* kb = a.evk[r] + (uint64_t)(2 * j) * LKN + koff;
-    s.kb = at_u32(reinterpret_cast<const ulonglong2*>(kb), w0 >> 1);
-    s.ka = at_u32(reinterpret_cast<const ulonglong2*>(kb + LKN), w0 >> 1);
+    s.kb = load_pair<NT>(kb, w0);
+    s.ka = load_pair<NT>(kb + LKN, w0);
     const bool own = t >= j * a.alpha && t < (j + 1) * a.alpha && t <= a.level;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
@@ -194,15 +212,20 @@ __device__ __forceinline__ void sum_ip_narrow(const SumIPArgs& a, const PrimeCon
       v[e] = cols_reduce<SH>(A[i][e >> 1][e & 1], q, pc.r64, pc.r64p, inv1);
       if (v[e] >= cut) v[e] -= 4 * q;
     }
-    at_u32(reinterpret_cast<ulonglong2*>(ob), w0 >> 1) = make_ulonglong2(v[0] + s0[i], v[1] + s1[i]);
-    at_u32(reinterpret_cast<ulonglong2*>(oa), w0 >> 1) = make_ulonglong2(v[2], v[3]);
+    store_pair<NT>(ob, w0, v[0] + s0[i], v[1] + s1[i]);
+    store_pair<NT>(oa, w0, v[2], v[3]);
   }
 }
 
 // Primes below 2^60.  The grid is (tiles of 512 words, target limbs, groups of
 // I items), groups fastest: the groups of one tile run together on one XCD
-// and share its key words in L2.
-template <int I>
+// and share its key words in L2.  With one group (ONE) a key word is used once,
+// and keys and results bypass L2's replacement: 262 -> 235 us for 4 items,
+// radix 8, N = 2^16, level 22, where the keys' 0.68 GB and the digits' and
+// results' 0.36 GB move at 4.5 TB/s; with two groups that loses 2 %.  Three or
+// four waves a SIMD, one or two words a thread and up to 8 items a thread take
+// the same time or more: the kernel is held by memory.
+template <int I, bool ONE>
 __global__ __launch_bounds__(256) void sum_ip_kernel(SumIPArgs a) {
   const nttc::GridPos gp = nttc::row_grid_pos<true>();
   const int t = gp.job;
@@ -210,9 +233,9 @@ __global__ __launch_bounds__(256) void sum_ip_kernel(SumIPArgs a) {
   const PrimeConst& pc = a.prime[keyl];
   const uint32_t w0 = (gp.tile * 256 + threadIdx.x) * 2;
   if (pc.q < (1ull << 54))
-    sum_ip_narrow<I, 27>(a, pc, t, keyl, gp.item * I, w0);
+    sum_ip_narrow<I, 27, ONE>(a, pc, t, keyl, gp.item * I, w0);
   else
-    sum_ip_narrow<I, 30>(a, pc, t, keyl, gp.item * I, w0);
+    sum_ip_narrow<I, 30, ONE>(a, pc, t, keyl, gp.item * I, w0);
 }
 
 // Primes up to 2^62: lazy Montgomery products as in the key switch, one item.
@@ -253,7 +276,7 @@ __global__ __launch_bounds__(256) void sum_ip_wide_kernel(SumIPArgs a) {
 }
 
 // Items a thread of the inner product holds: as many as the launch has, up to
-// 4 (24 accumulator registers an item; 4 leave three waves a SIMD).
+// 4 (24 accumulator registers an item).
 constexpr int kSumHeld = 4;
 
 int launch_sum_ip(Ctx* c, hipStream_t s, const SumIPArgs& a) {
@@ -261,9 +284,13 @@ int launch_sum_ip(Ctx* c, hipStream_t s, const SumIPArgs& a) {
   if (c->wide) {
     hipLaunchKernelGGL(sum_ip_wide_kernel, dim3(c->N / 256, a.next, a.n_items), dim3(256), 0, s, a);
   } else {
+    // even groups: past 4 items they hold 3 or 4
     const int groups = (a.n_items + kSumHeld - 1) / kSumHeld, held = (a.n_items + groups - 1) / groups;
-    auto fn = held == 1 ? sum_ip_kernel<1> : held == 2 ? sum_ip_kernel<2> : held == 3 ? sum_ip_kernel<3>
-                                                                                      : sum_ip_kernel<4>;
+    auto fn = groups > 1 ? (held == 3 ? sum_ip_kernel<3, false> : sum_ip_kernel<4, false>)
+              : held == 1 ? sum_ip_kernel<1, true>
+              : held == 2 ? sum_ip_kernel<2, true>
+              : held == 3 ? sum_ip_kernel<3, true>
+                          : sum_ip_kernel<4, true>;
     hipLaunchKernelGGL(fn, dim3(c->N / 512, a.next, (a.n_items + held - 1) / held), dim3(256), 0, s, a);
   }
   CKKS_HIP_CHECK(hipGetLastError());
