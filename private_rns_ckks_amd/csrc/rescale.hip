@@ -34,17 +34,18 @@ struct RescalePassArgs {
   uint64_t add0[64];  // has_add: added to component 0 of limb i (a constant in NTT form)
 };
 
-// Column-pass input: w_i computed from v on load.
+// Column-pass input: w_i computed from v on load.  A word above half of q_l
+// gets neg = -q_l mod q_i added and needs no reduction (below 2^63), since the
+// Shoup product takes any 64-bit word; its result, below 2q, is what the first
+// butterflies take.
 struct PrepIO {
   typedef NoOps Ops;
   const uint64_t* v;
   uint64_t* dst;
-  uint64_t q, inv1, qinv, qinvp, qlmod, half;
+  uint64_t q, qinv, qinvp, neg, half;
   __device__ __forceinline__ uint64_t load(uint32_t j) const {
     const uint64_t x = v[j];
-    uint64_t t = x >= q ? reduce64(x, q, inv1) : x;
-    if (x > half) t = sub_mod(t, qlmod, q);
-    return reduce_2q(mul_shoup(t, qinv, qinvp, q), q);
+    return mul_shoup(x + (x > half ? neg : 0), qinv, qinvp, q);
   }
   __device__ __forceinline__ void after_load(uint32_t, uint64_t) const {}
   __device__ __forceinline__ Ops fetch(uint32_t) const { return Ops(); }
@@ -63,10 +64,9 @@ __global__ __launch_bounds__(kThreads) void rescale_col_kernel(RescalePassArgs a
   io.v = a.v + item * a.v_bstride + ((uint64_t)comp << a.log_n);
   io.dst = a.w + item * a.w_bstride + ((uint64_t)job << a.log_n);
   io.q = pc.q;
-  io.inv1 = pc.inv1;
   io.qinv = rs[0];
   io.qinvp = rs[1];
-  io.qlmod = rs[2];
+  io.neg = pc.q - rs[2];
   io.half = (a.prime[a.level].q - 1) / 2;
   Finish fin{0, 0, 0, pc.inv1};
   run_pass<RA, RB, false, true, LOGN>(io, lds, blockIdx.x, a.log_n, a.tw + ((uint64_t)i << (a.log_n + 1)), pc.q,
