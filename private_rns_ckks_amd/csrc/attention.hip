@@ -308,7 +308,7 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
   // sums carried from one block of tokens to the next
   const uint64_t mid = 2ull * l * N, per = 3 * lim + (r ? ct + mid : 0) + sct + yct;
   const int gb = block_items(per + 3 * lim + sct, n_grp);
-  const int tb = block_items((per + 3 * lim) * gb, n_tok);
+  const int tb = std::min(block_items((per + 3 * lim) * gb, n_tok), std::max(1, 8192 / gb));  // one launch's items
   const uint64_t nb = (uint64_t)gb * tb;
   if ((rc = ensure_aux(c, per * nb + (3 * lim + sct) * gb))) return rc;
   uint64_t *X = c->aux, *S = X + 3 * lim * nb, *Z = S + sct * nb, *R = Z + yct * nb, *C = R + (r ? ct * nb : 0),
@@ -462,7 +462,7 @@ using namespace ckks;
   try {                                                                         \
     return call;                                                                \
   } catch (const std::exception&) {                                             \
-    return CKKS_ENOMEM;                                                         \
+    return set_error(CKKS_ENOMEM, "out of memory"); /* short: not allocated */  \
   }
 
 extern "C" {

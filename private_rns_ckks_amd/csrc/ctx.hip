@@ -47,7 +47,7 @@ int ensure_workspace(Ctx* c, size_t words) { return grow(c, c->ws, c->ws_words, 
 int ensure_aux(Ctx* c, size_t words) { return grow(c, c->aux, c->aux_words, words, "operand buffer"); }
 
 TraceScope::TraceScope(Ctx* c, hipStream_t s, const char* family, double units)
-    : c_(c), s_(s), on_(!c->no_alloc && !c->trace.name.empty() && c->trace.name == family) {
+    : c_(c), s_(s), on_(!c->no_alloc && !c->capturing && !c->trace.name.empty() && c->trace.name == family) {
   if (!on_) return;
   TraceState& t = c->trace;
   while (t.pool.size() < t.used + 2) {
@@ -109,9 +109,6 @@ static int upload(void** dst, const void* src, size_t bytes) {
 
 int ensure_lanes(Ctx* c) {
   if (c->lane[0]) return CKKS_OK;
-  if (c->capturing)
-    return set_error(CKKS_EHIP, "the internal streams would be created while the stream is being captured: run a call "
-                                "of this size first");
   for (int i = 0; i < Ctx::kMaxLanes; ++i) {
     CKKS_HIP_CHECK(hipStreamCreateWithFlags(&c->lane[i], hipStreamNonBlocking));
     CKKS_HIP_CHECK(hipEventCreateWithFlags(&c->join_ev[i], hipEventDisableTiming));

@@ -81,7 +81,7 @@ struct Ctx {
   // A stream capture has recorded the buffers above: growing keeps the old
   // ones (a graph may replay on them) until the context is destroyed.
   bool captured = false;
-  bool capturing = false;          // the running call's stream is being captured: growing is an error
+  bool capturing = false;          // the running call's stream is being captured: growing is an error, nothing is traced
   std::vector<uint64_t*> retired;
   TraceState trace;
   // Set while an allocation-free call runs: tracing records no events then

@@ -685,6 +685,25 @@ int debug_dump(Ctx* c, hipStream_t s, const char* stage, int n_items, const uint
   return CKKS_OK;
 }
 
+// First (column) or second (row) forward pass of the converted limbs of every
+// digit, E ([beta][next][N] per item), in place.
+int raised_pass(Ctx* c, hipStream_t s, int level, int n_items, uint64_t* E, uint64_t estride, bool first) {
+  const int next = level + 1 + (int)c->K, beta = c->beta(level);
+  NttJobs jobs;
+  for (int j = 0; j < beta; ++j)
+    for (int t = 0; t < next; ++t) {
+      const bool own = t >= c->modup[level][j].lo && t < c->modup[level][j].hi;
+      if (!own) jobs.add(j * next + t, j * next + t, c->ext_prime(level, t));
+      const bool last = j == beta - 1 && t == next - 1;
+      if (jobs.n < kMaxJobs && !last) continue;  // many digits take more jobs than one launch holds
+      if (jobs.n == 0) continue;
+      int rc = ntt_pass_only(c, s, E, E, estride, estride, n_items, jobs, false, first, 0, nullptr, nullptr);
+      if (rc) return rc;
+      jobs.n = 0;
+    }
+  return CKKS_OK;
+}
+
 int modup_steps(Ctx* c, hipStream_t s, int level, int n_items, uint64_t* Y, uint64_t ystride, uint64_t* E,
                 uint64_t estride) {
   const int nq = level + 1, next = nq + (int)c->K, beta = c->beta(level);
@@ -722,13 +741,7 @@ int modup_steps(Ctx* c, hipStream_t s, int level, int n_items, uint64_t* Y, uint
   }
   if ((rc = launch_modup(c, s, mu, beta, n_items))) return rc;
   if ((rc = debug_dump(c, s, "modup_out", n_items, E, estride, (uint64_t)beta * next * c->N))) return rc;
-  NttJobs jobs;
-  for (int j = 0; j < beta; ++j)
-    for (int t = 0; t < next; ++t) {
-      if (t >= c->modup[level][j].lo && t < c->modup[level][j].hi) continue;
-      jobs.add(j * next + t, j * next + t, c->ext_prime(level, t));
-    }
-  return ntt_pass_only(c, s, E, E, estride, estride, n_items, jobs, false, true, 0, nullptr, nullptr);
+  return raised_pass(c, s, level, n_items, E, estride, true);
 }
 
 // ModDown of the special accumulators A (item b at A + b*astride, [2][K][N],
@@ -955,16 +968,8 @@ int ks_decompose(Ctx* c, hipStream_t s, int level, int n_in, const uint64_t* c1,
       mu.offset[j] = en.offset;
     }
     if ((rc = launch_modup(c, s, mu, beta, n_in))) return rc;
-    NttJobs jobs;
-    for (int j = 0; j < beta; ++j)
-      for (int t = 0; t < next; ++t) {
-        if (t >= c->modup[level][j].lo && t < c->modup[level][j].hi) continue;
-        jobs.add(j * next + t, j * next + t, c->ext_prime(level, t));
-      }
-    if ((rc = ntt_pass_only(c, s, E, E, dec_stride, dec_stride, n_in, jobs, false, true, 0, nullptr, nullptr)))
-      return rc;
-    if ((rc = ntt_pass_only(c, s, E, E, dec_stride, dec_stride, n_in, jobs, false, false, 0, nullptr, nullptr)))
-      return rc;
+    if ((rc = raised_pass(c, s, level, n_in, E, dec_stride, true))) return rc;
+    if ((rc = raised_pass(c, s, level, n_in, E, dec_stride, false))) return rc;
   }
   return CKKS_OK;
 }

@@ -5,6 +5,9 @@
 
 namespace ckks {
 
+// Items whose workspace the batched calls of ops.hip hold at once, at most.
+constexpr int kBatchItems = 32;
+
 int check_level(const Ctx* c, int level);
 int check_galois(const Ctx* c, uint32_t g);
 

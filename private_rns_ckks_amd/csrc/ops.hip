@@ -55,8 +55,6 @@ int check_galois(const Ctx* c, uint32_t g) {
   return CKKS_OK;
 }
 
-// Rescale of `batch` items: in [2][level+1][N] at in + b*in_stride -> out
-// [2][level][N], plus acc (same layout as out, may equal it) when given.
 int rescale_batch(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
                   int batch, int level, uint64_t* ws, uint64_t ws_words, const uint64_t* add0, const uint64_t* acc) {
   const uint32_t N = c->N;
@@ -274,7 +272,7 @@ static int rotate_giant_steps(Ctx* c, hipStream_t s, const uint64_t* inner, uint
 
 // Hoisted rotations: input c (at in + c*in_stride, [2][l+1][N]) rotated by
 // g[r] (key evk[r]) into out + c*out_in_stride + r*out_rot_stride.  Inputs are
-// decomposed in groups of up to kMaxChunk on s; the rotations of each input
+// decomposed in groups of up to kBatchItems on s; the rotations of each input
 // then run in chunks alternating over the lanes.
 int rotate_hoisted(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, int n_in, int level, int n_rot,
                    const uint32_t* g, const uint64_t* const* evk, uint64_t* out, uint64_t out_in_stride,
@@ -295,7 +293,7 @@ int rotate_hoisted(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride
                                     hipMemcpyDeviceToDevice, s));
   }
   if (rots.empty() || n_in == 0) return CKKS_OK;
-  const int group = std::min(n_in, kMaxChunk);
+  const int group = std::min(n_in, kBatchItems);
   const int per_input = ((int)rots.size() + chunk - 1) / chunk;
   const int lanes = std::min(per_input * n_in, g_lanes_default());
   if ((rc = ensure_workspace(c, dec_per * group + back_per * chunk * lanes))) return rc;
@@ -484,7 +482,7 @@ int ckks_rescale(ckks_ctx* ctx, const uint64_t* d_in, uint64_t* d_out, int batch
   if (level == 0) return set_error(CKKS_ERANGE, "cannot rescale at level 0");
   REJECT_OVERLAP(d_out, 2ull * level * ctx->N * batch, d_in, 2ull * (level + 1) * ctx->N * batch, "the input");
   const uint64_t per = (uint64_t)ctx->N * (2 + 2 * level);
-  if ((rc = ensure_workspace(ctx, per * std::min(batch, kMaxChunk)))) return rc;
+  if ((rc = ensure_workspace(ctx, per * std::min(batch, kBatchItems)))) return rc;
   return rescale_batch(ctx, stream, d_in, 2ull * (level + 1) * ctx->N, d_out, 2ull * level * ctx->N, batch, level,
                        ctx->ws, ctx->ws_words);
 }
@@ -576,7 +574,7 @@ int ckks_poly_eval(ckks_ctx* ctx, const uint64_t* d_ct_in, int batch, int level,
   }
   uint64_t* dst = d == 1 ? d_ct_out : acc[0];
   const uint64_t rs_per = (uint64_t)N * (2 + 2 * level);
-  if ((rc = ensure_workspace(ctx, rs_per * std::min(batch, kMaxChunk)))) return rc;
+  if ((rc = ensure_workspace(ctx, rs_per * std::min(batch, kBatchItems)))) return rc;
   // the constants enter in NTT form (the same value in every word of a limb),
   // added to component 0 by the final store of each rescale
   uint64_t cv[64];
@@ -675,7 +673,7 @@ struct TreeEval {
     int rc = launch_term_mac(ctx, s, ta, n);
     if (rc) return rc;
     const uint64_t rs_per = (uint64_t)N * (2 + 2 * (t + 1));
-    if ((rc = ensure_workspace(ctx, rs_per * std::min(n, kMaxChunk)))) return rc;
+    if ((rc = ensure_workspace(ctx, rs_per * std::min(n, kBatchItems)))) return rc;
     uint64_t cv[64];
     if (has_k0) consts(t, k0, cv);
     return rescale_batch(ctx, s, G, ct_words(t + 1), out, ct_words(t), n, t + 1, ctx->ws, ctx->ws_words,
@@ -883,7 +881,7 @@ int ckks_ptmatvec(ckks_ctx* ctx, const uint64_t* d_x, int n_in, const uint64_t* 
     if (rc) break;
     if (rescale) {
       const uint64_t rs_per = (uint64_t)N * (2 + 2 * level);
-      if ((rc = ensure_workspace(ctx, rs_per * std::min(n_out, kMaxChunk)))) break;
+      if ((rc = ensure_workspace(ctx, rs_per * std::min(n_out, kBatchItems)))) break;
       rc = rescale_batch(ctx, stream, rot, ct * n2, d_y, 2ull * level * N, n_out, level, ctx->ws, ctx->ws_words);
     } else {
       for (int o = 0; o < n_out && !rc; ++o)
@@ -1010,7 +1008,7 @@ int ckks_ctmatvec(ckks_ctx* ctx, const uint64_t* d_x, int n_in, const uint64_t* 
     if (rc) break;
     if (rescale) {
       const uint64_t rs_per = (uint64_t)N * (2 + 2 * level);
-      if ((rc = ensure_workspace(ctx, rs_per * std::min(n_out, kMaxChunk)))) break;
+      if ((rc = ensure_workspace(ctx, rs_per * std::min(n_out, kBatchItems)))) break;
       rc = rescale_batch(ctx, stream, rot, ct * n2, d_y, 2ull * level * N, n_out, level, ctx->ws, ctx->ws_words);
     } else {
       for (int o = 0; o < n_out && !rc; ++o)

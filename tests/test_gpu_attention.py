@@ -20,6 +20,7 @@ SETS = {
     "c3": (12, 24, 54, 8, 60, 3),
     "one_digit": (11, 12, 50, 12, 60, 1),
     "many_digits": (10, 9, 54, 1, 60, 9),
+    "digit_each": (10, 14, 50, 1, 60, 14),  # 14 x 15 extended limbs: more transforms than one launch lists
     "q57": (13, 6, 57, 3, 60, 2),
     "wide": (12, 6, 62, 2, 61, 3),
     "wide61": (11, 8, 61, 4, 62, 2),
@@ -79,6 +80,8 @@ SUMS = [
     ("c3", 23, 2, [8, 2]), ("c3", 16, 3, [3]), ("c3", 7, 1, [4]), ("one_digit", 11, 2, [6]), ("one_digit", 4, 1, [2, 2]),
     ("many_digits", 8, 2, [9]), ("many_digits", 3, 17, [2]), ("q57", 5, 3, [8]), ("wide", 5, 2, [8]), ("wide", 1, 1, [3]),
     ("wide61", 7, 2, [5, 3]), ("small", 3, 1, [32]), ("tiny", 2, 8, [4]),
+    ("many_digits", 8, 1, [32]),  # 9 digits x 31 rotations: the column sums fold on the way
+    ("digit_each", 13, 2, [3]), ("small", 4, 131, [2]),
 ]
 
 
@@ -93,7 +96,7 @@ def test_rotate_sum_parity(lib, orc, sets, name, level, batch, radices):
     same(out, np.stack([orc.rotate_sum(P, level, c, gal, keys) for c in x]))
 
 
-@pytest.mark.parametrize("name,level,radices", [("c3", 23, [8]), ("q57", 5, [32]), ("many_digits", 8, [16]),
+@pytest.mark.parametrize("name,level,radices", [("c3", 23, [8]), ("q57", 5, [32]), ("many_digits", 8, [32]),
                                                  ("wide", 5, [16]), ("wide61", 7, [8]), ("one_digit", 11, [8])])
 def test_rotate_sum_top_of_range(lib, orc, sets, name, level, radices):
     ctx, P = sets(name)
@@ -247,7 +250,7 @@ def test_linattn_chunk_parity(lib, orc, sets, name, level, T, G, R, read, carry,
     ("tiny", 3, 1, 1, True, [2]), ("tiny", 2, 1, 0, True, [3]), ("tiny", 3, 2, 1, False, []), ("small", 5, 3, 2, True, [4]),
     ("small", 4, 11, 11, True, [2]), ("small", 2, 2, 0, False, [2, 2]), ("c3", 23, 2, 1, True, [3]),
     ("c3", 12, 1, 0, True, [8]), ("wide", 5, 2, 1, True, [2]), ("wide61", 7, 1, 0, True, [2]),
-    ("many_digits", 8, 1, 1, True, [2]), ("one_digit", 6, 1, 1, True, [2])])
+    ("many_digits", 8, 1, 1, True, [2]), ("one_digit", 6, 1, 1, True, [2]), ("digit_each", 13, 1, 1, True, [2])])
 @pytest.mark.parametrize("top", [False, True])
 def test_linattn_step_parity(lib, orc, sets, name, level, G, R, state, radices, top):
     ctx, P = sets(name)
