@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libckks_mi355x.so")
 SOURCES = ["ctx.hip", "ntt.hip", "kernels.hip", "keyswitch.hip", "rescale.hip", "ops.hip", "sumrot.hip",
-           "attn_kernels.hip", "attention.hip", "noalloc.hip", "probe.hip"]
+           "attn_kernels.hip", "attention.hip", "small.hip", "noalloc.hip", "probe.hip"]
 FLAGS = [
     "--offload-arch=gfx950",
     "-O3",

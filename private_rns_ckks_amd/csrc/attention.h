@@ -10,6 +10,17 @@ constexpr int kMaxSumRot = CKKS_SUM_MAX_RADIX - 1;  // rotations of one stage
 // Words of workspace sum_stages needs for `batch` items at `level`.
 size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage);
 
+// Inner products of n items' raised digits (E: item b at E + b*E_stride,
+// [beta][next][N]; own: the NTT-form input [nq][N], own_stride apart) with the
+// keys of n_rot rotations, each through tau_g: acc[c] = sum_r sum_j
+// tau_{g_r}(D_j) evk_{r,j}.c into A (item b at A + b*A_stride, [2][next][N]).
+// c0 (optional, [nq][N], own_stride apart): component 0 of the ciphertext
+// limbs gets P sum_r tau_{g_r}(c0) added.  Ciphertext limbs are left congruent
+// (below 10 q), special limbs below 4q.
+int key_ip(Ctx* c, hipStream_t s, int level, int n, const uint64_t* E, uint64_t E_stride, const uint64_t* own,
+           uint64_t own_stride, const uint64_t* c0, uint64_t* A, uint64_t A_stride, int n_rot, const uint32_t* g,
+           const uint64_t* const* evk);
+
 // `batch` ciphertexts (item b at in + b*in_stride) through every stage of the
 // checked plan into out + b*out_stride.  ws holds sum_ws_words.
 int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,

@@ -102,6 +102,24 @@ int ks_rescale(Ctx* c, hipStream_t s, int level, int drop, int n_items, const ui
 int drop_col_pass(Ctx* c, hipStream_t s, uint64_t* A, uint64_t* W, uint64_t per, int n_items, int level, int drop,
                   int comp_limbs);
 
+// The same steps on small rings (small.hip), which ks_decompose, ks_back and
+// ks_rescale take there: `per` is the distance between items of the workspace.
+// The rule for n items: N <= 2^12 and n limbs of n * (level + 1) * N <= 2^21
+// words, past which one workgroup per limb loses to the two-pass kernels' finer
+// tiles.  A stage of radix 8: 34 against 56 us for 1 item of 5 limbs at N =
+// 2^10, 68 against 129 us for 16 items of 12 limbs at N = 2^11, 97 against 146
+// us for 32 items of 4 limbs at N = 2^12; 459 against 421 us for 128 items of 8
+// limbs there.  At N = 2^13 one item of 5 limbs took 98 us against 68.
+inline bool small_ring(const Ctx* c, int level, int n) {
+  return c->log_n <= 12 && (uint64_t)n * (level + 1) * c->N <= (1u << 21);
+}
+int small_decompose(Ctx* c, hipStream_t s, int level, int n, const uint64_t* src, uint64_t src_stride, uint64_t* Y,
+                    uint64_t* E, uint64_t per);
+int small_back(Ctx* c, hipStream_t s, int level, int drop, int n, const KSItem* it, uint64_t* A, uint64_t per,
+               uint64_t add_stride, uint64_t accum_stride, uint64_t out_stride, int out_comp_limbs);
+int small_rescale(Ctx* c, hipStream_t s, int level, int drop, int n, const uint64_t* X, uint64_t x_stride,
+                  const uint64_t* rlk, uint64_t* out, uint64_t out_stride, uint64_t* ws, uint64_t per);
+
 // Hoisted rotations of several inputs that share one decomposition each:
 // ks_decompose raises the digits of c1 (input i at c1 + i*c1_stride, NTT form)
 // to the extended basis and transforms them, into dec (input i at

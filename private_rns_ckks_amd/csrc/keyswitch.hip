@@ -830,6 +830,8 @@ int ks_back(Ctx* c, hipStream_t s, int level, int n_items, const KSItem* it, uin
   const int log_n = (int)c->log_n;
   const int nq = level + 1, next = nq + (int)c->K;
   int rc;
+  if (small_ring(c, level, n_items))
+    return small_back(c, s, level, 0, n_items, it, A, per, add_stride, accum_stride, out_stride, out_comp_limbs);
   // F, G: inverse NTT of the special limbs, times [phat_k^-1 N^-1]: y_k
   {
     NttJobs jobs;
@@ -920,6 +922,7 @@ int ks_decompose(Ctx* c, hipStream_t s, int level, int n_in, const uint64_t* c1,
   const int lr = logb_row(log_n);
   int rc;
   if (n_in > kMaxChunk) return set_error(CKKS_EINTERNAL, "too many inputs to decompose at once");
+  if (small_ring(c, level, n_in)) return small_decompose(c, s, level, n_in, c1, c1_stride, Y, E, dec_stride);
   // inverse row pass of c1
   {
     GatherArgs ga;
@@ -1137,6 +1140,8 @@ int ks_rescale(Ctx* c, hipStream_t s, int level, int drop, int n_items, const ui
   const int nq = level + 1, next = nq + (int)c->K, beta = c->beta(level), K = (int)c->K, low = nq - drop;
   if (n_items > kMaxChunk || drop < 1 || drop > 2 || low < 1) return set_error(CKKS_EINTERNAL, "bad rescale chunk");
   const uint64_t per = ks_rescale_ws_words(c, level, drop);
+  if (small_ring(c, level, n_items))
+    return small_rescale(c, s, level, drop, n_items, X, x_stride, rlk, out, out_stride, ws, per);
   uint64_t* Y = ws;
   uint64_t* E = Y + (uint64_t)nq * N;
   uint64_t* A = E + (uint64_t)beta * next * N;  // [2][drop + K][N]

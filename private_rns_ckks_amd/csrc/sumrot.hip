@@ -16,10 +16,11 @@ namespace {
 using nttc::at_u32;
 
 struct SumIPArgs {
-  const uint64_t* E;   // item b: E + b*E_bstride, [beta][next][N] raised digits
-  const uint64_t* ct;  // item b: ct + b*ct_bstride, [2][nq][N]: the stage's input
-  uint64_t* acc;       // item b: acc + b*acc_bstride, [2][next][N]
-  uint64_t E_bstride, ct_bstride, acc_bstride;
+  const uint64_t* E;    // item b: E + b*E_bstride, [beta][next][N] raised digits
+  const uint64_t* own;  // item b: own + b*own_bstride, [nq][N]: the input (limbs inside their own digit)
+  const uint64_t* c0;   // or NULL, own_bstride apart
+  uint64_t* acc;        // item b: acc + b*acc_bstride, [2][next][N]
+  uint64_t E_bstride, own_bstride, acc_bstride;
   const uint64_t* evk[kMaxSumRot];
   uint32_t g[kMaxSumRot];
   const PrimeConst* prime;
@@ -111,9 +112,12 @@ struct SumTerm {
 // order onto an aligned pair, perhaps swapped, so a gather is one 16-byte load.
 // Digits are the outer loop: the I limbs of one digit (I * 512 KB at N = 2^16)
 // stay in an XCD's L2 while the rotations gather from them.
-template <int I, int SH, bool NT>
+//
+// SPLIT > 1: the terms are dealt to SPLIT waves that hold the same words
+// (`part` of them in turn), joined through LDS by the first.
+template <int I, int SH, bool NT, int SPLIT>
 __device__ __forceinline__ void sum_ip_narrow(const SumIPArgs& a, const PrimeConst& pc, int t, int keyl, int item0,
-                                              uint32_t w0) {
+                                              uint32_t w0, int part, uint64_t* lds) {
   const int log_n = a.log_n;
   const uint64_t q = pc.q, inv1 = pc.inv1;
   const uint64_t LKN = (uint64_t)(a.L + a.K) << log_n;
@@ -130,7 +134,7 @@ __device__ __forceinline__ void sum_ip_narrow(const SumIPArgs& a, const PrimeCon
     const bool own = t >= j * a.alpha && t < (j + 1) * a.alpha && t <= a.level;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const uint64_t* d = own ? a.ct + it[i] * a.ct_bstride + ((uint64_t)(a.level + 1 + t) << log_n)
+      const uint64_t* d = own ? a.own + it[i] * a.own_bstride + ((uint64_t)t << log_n)
                               : a.E + it[i] * a.E_bstride + ((uint64_t)(j * a.next + t) << log_n);
       s.x[i] = at_u32(reinterpret_cast<const ulonglong2*>(d), src >> 1);
     }
@@ -140,39 +144,61 @@ __device__ __forceinline__ void sum_ip_narrow(const SumIPArgs& a, const PrimeCon
   for (int i = 0; i < I; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) A[i][e >> 1][e & 1] = Cols<SH>{0, 0, 0};
+  // DEPTH terms load ahead: with one or two items a term computes for less
+  // time than its key words take from HBM (with three or four, a second term's
+  // registers would cost a wave)
+  constexpr int DEPTH = I <= 2 ? 3 : 1;
   const int terms = a.beta * a.n_rot;
-  int since = 0, j = 0, r = 0;
-  SumTerm<I> cur;
-  load(0, 0, cur);
-  for (int n = 0; n < terms; ++n) {
-    if (++r == a.n_rot) {
-      r = 0;
+  int since = 0, j = 0, r = part;  // j, r: the next term to load
+  auto carry = [&] {
+    while (r >= a.n_rot) {
+      r -= a.n_rot;
       ++j;
     }
-    SumTerm<I> next = cur;
-    if (n + 1 < terms) load(j, r, next);
-    const uint32_t bl0 = low_half<SH>(cur.kb.x), bh0 = (uint32_t)(cur.kb.x >> SH);
-    const uint32_t bl1 = low_half<SH>(cur.kb.y), bh1 = (uint32_t)(cur.kb.y >> SH);
-    const uint32_t al0 = low_half<SH>(cur.ka.x), ah0 = (uint32_t)(cur.ka.x >> SH);
-    const uint32_t al1 = low_half<SH>(cur.ka.y), ah1 = (uint32_t)(cur.ka.y >> SH);
+  };
+  auto advance = [&] {
+    r += SPLIT;
+    carry();
+  };
+  carry();
+  SumTerm<I> buf[DEPTH];
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const uint64_t x0 = cur.swap ? cur.x[i].y : cur.x[i].x, x1 = cur.swap ? cur.x[i].x : cur.x[i].y;
-      const uint32_t l0 = low_half<SH>(x0), h0 = (uint32_t)(x0 >> SH);
-      const uint32_t l1 = low_half<SH>(x1), h1 = (uint32_t)(x1 >> SH);
-      cols_mac<SH>(A[i][0][0], l0, h0, bl0, bh0);
-      cols_mac<SH>(A[i][0][1], l1, h1, bl1, bh1);
-      cols_mac<SH>(A[i][1][0], l0, h0, al0, ah0);
-      cols_mac<SH>(A[i][1][1], l1, h1, al1, ah1);
+  for (int d = 0; d < DEPTH; ++d)
+    if (part + d * SPLIT < terms) {
+      load(j, r, buf[d]);
+      advance();
     }
-    if (++since == kFoldTerms<SH>) {
-      since = 0;
+  for (int n = part; n < terms; n += DEPTH * SPLIT) {
 #pragma unroll
-      for (int i = 0; i < I; ++i)
+    for (int d = 0; d < DEPTH; ++d) {
+      if (n + d * SPLIT >= terms) break;
+      const SumTerm<I> cur = buf[d];
+      if (n + (d + DEPTH) * SPLIT < terms) {
+        load(j, r, buf[d]);
+        advance();
+      }
+      const uint32_t bl0 = low_half<SH>(cur.kb.x), bh0 = (uint32_t)(cur.kb.x >> SH);
+      const uint32_t bl1 = low_half<SH>(cur.kb.y), bh1 = (uint32_t)(cur.kb.y >> SH);
+      const uint32_t al0 = low_half<SH>(cur.ka.x), ah0 = (uint32_t)(cur.ka.x >> SH);
+      const uint32_t al1 = low_half<SH>(cur.ka.y), ah1 = (uint32_t)(cur.ka.y >> SH);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) cols_fold<SH>(A[i][e >> 1][e & 1], q, inv1);
+      for (int i = 0; i < I; ++i) {
+        const uint64_t x0 = cur.swap ? cur.x[i].y : cur.x[i].x, x1 = cur.swap ? cur.x[i].x : cur.x[i].y;
+        const uint32_t l0 = low_half<SH>(x0), h0 = (uint32_t)(x0 >> SH);
+        const uint32_t l1 = low_half<SH>(x1), h1 = (uint32_t)(x1 >> SH);
+        cols_mac<SH>(A[i][0][0], l0, h0, bl0, bh0);
+        cols_mac<SH>(A[i][0][1], l1, h1, bl1, bh1);
+        cols_mac<SH>(A[i][1][0], l0, h0, al0, ah0);
+        cols_mac<SH>(A[i][1][1], l1, h1, al1, ah1);
+      }
+      if (++since == kFoldTerms<SH>) {
+        since = 0;
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) cols_fold<SH>(A[i][e >> 1][e & 1], q, inv1);
+      }
     }
-    cur = next;
   }
   // Ciphertext limbs leave the kernel congruent, below 10 q < 2^64: the last
   // pass multiplies them by P^-1 with a product that takes any 64-bit word.
@@ -181,39 +207,67 @@ __device__ __forceinline__ void sum_ip_narrow(const SumIPArgs& a, const PrimeCon
 #pragma unroll
   for (int i = 0; i < I; ++i) s0[i] = s1[i] = 0;
   const bool low = t <= a.level;
-  if (low) {
-    for (int k = 0; k < a.n_rot; ++k) {
+  if (low && a.c0) {
+    for (int k = part; k < a.n_rot; k += SPLIT) {
       const uint32_t src = automorph_src(w0, a.g[k], log_n);
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         const ulonglong2 v = at_u32(
-            reinterpret_cast<const ulonglong2*>(a.ct + it[i] * a.ct_bstride + ((uint64_t)t << log_n)), src >> 1);
+            reinterpret_cast<const ulonglong2*>(a.c0 + it[i] * a.own_bstride + ((uint64_t)t << log_n)), src >> 1);
         const uint64_t x0 = src & 1 ? v.y : v.x, x1 = src & 1 ? v.x : v.y;
         s0[i] = SH == 27 ? s0[i] + x0 : add_mod(s0[i], x0, q);  // at most 31 words below 2^54
         s1[i] = SH == 27 ? s1[i] + x1 : add_mod(s1[i], x1, q);
       }
     }
-    const uint64_t pw = a.pmod[2 * t], pwp = a.pmod[2 * t + 1];
+  }
+  uint64_t v[I][4];
+  const uint64_t cut = low && SPLIT == 1 ? ~0ull : 4 * q;
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[i][e] = cols_reduce<SH>(A[i][e >> 1][e & 1], q, pc.r64, pc.r64p, inv1);
+      if (v[i][e] >= cut) v[i][e] -= 4 * q;
+    }
+  if constexpr (SPLIT > 1) {
+    constexpr int PER = 6 * I;  // words a lane hands over
+    const int lane = threadIdx.x & 63;
+    if (part) {
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lds[((part - 1) * PER + i * 6 + e) * 64 + lane] = v[i][e];
+        lds[((part - 1) * PER + i * 6 + 4) * 64 + lane] = s0[i];
+        lds[((part - 1) * PER + i * 6 + 5) * 64 + lane] = s1[i];
+      }
+    }
+    __syncthreads();
+    if (part) return;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      s0[i] = mul_shoup_lazy(s0[i], pw, pwp, q);  // [0, 4q)
-      s1[i] = mul_shoup_lazy(s1[i], pw, pwp, q);
+#pragma unroll
+      for (int p = 0; p < SPLIT - 1; ++p) {  // 4 x 4q < 2^64, 4 x 31 words below 2^54 or 4 below q
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] += lds[(p * PER + i * 6 + e) * 64 + lane];
+        s0[i] += lds[(p * PER + i * 6 + 4) * 64 + lane];
+        s1[i] += lds[(p * PER + i * 6 + 5) * 64 + lane];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = reduce64(v[i][e], q, inv1);
     }
   }
-  const uint64_t cut = low ? ~0ull : 4 * q;
+  const uint64_t pw = low ? a.pmod[2 * t] : 0, pwp = low ? a.pmod[2 * t + 1] : 0;
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     if (item0 + i >= a.n_items) break;
+    if (low && a.c0) {  // [0, 4q)
+      v[i][0] += mul_shoup_lazy(s0[i], pw, pwp, q);
+      v[i][1] += mul_shoup_lazy(s1[i], pw, pwp, q);
+    }
     uint64_t* ob = a.acc + (item0 + i) * a.acc_bstride + ((uint64_t)t << log_n);
     uint64_t* oa = ob + ((uint64_t)a.next << log_n);
-    uint64_t v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = cols_reduce<SH>(A[i][e >> 1][e & 1], q, pc.r64, pc.r64p, inv1);
-      if (v[e] >= cut) v[e] -= 4 * q;
-    }
-    store_pair<NT>(ob, w0, v[0] + s0[i], v[1] + s1[i]);
-    store_pair<NT>(oa, w0, v[2], v[3]);
+    store_pair<NT>(ob, w0, v[i][0], v[i][1]);
+    store_pair<NT>(oa, w0, v[i][2], v[i][3]);
   }
 }
 
@@ -233,9 +287,27 @@ __global__ __launch_bounds__(256) void sum_ip_kernel(SumIPArgs a) {
   const PrimeConst& pc = a.prime[keyl];
   const uint32_t w0 = (gp.tile * 256 + threadIdx.x) * 2;
   if (pc.q < (1ull << 54))
-    sum_ip_narrow<I, 27, ONE>(a, pc, t, keyl, gp.item * I, w0);
+    sum_ip_narrow<I, 27, ONE, 1>(a, pc, t, keyl, gp.item * I, w0, 0, nullptr);
   else
-    sum_ip_narrow<I, 30, ONE>(a, pc, t, keyl, gp.item * I, w0);
+    sum_ip_narrow<I, 30, ONE, 1>(a, pc, t, keyl, gp.item * I, w0, 0, nullptr);
+}
+
+// The same for launches of less than a wave a SIMD, whose time is one wave's
+// chain of terms: tiles of 128 words, the terms dealt to the workgroup's four
+// waves.  1 item, 28 terms, 5 limbs, N = 2^12: 13.7 -> 6.9 us.
+constexpr int kSumSplit = 4;
+template <int I>
+__global__ __launch_bounds__(256) void sum_ip_split_kernel(SumIPArgs a) {
+  __shared__ uint64_t lds[(kSumSplit - 1) * 6 * I * 64];
+  const int t = blockIdx.y;
+  const int keyl = t <= a.level ? t : a.L + (t - a.level - 1);
+  const PrimeConst& pc = a.prime[keyl];
+  const uint32_t w0 = (blockIdx.x * 64 + (threadIdx.x & 63)) * 2;
+  const int part = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (pc.q < (1ull << 54))
+    sum_ip_narrow<I, 27, true, kSumSplit>(a, pc, t, keyl, 0, w0, part, lds);
+  else
+    sum_ip_narrow<I, 30, true, kSumSplit>(a, pc, t, keyl, 0, w0, part, lds);
 }
 
 // Primes up to 2^62: lazy Montgomery products as in the key switch, one item.
@@ -247,7 +319,8 @@ __global__ __launch_bounds__(256) void sum_ip_wide_kernel(SumIPArgs a) {
   const int log_n = a.log_n;
   const uint32_t w = blockIdx.x * blockDim.x + threadIdx.x;
   const uint64_t LKN = (uint64_t)(a.L + a.K) << log_n;
-  const uint64_t* c0 = a.ct + item * a.ct_bstride + ((uint64_t)t << log_n);
+  const uint64_t limb = item * a.own_bstride + ((uint64_t)t << log_n);
+  const bool add = t <= a.level && a.c0;
   uint64_t b = 0, c = 0, rot = 0;
   const int fold = mont_fold(q);
   int since = 0;
@@ -256,7 +329,7 @@ __global__ __launch_bounds__(256) void sum_ip_wide_kernel(SumIPArgs a) {
     const uint64_t* evk = a.evk[r] + ((uint64_t)keyl << log_n) + w;
     for (int j = 0; j < a.beta; ++j) {
       const bool own = t >= j * a.alpha && t < (j + 1) * a.alpha && t <= a.level;
-      const uint64_t x = own ? c0[((uint64_t)(a.level + 1) << log_n) + src]
+      const uint64_t x = own ? a.own[limb + src]
                              : a.E[item * a.E_bstride + ((uint64_t)(j * a.next + t) << log_n) + src];
       b += mont_mul_lazy(x, evk[(uint64_t)(2 * j) * LKN], q, mp);
       c += mont_mul_lazy(x, evk[(uint64_t)(2 * j + 1) * LKN], q, mp);
@@ -266,10 +339,10 @@ __global__ __launch_bounds__(256) void sum_ip_wide_kernel(SumIPArgs a) {
         c = reduce64(c, q, pc.inv1);
       }
     }
-    if (t <= a.level) rot = add_mod(rot, c0[src], q);
+    if (add) rot = add_mod(rot, a.c0[limb + src], q);
   }
   b = reduce_4q(mul_shoup_lazy(b, pc.r64, pc.r64p, q), q);
-  if (t <= a.level) b = add_mod(b, reduce_4q(mul_shoup_lazy(rot, a.pmod[2 * t], a.pmod[2 * t + 1], q), q), q);
+  if (add) b = add_mod(b, reduce_4q(mul_shoup_lazy(rot, a.pmod[2 * t], a.pmod[2 * t + 1], q), q), q);
   uint64_t* o = a.acc + item * a.acc_bstride + ((uint64_t)t << log_n) + w;
   o[0] = b;
   o[(uint64_t)a.next << log_n] = reduce_4q(mul_shoup_lazy(c, pc.r64, pc.r64p, q), q);
@@ -286,6 +359,16 @@ int launch_sum_ip(Ctx* c, hipStream_t s, const SumIPArgs& a) {
   } else {
     // even groups: past 4 items they hold 3 or 4
     const int groups = (a.n_items + kSumHeld - 1) / kSumHeld, held = (a.n_items + groups - 1) / groups;
+    // 1024 SIMDs; a workgroup of the split kernel takes four waves for 128 words
+    if (groups == 1 && (uint64_t)(c->N / 128) * a.next <= 1024 && a.beta * a.n_rot >= 2 * kSumSplit) {
+      auto fs = held == 1   ? sum_ip_split_kernel<1>
+                : held == 2 ? sum_ip_split_kernel<2>
+                : held == 3 ? sum_ip_split_kernel<3>
+                            : sum_ip_split_kernel<4>;
+      hipLaunchKernelGGL(fs, dim3(c->N / 128, a.next), dim3(256), 0, s, a);
+      CKKS_HIP_CHECK(hipGetLastError());
+      return CKKS_OK;
+    }
     auto fn = groups > 1 ? (held == 3 ? sum_ip_kernel<3, false> : sum_ip_kernel<4, false>)
               : held == 1 ? sum_ip_kernel<1, true>
               : held == 2 ? sum_ip_kernel<2, true>
@@ -300,25 +383,20 @@ int launch_sum_ip(Ctx* c, hipStream_t s, const SumIPArgs& a) {
 // Words per item: decomposition, accumulators, ModDown conversion.
 size_t stage_words(const Ctx* c, int level) { return ks_dec_words(c, level) + ks_back_words(c, level); }
 
-// One stage on n items (n <= kMaxChunk): decomposition, inner product, and
-// the ModDown of a key switch, whose last pass adds the stage's input.
-int sum_stage(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride, int n,
-              int level, int n_rot, const uint32_t* g, const uint64_t* const* evk, uint64_t* ws) {
-  const uint32_t N = c->N;
-  const int nq = level + 1, next = nq + (int)c->K;
-  const uint64_t dec_per = ks_dec_words(c, level), per = ks_back_words(c, level);
-  uint64_t* dec = ws;
-  uint64_t* A = ws + dec_per * n;
-  int rc = ks_decompose(c, s, level, n, in + (uint64_t)nq * N, in_stride, dec, dec_per);
-  if (rc) return rc;
+}  // namespace
+
+int key_ip(Ctx* c, hipStream_t s, int level, int n, const uint64_t* E, uint64_t E_stride, const uint64_t* own,
+           uint64_t own_stride, const uint64_t* c0, uint64_t* A, uint64_t A_stride, int n_rot, const uint32_t* g,
+           const uint64_t* const* evk) {
   SumIPArgs a;
   memset(&a, 0, sizeof(a));
-  a.E = dec + (uint64_t)nq * N;
-  a.E_bstride = dec_per;
-  a.ct = in;
-  a.ct_bstride = in_stride;
+  a.E = E;
+  a.E_bstride = E_stride;
+  a.own = own;
+  a.own_bstride = own_stride;
+  a.c0 = c0;
   a.acc = A;
-  a.acc_bstride = per;
+  a.acc_bstride = A_stride;
   for (int r = 0; r < n_rot; ++r) {
     a.evk[r] = evk[r];
     a.g[r] = g[r];
@@ -327,22 +405,35 @@ int sum_stage(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uin
   a.pmod = c->d_moddown + c->md.pmod;
   a.log_n = (int)c->log_n;
   a.level = level;
-  a.next = next;
+  a.next = level + 1 + (int)c->K;
   a.beta = c->beta(level);
   a.alpha = (int)c->alpha;
   a.L = (int)c->L;
   a.K = (int)c->K;
   a.n_rot = n_rot;
   a.n_items = n;
-  if ((rc = launch_sum_ip(c, s, a))) return rc;
+  return launch_sum_ip(c, s, a);
+}
+
+// One stage on n items (n <= kMaxChunk): decomposition, inner product, and
+// the ModDown of a key switch, whose last pass adds the stage's input.
+static int sum_stage(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
+                     int n, int level, int n_rot, const uint32_t* g, const uint64_t* const* evk, uint64_t* ws) {
+  const uint32_t N = c->N;
+  const int nq = level + 1, next = nq + (int)c->K;
+  const uint64_t dec_per = ks_dec_words(c, level), per = ks_back_words(c, level);
+  uint64_t* dec = ws;
+  uint64_t* A = ws + dec_per * n;
+  const uint64_t* c1 = in + (uint64_t)nq * N;
+  int rc = ks_decompose(c, s, level, n, c1, in_stride, dec, dec_per);
+  if (rc) return rc;
+  if ((rc = key_ip(c, s, level, n, dec + (uint64_t)nq * N, dec_per, c1, in_stride, in, A, per, n_rot, g, evk))) return rc;
   KSItem it[kMaxChunk];
-  memset(it, 0, sizeof(it));
+  memset(it, 0, sizeof(KSItem) * n);
   it[0].accum = in;
   it[0].out = out;
   return ks_back(c, s, level, n, it, A, A + 2ull * next * N, per, 0, in_stride, out_stride, nq);
 }
-
-}  // namespace
 
 // Words of a group of items that goes through the stages together, with the
 // two buffers between stages.
