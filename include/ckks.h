@@ -381,9 +381,8 @@ int ckks_ctmatvec(ckks_ctx* ctx, const uint64_t* d_x, int n_in, const uint64_t* 
  *   D_j     raised digits of c1, as in ckks_rotate_hoisted
  *   U       = sum_r sum_j tau_{g_r}(D_j) * evk_{r,j}    (extended basis)
  *   out     = (c0 + sum_r tau_{g_r}(c0) + ModDown(U_0), c1 + ModDown(U_1))
- * so a radix of 4 to 8 takes about half the time of the same sum by
- * ckks_rotate with CKKS_ROT_ACCUMULATE (radix 2 is that rotation up to the
- * words of the decomposition), for radix-1 keys instead of log2(radix). */
+ * so a stage of radix 8 takes about half the time of the same sum by three
+ * calls of ckks_rotate with CKKS_ROT_ACCUMULATE, for 7 keys instead of 3. */
 typedef struct {
   int n_stage;                    /* 0..CKKS_SUM_MAX_STAGES */
   const int* radix;               /* host [n_stage], each 2..CKKS_SUM_MAX_RADIX */

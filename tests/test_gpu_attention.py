@@ -22,6 +22,12 @@ SETS = {
     "many_digits": (10, 9, 54, 1, 60, 9),
     "digit_each": (10, 14, 50, 1, 60, 14),  # 14 x 15 extended limbs: more transforms than one launch lists
     "q57": (13, 6, 57, 3, 60, 2),
+    "mid": (13, 8, 54, 3, 60, 3),
+    "mid14": (14, 5, 50, 2, 60, 3),
+    "mid15": (15, 4, 45, 2, 60, 2),
+    "mid57": (13, 6, 57, 3, 59, 2),
+    "midwide": (13, 6, 62, 2, 61, 3),
+    "mid16": (13, 16, 54, 16, 60, 1),
     "wide": (12, 6, 62, 2, 61, 3),
     "wide61": (11, 8, 61, 4, 62, 2),
 }
@@ -81,7 +87,10 @@ SUMS = [
     ("many_digits", 8, 2, [9]), ("many_digits", 3, 17, [2]), ("q57", 5, 3, [8]), ("wide", 5, 2, [8]), ("wide", 1, 1, [3]),
     ("wide61", 7, 2, [5, 3]), ("small", 3, 1, [32]), ("tiny", 2, 8, [4]),
     ("many_digits", 8, 1, [32]),  # 9 digits x 31 rotations: the column sums fold on the way
-    ("digit_each", 13, 2, [3]), ("small", 4, 131, [2]),
+    ("many_digits", 8, 5, [32]),
+    ("digit_each", 13, 2, [3]), ("small", 4, 131, [2]), ("c3", 23, 23, [2]),
+    ("mid", 7, 2, [8]), ("mid14", 4, 5, [4, 2]), ("mid15", 3, 1, [3]), ("mid57", 5, 2, [4]), ("midwide", 5, 2, [3]),
+    ("mid16", 15, 1, [3]),
 ]
 
 
@@ -97,16 +106,19 @@ def test_rotate_sum_parity(lib, orc, sets, name, level, batch, radices):
 
 
 @pytest.mark.parametrize("name,level,radices", [("c3", 23, [8]), ("q57", 5, [32]), ("many_digits", 8, [32]),
-                                                 ("wide", 5, [16]), ("wide61", 7, [8]), ("one_digit", 11, [8])])
-def test_rotate_sum_top_of_range(lib, orc, sets, name, level, radices):
+                                                 ("wide", 5, [16]), ("wide61", 7, [8]), ("one_digit", 11, [8]),
+                                                 ("mid", 7, [32]), ("midwide", 5, [8])])
+@pytest.mark.parametrize("batch", [1, 2, 5])
+def test_rotate_sum_top_of_range(lib, orc, sets, name, level, radices, batch):
     ctx, P = sets(name)
-    announce("rotate_sum top of range %s" % name)
+    announce("rotate_sum top of range %s batch=%d" % (name, batch))
     st, (gal, keys) = steps(lib, P, radices, top=True)
-    x = words(P, 1, "top", level + 1, (1, 2), top=True)
+    x = words(P, 1, "top", level + 1, (batch, 2), top=True)
     x[0, 0, 0, :] = np.uint64(P.q[0] - 1)
     out = empty_dev(x.shape)
-    lib.ckks_rotate_sum(ctx, to_dev(x), out, 1, level, st)
+    lib.ckks_rotate_sum(ctx, to_dev(x), out, batch, level, st)
     same(out[0], orc.rotate_sum(P, level, x[0], gal, keys))
+    same(out[batch - 1], orc.rotate_sum(P, level, x[batch - 1], gal, keys))
 
 
 def test_rotate_sum_elements_twice_and_conjugation(lib, orc, sets):
@@ -145,7 +157,8 @@ def test_rotate_sum_encrypted(lib, orc, sets):
 
 @pytest.mark.parametrize("name,level,G,nq,nk,radices", [
     ("tiny", 3, 1, 1, 1, [2]), ("tiny", 1, 1, 2, 3, []), ("small", 5, 2, 3, 2, [4]), ("c3", 23, 1, 1, 2, [3]),
-    ("c3", 12, 2, 1, 1, [2, 2]), ("wide", 5, 1, 2, 1, [3]), ("one_digit", 11, 1, 1, 1, [2]), ("small", 2, 1, 7, 5, [2])])
+    ("c3", 12, 2, 1, 1, [2, 2]), ("wide", 5, 1, 2, 1, [3]), ("one_digit", 11, 1, 1, 1, [2]), ("small", 2, 1, 7, 5, [2]),
+    ("mid", 7, 1, 2, 3, [4]), ("mid14", 1, 1, 1, 2, []), ("midwide", 3, 1, 1, 1, [2])])
 def test_attn_scores_parity(lib, orc, sets, name, level, G, nq, nk, radices):
     ctx, P = sets(name)
     announce("attn_scores %s level=%d %dx%dx%d" % (name, level, G, nq, nk))
@@ -160,7 +173,8 @@ def test_attn_scores_parity(lib, orc, sets, name, level, G, nq, nk, radices):
 @pytest.mark.parametrize("name,level,G,nq,nk,M,radices", [
     ("tiny", 3, 1, 1, 1, 1, [2]), ("tiny", 2, 2, 2, 3, 1, []), ("tiny", 1, 1, 1, 2, 0, [2]), ("small", 5, 3, 2, 2, 2, [4]),
     ("small", 4, 2, 1, 9, 0, [2, 2]), ("c3", 12, 1, 2, 3, 1, [3]), ("wide", 5, 2, 1, 2, 2, [2]),
-    ("wide61", 7, 1, 1, 9, 1, []), ("small", 3, 1, 11, 1, 1, [2])])
+    ("wide61", 7, 1, 1, 9, 1, []), ("small", 3, 1, 11, 1, 1, [2]), ("mid", 7, 2, 2, 2, 2, [4]), ("mid14", 2, 1, 1, 2, 1, [2]),
+    ("mid57", 5, 1, 1, 2, 0, []), ("midwide", 5, 1, 1, 2, 1, [2]), ("mid16", 15, 1, 1, 1, 1, [])])
 @pytest.mark.parametrize("top", [False, True])
 def test_attn_mix_parity(lib, orc, sets, name, level, G, nq, nk, M, radices, top):
     ctx, P = sets(name)
@@ -206,6 +220,9 @@ CHUNKS = [
     ("small", 4, 2, 2, 1, False, True, False, [2, 2]), ("c3", 23, 2, 1, 1, True, True, True, [3]),
     ("wide", 5, 3, 1, 1, True, True, True, [2]), ("wide61", 7, 2, 2, 1, True, False, False, [3]),
     ("one_digit", 11, 2, 1, 1, True, True, True, [2]), ("small", 3, 13, 1, 1, True, True, True, [2]),
+    ("mid", 7, 2, 2, 1, True, True, True, [4]), ("mid14", 3, 2, 1, 1, False, False, True, [2]),
+    ("mid15", 3, 1, 1, 1, True, True, False, []), ("mid57", 5, 2, 1, 1, True, False, True, [2]),
+    ("midwide", 5, 3, 1, 1, True, True, True, [2]), ("mid16", 15, 1, 1, 1, False, False, True, [2]),
 ]
 
 
@@ -250,7 +267,9 @@ def test_linattn_chunk_parity(lib, orc, sets, name, level, T, G, R, read, carry,
     ("tiny", 3, 1, 1, True, [2]), ("tiny", 2, 1, 0, True, [3]), ("tiny", 3, 2, 1, False, []), ("small", 5, 3, 2, True, [4]),
     ("small", 4, 11, 11, True, [2]), ("small", 2, 2, 0, False, [2, 2]), ("c3", 23, 2, 1, True, [3]),
     ("c3", 12, 1, 0, True, [8]), ("wide", 5, 2, 1, True, [2]), ("wide61", 7, 1, 0, True, [2]),
-    ("many_digits", 8, 1, 1, True, [2]), ("one_digit", 6, 1, 1, True, [2]), ("digit_each", 13, 1, 1, True, [2])])
+    ("many_digits", 8, 1, 1, True, [2]), ("one_digit", 6, 1, 1, True, [2]), ("digit_each", 13, 1, 1, True, [2]),
+    ("mid", 7, 3, 2, True, [4]), ("mid14", 2, 1, 0, True, []), ("mid15", 3, 1, 1, True, [2]), ("mid57", 5, 2, 0, True, [2]),
+    ("midwide", 5, 2, 1, True, [2]), ("mid16", 15, 1, 1, True, [])])
 @pytest.mark.parametrize("top", [False, True])
 def test_linattn_step_parity(lib, orc, sets, name, level, G, R, state, radices, top):
     ctx, P = sets(name)
@@ -401,6 +420,27 @@ def test_on_another_stream(lib, orc, sets):
     lib.ckks_rotate_sum(ctx, dx, out, 2, 5, st, stream=side)
     side.synchronize()
     same(out, ref)
+
+
+def test_two_contexts_on_two_streams(lib, orc, sets):
+    """Calls of two contexts in flight at once on two streams."""
+    torch = torch_cuda()
+    made = [sets("mid"), make_pair(lib, orc, *SETS["small"])]
+    announce("two contexts")
+    runs = []
+    for n, (ctx, P) in enumerate(made):
+        st, ref_st = steps(lib, P, [4, 2], seed=n)
+        x = words(P, n, "two", P.L, (6, 2))
+        runs.append((ctx, P, st, ref_st, x, to_dev(x), empty_dev(x.shape), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for ctx, P, st, _, x, dx, out, stream in runs:
+            lib.ckks_rotate_sum(ctx, dx, out, 6, P.L - 1, st, stream=stream)
+    torch.cuda.synchronize()
+    for ctx, P, st, ref_st, x, dx, out, stream in runs:
+        same(out[0], orc.rotate_sum(P, P.L - 1, x[0], *ref_st))
+        same(out[5], orc.rotate_sum(P, P.L - 1, x[5], *ref_st))
+    made[1][0].close()
 
 
 def test_captured_step_replays(lib, orc):
