@@ -99,23 +99,43 @@ struct Tail {
   uint64_t limb(int l) const { return (uint64_t)(l + 1) * c->N; }
   DropOut drop_out(int drop) const { return DropOut{c->d_rescale, (int)c->L, drop}; }
 
+  uint64_t* ws;  // reserved words of the context's workspace
+  uint64_t ws_words;
+
+  // Words of workspace each step takes; relinearisations go in launches of as
+  // many items as 2 GiB hold (the items of a launch share the key).
+  int relin_items(int n, int level, int drop) const {
+    const uint64_t fit = (1ull << 28) / ks_rescale_ws_words(c, level, drop);
+    return (int)std::max<uint64_t>(1, std::min<uint64_t>({fit, (uint64_t)kMaxChunk, (uint64_t)n}));
+  }
+  uint64_t relin_words(int n, int level, int drop) const {
+    return ks_rescale_ws_words(c, level, drop) * relin_items(n, level, drop);
+  }
+  uint64_t rescale_words(int n, int level) const { return (uint64_t)c->N * (2 + 2 * level) * std::min(n, kMaxChunk); }
+  uint64_t sum_words(int n, int level) const {
+    return st.n_stage ? sum_ws_words(c, level, n, st.n_stage) : 0;
+  }
+
+  // `main` words for this stream's steps, `side` more for Side's.
+  int reserve(uint64_t main, uint64_t side = 0) {
+    int rc = ensure_workspace(c, main + side);
+    ws = c->ws;
+    ws_words = main;
+    return rc;
+  }
+
   // n three-part items X ([3][level+1][N] each, written with drop_out(drop))
-  // into out ([2][level+1-drop][N] each), in launches of as many items as 2 GiB
-  // of workspace hold: the items of a launch share the key.
+  // into out ([2][level+1-drop][N] each).
   int relin_rescale(const uint64_t* X, uint64_t* out, int n, int level, int drop) const {
-    const uint64_t per = ks_rescale_ws_words(c, level, drop);
-    const int chunk = (int)std::max<uint64_t>(1, std::min<uint64_t>({(1ull << 28) / per, (uint64_t)kMaxChunk, (uint64_t)n}));
-    int rc = ensure_workspace(c, per * chunk);
+    const int chunk = relin_items(n, level, drop);
+    int rc = CKKS_OK;
     for (int b0 = 0; b0 < n && rc == CKKS_OK; b0 += chunk)
       rc = ks_rescale(c, s, level, drop, std::min(chunk, n - b0), X + b0 * 3 * limb(level), 3 * limb(level), rlk,
-                      out + b0 * 2 * limb(level - drop), 2 * limb(level - drop), c->ws);
+                      out + b0 * 2 * limb(level - drop), 2 * limb(level - drop), ws);
     return rc;
   }
   int rescale(const uint64_t* R, uint64_t* Z, int n, int level) const {
-    const uint64_t per = (uint64_t)c->N * (2 + 2 * level);
-    int rc = ensure_workspace(c, per * std::min(n, kMaxChunk));
-    if (rc) return rc;
-    return rescale_batch(c, s, R, 2 * limb(level), Z, 2 * limb(level - 1), n, level, c->ws, c->ws_words);
+    return rescale_batch(c, s, R, 2 * limb(level), Z, 2 * limb(level - 1), n, level, ws, ws_words);
   }
   int sum(const uint64_t* Z, uint64_t* out, int n, int level) const {
     const uint64_t ct = 2 * limb(level);
@@ -123,10 +143,50 @@ struct Tail {
       CKKS_HIP_CHECK(hipMemcpyAsync(out, Z, ct * n * 8, hipMemcpyDeviceToDevice, s));
       return CKKS_OK;
     }
-    int rc = ensure_workspace(c, sum_ws_words(c, level, n, st.n_stage));
-    if (rc) return rc;
-    return sum_stages(c, s, Z, ct, out, ct, n, level, st, c->ws);
+    return sum_stages(c, s, Z, ct, out, ct, n, level, st, ws);
   }
+};
+
+// Steps that do not depend on the ones a Tail runs next, on an internal stream
+// that starts where the Tail's stream is now; join() (or the end of the scope)
+// makes that stream wait for them.  Two chains of launches that each leave the
+// chip part empty then overlap: attn_mix with its normaliser, one after the
+// other and so, takes 334 and 233 us for one row of 5 limbs at N = 2^13, 1229
+// and 899 for one of 13 limbs at N = 2^16, 3640 and 3250 for six of them;
+// linattn_chunk's r q beside the states 397 and 385 us for one token of 7 limbs
+// at N = 2^14, 2369 and 2288 for 16 of 2^16.  Where the runtime puts both streams
+// on one hardware queue nothing overlaps, and the events cost some 18 us a call.
+class Side {
+ public:
+  Side(const Tail& t, uint64_t side_words) : tail(t), c_(t.c), s_(t.s) {
+    rc = start();
+    tail.s = c_->lane[0];
+    tail.ws = t.ws + t.ws_words;
+    tail.ws_words = side_words;
+  }
+  ~Side() { (void)join(); }
+  int join() {
+    if (!open_) return CKKS_OK;
+    open_ = false;
+    CKKS_HIP_CHECK(hipEventRecord(c_->join_ev[0], tail.s));
+    CKKS_HIP_CHECK(hipStreamWaitEvent(s_, c_->join_ev[0], 0));
+    return CKKS_OK;
+  }
+  Tail tail;  // the steps, on the internal stream
+  int rc;     // of the constructor
+
+ private:
+  int start() {
+    int r = ensure_lanes(c_);
+    if (r) return r;
+    CKKS_HIP_CHECK(hipEventRecord(c_->fork_ev, s_));
+    CKKS_HIP_CHECK(hipStreamWaitEvent(c_->lane[0], c_->fork_ev, 0));
+    open_ = true;
+    return CKKS_OK;
+  }
+  Ctx* c_;
+  hipStream_t s_;
+  bool open_ = false;
 };
 
 int rotate_sum(Ctx* c, const uint64_t* in, uint64_t* out, int batch, int level, const ckks_sum_steps* steps,
@@ -138,11 +198,12 @@ int rotate_sum(Ctx* c, const uint64_t* in, uint64_t* out, int batch, int level, 
   const uint64_t ct = 2ull * (level + 1) * c->N;
   if ((rc = check_count(batch))) return rc;
   std::vector<Range> ins = {{in, ct * batch}};
-  Tail t{c, s, nullptr, {}};
+  Tail t{c, s, nullptr, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges({{out, ct * batch}}, ins))) return rc;
   if (t.st.n_stage == 0) return set_error(CKKS_EINVAL, "a sum needs at least one stage");
   if (batch == 0) return CKKS_OK;
   CaptureScope cap(c, s);
+  if ((rc = t.reserve(t.sum_words(batch, level)))) return rc;
   return t.sum(in, out, batch, level);
 }
 
@@ -160,13 +221,14 @@ int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, 
   const int items = n_grp * n_q * n_k, l = level;
   const uint64_t N = c->N, lim = (uint64_t)(l + 1) * N, zct = 2ull * l * N;
   std::vector<Range> ins = {{q, 2 * lim * n_grp * n_q}, {k, 2 * lim * n_grp * n_k}, {rlk, key_words(c)}};
-  Tail t{c, s, rlk, {}};
+  Tail t{c, s, rlk, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges({{out, zct * items}}, ins))) return rc;
   if (items == 0) return CKKS_OK;
   CaptureScope cap(c, s);
   const uint64_t per = 3 * lim + zct;
   const int block = block_items(per, items);
   if ((rc = ensure_aux(c, per * block))) return rc;
+  if ((rc = t.reserve(std::max(t.relin_words(block, l, 1), t.sum_words(block, l - 1))))) return rc;
   uint64_t *X = c->aux, *Z = X + 3 * lim * block;
   for (int b0 = 0; b0 < items; b0 += block) {
     const int n = std::min(block, items - b0);
@@ -214,14 +276,17 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
   if (mask) ins.push_back({mask, lim * n_mask * n_k});
   std::vector<Range> outs = {{num, nct * rows}};
   if (den) outs.push_back({den, dct * rows});
-  Tail t{c, s, rlk, {}};
+  Tail t{c, s, rlk, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges(outs, ins))) return rc;
   if (rows == 0) return CKKS_OK;
   CaptureScope cap(c, s);
-  const uint64_t per = 3 * lim + 2 * lim + mid;
+  const uint64_t per = 3 * lim + 2 * lim + 2 * mid;
   const int block = block_items(per, rows);
   if ((rc = ensure_aux(c, per * block))) return rc;
-  uint64_t *X = c->aux, *D = X + 3 * lim * block, *Z = D + 2 * lim * block;
+  uint64_t *X = c->aux, *D = X + 3 * lim * block, *Z = D + 2 * lim * block, *Y = Z + mid * block;
+  const int ld = mask ? l - 1 : l;  // den's level
+  const uint64_t side_words = den ? std::max(mask ? t.rescale_words(block, l) : 0, t.sum_words(block, ld)) : 0;
+  if ((rc = t.reserve(std::max(t.relin_words(block, l, drop), t.sum_words(block, l - drop)), side_words))) return rc;
   for (int b0 = 0; b0 < rows; b0 += block) {
     const int n = std::min(block, rows - b0);
     MixArgs m;
@@ -239,14 +304,15 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
     m.n_k = n_k;
     m.n_row = mask ? n_mask : 1;
     m.first = b0;
-    uint64_t* to = num + b0 * nct;
-    if ((rc = launch_mix(c, s, m, n)) || (rc = t.relin_rescale(X, Z, n, l, drop)) || (rc = t.sum(Z, to, n, l - drop)))
-      return rc;
-    if (!den) continue;
-    uint64_t* de = den + b0 * dct;
-    if (mask) {
-      if ((rc = t.rescale(D, Z, n, l)) || (rc = t.sum(Z, de, n, l - 1))) return rc;
-    } else if ((rc = t.sum(D, de, n, l))) {
+    if ((rc = launch_mix(c, s, m, n))) return rc;
+    if (den) {  // the normaliser's steps beside the sum's
+      Side side(t, side_words);
+      uint64_t* de = den + b0 * dct;
+      if ((rc = side.rc) || (mask && (rc = side.tail.rescale(D, Y, n, l))) || (rc = side.tail.sum(mask ? Y : D, de, n, ld)))
+        return rc;
+      if ((rc = t.relin_rescale(X, Z, n, l, drop)) || (rc = t.sum(Z, num + b0 * nct, n, l - drop)) || (rc = side.join()))
+        return rc;
+    } else if ((rc = t.relin_rescale(X, Z, n, l, drop)) || (rc = t.sum(Z, num + b0 * nct, n, l - drop))) {
       return rc;
     }
   }
@@ -277,6 +343,19 @@ int state_times_q(const Tail& t, const uint64_t* state, const uint64_t* q, uint6
   return launch_pair(t.c, t.s, a, n);
 }
 
+// The outputs of a block of nt tokens x ng groups from the states' products X:
+// relinearised into Z and summed into y, whose item (token, group) (0, 0) is
+// item `at` of n_grp a token.
+int outputs(const Tail& t, const uint64_t* X, uint64_t* Z, uint64_t* y, uint64_t at, int nt, int ng, int n_grp, int l) {
+  const uint64_t yct = 2 * t.limb(l - 3);
+  int rc = t.relin_rescale(X, Z, nt * ng, l - 2, 1);
+  if (rc) return rc;
+  if (ng == n_grp) return t.sum(Z, y + at * yct, nt * ng, l - 3);
+  for (int i = 0; i < nt; ++i)  // a token's outputs are contiguous
+    if ((rc = t.sum(Z + (uint64_t)i * ng * yct, y + (at + (uint64_t)i * n_grp) * yct, ng, l - 3))) return rc;
+  return CKKS_OK;
+}
+
 int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v, int n_tok, int n_grp,
                   const uint64_t* w, const uint64_t* r, const uint64_t* carry, int n_row, const uint64_t* state_in,
                   int level, const uint64_t* rlk, const ckks_sum_steps* steps, uint64_t* y, uint64_t* state_out,
@@ -297,7 +376,7 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
   if (r) ins.push_back({r, lim * n_tok * n_row});
   if (carry) ins.push_back({carry, sct / 2 * n_row});
   if (state_in) ins.push_back({state_in, sct * n_grp});
-  Tail t{c, s, rlk, {}};
+  Tail t{c, s, rlk, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) ||
       (rc = check_ranges({{y, yct * items}, {state_out, oct * n_grp}}, ins)))
     return rc;
@@ -313,6 +392,11 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
   if ((rc = ensure_aux(c, per * nb + (3 * lim + sct) * gb))) return rc;
   uint64_t *X = c->aux, *S = X + 3 * lim * nb, *Z = S + sct * nb, *R = Z + yct * nb, *C = R + (r ? ct * nb : 0),
            *P = C + (r ? mid * nb : 0), *V = P + 3 * lim * gb;
+  const uint64_t side_words = std::max(r ? t.rescale_words((int)nb, l) : 0, carry ? t.rescale_words(gb, l - 2) : 0);
+  if ((rc = t.reserve(std::max({t.relin_words((int)nb, l, 2), t.relin_words((int)nb, l - 2, 1),
+                                t.sum_words((int)nb, l - 3)}),
+                      side_words)))
+    return rc;
   for (int g0 = 0; g0 < n_grp; g0 += gb) {
     const int ng = std::min(gb, n_grp - g0);
     for (int t0 = 0; t0 < n_tok; t0 += tb) {
@@ -336,9 +420,9 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
       sc.n_grp = ng;
       sc.n_row = n_row;
       sc.g0 = g0;
-      if ((rc = launch_scan(c, s, sc)) || (rc = t.relin_rescale(X, S, n, l, 2))) return rc;
       const uint64_t* qt = q + at * ct;
-      if (r) {
+      if (r) {  // rescale(r q) beside the states
+        Side side(t, side_words);
         PlainMulArgs pm;
         memset(&pm, 0, sizeof(pm));
         pm.in = qt;
@@ -354,37 +438,41 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
         pm.n_grp = n_grp;
         pm.n_row = n_row;
         pm.g0 = g0;
-        if ((rc = launch_plain_mul(c, s, pm, n)) || (rc = t.rescale(R, C, n, l))) return rc;
+        if ((rc = side.rc) || (rc = launch_plain_mul(c, side.tail.s, pm, n)) || (rc = side.tail.rescale(R, C, n, l)))
+          return rc;
+        if ((rc = launch_scan(c, s, sc)) || (rc = t.relin_rescale(X, S, n, l, 2)) || (rc = side.join())) return rc;
         if ((rc = state_times_q(t, S, C, mid, mid / 2, 1, 1, X, n, l - 2))) return rc;
-      } else if ((rc = state_times_q(t, S, qt, ct, lim, ng, n_grp, X, n, l - 2))) {
+      } else if ((rc = launch_scan(c, s, sc)) || (rc = t.relin_rescale(X, S, n, l, 2)) ||
+                 (rc = state_times_q(t, S, qt, ct, lim, ng, n_grp, X, n, l - 2))) {
         return rc;
       }
-      if ((rc = t.relin_rescale(X, Z, n, l - 2, 1))) return rc;
-      // the block's outputs are contiguous when it holds every group
-      for (int i = 0; i < (ng == n_grp ? 1 : nt); ++i)
-        if ((rc = t.sum(Z + (uint64_t)i * ng * yct, y + (at + (uint64_t)i * n_grp) * yct, ng == n_grp ? n : ng, l - 3)))
-          return rc;
-      if (t0 + nt < n_tok) continue;
       const uint64_t* last = S + (uint64_t)(nt - 1) * ng * sct;
-      if (!carry) {
+      const bool end = t0 + nt == n_tok;
+      if (end && !carry)
         CKKS_HIP_CHECK(hipMemcpyAsync(state_out + g0 * sct, last, sct * ng * 8, hipMemcpyDeviceToDevice, s));
-        continue;
+      if (end && carry) {  // rescale(carry S) beside the outputs
+        Side side(t, side_words);
+        PlainMulArgs pm;
+        memset(&pm, 0, sizeof(pm));
+        pm.in = last;
+        pm.in_bstride = sct;
+        pm.in_comp = sct / 2;
+        pm.p = carry;
+        pm.out = V;
+        pm.out_bstride = sct;
+        pm.prime = c->d_prime;
+        pm.log_n = (int)c->log_n;
+        pm.nl = l - 1;
+        pm.ng = pm.n_grp = ng;
+        pm.n_row = n_row;
+        pm.g0 = g0;
+        if ((rc = side.rc) || (rc = launch_plain_mul(c, side.tail.s, pm, ng)) ||
+            (rc = side.tail.rescale(V, state_out + g0 * yct, ng, l - 2)) || (rc = outputs(t, X, Z, y, at, nt, ng, n_grp, l)) ||
+            (rc = side.join()))
+          return rc;
+      } else if ((rc = outputs(t, X, Z, y, at, nt, ng, n_grp, l))) {
+        return rc;
       }
-      PlainMulArgs pm;
-      memset(&pm, 0, sizeof(pm));
-      pm.in = last;
-      pm.in_bstride = sct;
-      pm.in_comp = sct / 2;
-      pm.p = carry;
-      pm.out = V;
-      pm.out_bstride = sct;
-      pm.prime = c->d_prime;
-      pm.log_n = (int)c->log_n;
-      pm.nl = l - 1;
-      pm.ng = pm.n_grp = ng;
-      pm.n_row = n_row;
-      pm.g0 = g0;
-      if ((rc = launch_plain_mul(c, s, pm, ng)) || (rc = t.rescale(V, state_out + g0 * yct, ng, l - 2))) return rc;
     }
   }
   return CKKS_OK;
@@ -408,7 +496,7 @@ int linattn_step(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v
   std::vector<Range> ins = {{q, ct * n_grp}, {k, ct * n_grp}, {v, ct * n_grp}, {rlk, key_words(c)}};
   if (decay) ins.push_back({decay, lim * n_row});
   if (state_in) ins.push_back({state_in, in_ct * n_grp});
-  Tail t{c, s, rlk, {}};
+  Tail t{c, s, rlk, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) ||
       (rc = check_ranges({{y, yct * n_grp}, {state_out, sct * n_grp}}, ins)))
     return rc;
@@ -417,6 +505,8 @@ int linattn_step(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v
   const uint64_t per = 3 * lim + yct;
   const int block = block_items(per, n_grp);
   if ((rc = ensure_aux(c, per * block))) return rc;
+  if ((rc = t.reserve(std::max({t.relin_words(block, l, 1), t.relin_words(block, l - 1, 1), t.sum_words(block, l - 2)}))))
+    return rc;
   uint64_t *X = c->aux, *Z = X + 3 * lim * block;
   for (int b0 = 0; b0 < n_grp; b0 += block) {
     const int n = std::min(block, n_grp - b0);

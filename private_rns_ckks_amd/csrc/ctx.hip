@@ -109,6 +109,9 @@ static int upload(void** dst, const void* src, size_t bytes) {
 
 int ensure_lanes(Ctx* c) {
   if (c->lane[0]) return CKKS_OK;
+  if (c->capturing)
+    return set_error(CKKS_EHIP, "the internal streams would be created while the stream is being captured: run a call "
+                                "of this size first");
   for (int i = 0; i < Ctx::kMaxLanes; ++i) {
     CKKS_HIP_CHECK(hipStreamCreateWithFlags(&c->lane[i], hipStreamNonBlocking));
     CKKS_HIP_CHECK(hipEventCreateWithFlags(&c->join_ev[i], hipEventDisableTiming));

@@ -521,6 +521,101 @@ def test_capture_of_a_first_call_is_refused(lib, orc):
     ctx.close()
 
 
+def test_captured_mix_and_chunk_replay(lib, orc):
+    """The calls that run steps side by side on an internal stream, captured: every replay equals the oracle's
+    words for its inputs, with eager calls of the same context between the replays."""
+    torch = torch_cuda()
+    ctx, P = make_pair(lib, orc, *SETS["small"])
+    announce("captured mix and chunk")
+    st, ref_st = steps(lib, P, [3])
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    lv, n = 5, 6
+    names = ("a", "v", "q", "k", "x")
+
+    def inputs(seed):
+        return ({t: words(P, seed, t, n, (2, 2)) for t in names}, {t: words(P, seed, t, n, (2,)) for t in ("m", "w", "r")},
+                words(P, seed, "carry", n - 2, (1,)), words(P, seed, "s", n - 2, (1, 2)))
+
+    host = inputs(0)
+    ct, pt = ({t: to_dev(x) for t, x in h.items()} for h in host[:2])
+    carry, state = to_dev(host[2]), to_dev(host[3])
+    num, den = empty_dev((1, 2, lv - 1, P.N)), empty_dev((1, 2, lv, P.N))
+    y, end = empty_dev((2, 2, lv - 2, P.N)), empty_dev((1, 2, lv - 2, P.N))
+
+    def call():
+        lib.ckks_attn_mix(ctx, ct["a"], 1, ct["v"], 2, 1, pt["m"], 1, lv, d_rlk, st, num, den)
+        lib.ckks_linattn_chunk(ctx, ct["q"], ct["k"], ct["x"], 2, 1, pt["w"], pt["r"], carry, 1, state, lv, d_rlk, st,
+                               y, end)
+
+    def check(h, what):
+        c, p, car, s_in = h
+        rn, rd = orc.attn_mix(P, lv, c["a"][None, None], c["v"][None], p["m"][None], rlk, *ref_st)
+        same(num, rn[0], what)
+        same(den, rd[0], what)
+        ry, rs = orc.linattn_chunk(P, lv, c["q"][:, None], c["k"][:, None], c["x"][:, None], p["w"][:, None],
+                                   p["r"][:, None], car, s_in, rlk, *ref_st)
+        same(y, ry[:, 0], what)
+        same(end, rs, what)
+
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for i in range(4):
+        host = inputs(10 + i)
+        for group, h in zip((ct, pt), host):
+            for t, x in h.items():
+                group[t].copy_(to_dev(x))
+        carry.copy_(to_dev(host[2]))
+        state.copy_(to_dev(host[3]))
+        for o in (num, den, y, end):
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(host, "replay %d" % i)
+        for o in (num, den, y, end):
+            o.zero_()
+        call()
+        torch.cuda.synchronize()
+        check(host, "eager after replay %d" % i)
+    del graph
+    ctx.close()
+
+
+def test_capture_before_the_internal_streams_is_refused(lib, orc):
+    """A call that would create the internal streams during a capture raises, though the buffers are large enough."""
+    torch = torch_cuda()
+    ctx, P = make_pair(lib, orc, *SETS["small"])
+    announce("capture without internal streams")
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    a, v = (words(P, 1, t, 6, (8, 2)) for t in "av")
+    da, dv = to_dev(a), to_dev(v)
+    num, den = empty_dev((8, 2, 5, P.N)), empty_dev((8, 2, 6, P.N))
+    lib.ckks_attn_mix(ctx, da, 1, dv, 1, 8, None, 0, 5, d_rlk, None, num, None)  # no normaliser: one stream
+    torch.cuda.synchronize()
+    marker = torch.zeros(8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        with pytest.raises(lib.CKKSError) as e:
+            lib.ckks_attn_mix(ctx, da, 1, dv, 1, 1, None, 0, 5, d_rlk, None, num, den)
+        marker.add_(1.0)
+    assert e.value.code == lib.CKKS_EHIP and "captured" in str(e.value)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert marker.tolist() == [1.0] * 8
+    lib.ckks_attn_mix(ctx, da, 1, dv, 1, 1, None, 0, 5, d_rlk, None, num, den)
+    torch.cuda.synchronize()
+    rn, rd = orc.attn_mix(P, 5, a[:1, None, None], v[:1, None], None, rlk, [], [])
+    same(num[:1], rn[0])
+    same(den[:1], rd[0])
+    ctx.close()
+
+
 # ---------------------------------------------------------------- refusals
 
 def refused(lib, code, fn, text=None):
