@@ -137,8 +137,12 @@ struct Tail {
   int rescale(const uint64_t* R, uint64_t* Z, int n, int level) const {
     return rescale_batch(c, s, R, 2 * limb(level), Z, 2 * limb(level - 1), n, level, ws, ws_words);
   }
+  // Where a step writes the n ciphertexts that sum() takes to out: there
+  // already if the plan has no stages.
+  uint64_t* before_sum(uint64_t* Z, uint64_t* out) const { return st.n_stage ? Z : out; }
   int sum(const uint64_t* Z, uint64_t* out, int n, int level) const {
     const uint64_t ct = 2 * limb(level);
+    if (Z == out) return CKKS_OK;
     if (st.n_stage == 0) {
       CKKS_HIP_CHECK(hipMemcpyAsync(out, Z, ct * n * 8, hipMemcpyDeviceToDevice, s));
       return CKKS_OK;
@@ -248,8 +252,8 @@ int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, 
     a.n_row = 1;
     a.first = b0;
     uint64_t* dst = out + b0 * zct;
-    if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin_rescale(X, t.st.n_stage ? Z : dst, n, l, 1))) return rc;
-    if (t.st.n_stage && (rc = t.sum(Z, dst, n, l - 1))) return rc;
+    Z = t.before_sum(Z, dst);
+    if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin_rescale(X, Z, n, l, 1)) || (rc = t.sum(Z, dst, n, l - 1))) return rc;
   }
   return CKKS_OK;
 }
@@ -295,7 +299,10 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
     m.v = v;
     m.m = mask;
     m.num = X;
-    m.den = den ? D : nullptr;
+    uint64_t *to = num + b0 * nct, *de = den ? den + b0 * dct : nullptr;
+    Z = t.before_sum(Z, to);
+    uint64_t* di = t.before_sum(mask ? Y : D, de);  // den before its sum
+    m.den = !den ? nullptr : mask ? D : di;
     m.drop = t.drop_out(drop);
     m.prime = c->d_prime;
     m.log_n = (int)c->log_n;
@@ -305,14 +312,12 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
     m.n_row = mask ? n_mask : 1;
     m.first = b0;
     if ((rc = launch_mix(c, s, m, n))) return rc;
-    if (den) {  // the normaliser's steps beside the sum's
+    if (den && (mask || t.st.n_stage)) {  // the normaliser's steps beside the sum's
       Side side(t, side_words);
-      uint64_t* de = den + b0 * dct;
-      if ((rc = side.rc) || (mask && (rc = side.tail.rescale(D, Y, n, l))) || (rc = side.tail.sum(mask ? Y : D, de, n, ld)))
+      if ((rc = side.rc) || (mask && (rc = side.tail.rescale(D, di, n, l))) || (rc = side.tail.sum(di, de, n, ld)))
         return rc;
-      if ((rc = t.relin_rescale(X, Z, n, l, drop)) || (rc = t.sum(Z, num + b0 * nct, n, l - drop)) || (rc = side.join()))
-        return rc;
-    } else if ((rc = t.relin_rescale(X, Z, n, l, drop)) || (rc = t.sum(Z, num + b0 * nct, n, l - drop))) {
+      if ((rc = t.relin_rescale(X, Z, n, l, drop)) || (rc = t.sum(Z, to, n, l - drop)) || (rc = side.join())) return rc;
+    } else if ((rc = t.relin_rescale(X, Z, n, l, drop)) || (rc = t.sum(Z, to, n, l - drop))) {
       return rc;
     }
   }
@@ -348,6 +353,7 @@ int state_times_q(const Tail& t, const uint64_t* state, const uint64_t* q, uint6
 // item `at` of n_grp a token.
 int outputs(const Tail& t, const uint64_t* X, uint64_t* Z, uint64_t* y, uint64_t at, int nt, int ng, int n_grp, int l) {
   const uint64_t yct = 2 * t.limb(l - 3);
+  if (ng == n_grp) Z = t.before_sum(Z, y + at * yct);
   int rc = t.relin_rescale(X, Z, nt * ng, l - 2, 1);
   if (rc) return rc;
   if (ng == n_grp) return t.sum(Z, y + at * yct, nt * ng, l - 3);
@@ -534,9 +540,11 @@ int linattn_step(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v
     a.first = b0;
     uint64_t* S = state_out + b0 * sct;
     if ((rc = launch_pair(c, s, a, n)) || (rc = t.relin_rescale(X, S, n, l, 1))) return rc;
-    if ((rc = state_times_q(t, S, q + b0 * ct, ct, lim, 1, 1, X, n, l - 1)) || (rc = t.relin_rescale(X, Z, n, l - 1, 1)))
+    uint64_t* yb = y + b0 * yct;
+    Z = t.before_sum(Z, yb);
+    if ((rc = state_times_q(t, S, q + b0 * ct, ct, lim, 1, 1, X, n, l - 1)) || (rc = t.relin_rescale(X, Z, n, l - 1, 1)) ||
+        (rc = t.sum(Z, yb, n, l - 2)))
       return rc;
-    if ((rc = t.sum(Z, y + b0 * yct, n, l - 2))) return rc;
   }
   return CKKS_OK;
 }

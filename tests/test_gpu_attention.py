@@ -591,26 +591,27 @@ def test_capture_before_the_internal_streams_is_refused(lib, orc):
     torch = torch_cuda()
     ctx, P = make_pair(lib, orc, *SETS["small"])
     announce("capture without internal streams")
+    st, ref_st = steps(lib, P, [2])
     rlk = key(P, 0, "rlk")
     d_rlk = to_dev(rlk)
     a, v = (words(P, 1, t, 6, (8, 2)) for t in "av")
     da, dv = to_dev(a), to_dev(v)
     num, den = empty_dev((8, 2, 5, P.N)), empty_dev((8, 2, 6, P.N))
-    lib.ckks_attn_mix(ctx, da, 1, dv, 1, 8, None, 0, 5, d_rlk, None, num, None)  # no normaliser: one stream
+    lib.ckks_attn_mix(ctx, da, 1, dv, 1, 8, None, 0, 5, d_rlk, st, num, None)  # no normaliser: one stream
     torch.cuda.synchronize()
     marker = torch.zeros(8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
         with pytest.raises(lib.CKKSError) as e:
-            lib.ckks_attn_mix(ctx, da, 1, dv, 1, 1, None, 0, 5, d_rlk, None, num, den)
+            lib.ckks_attn_mix(ctx, da, 1, dv, 1, 1, None, 0, 5, d_rlk, st, num, den)
         marker.add_(1.0)
     assert e.value.code == lib.CKKS_EHIP and "captured" in str(e.value)
     graph.replay()
     torch.cuda.synchronize()
     assert marker.tolist() == [1.0] * 8
-    lib.ckks_attn_mix(ctx, da, 1, dv, 1, 1, None, 0, 5, d_rlk, None, num, den)
+    lib.ckks_attn_mix(ctx, da, 1, dv, 1, 1, None, 0, 5, d_rlk, st, num, den)
     torch.cuda.synchronize()
-    rn, rd = orc.attn_mix(P, 5, a[:1, None, None], v[:1, None], None, rlk, [], [])
+    rn, rd = orc.attn_mix(P, 5, a[:1, None, None], v[:1, None], None, rlk, *ref_st)
     same(num[:1], rn[0])
     same(den[:1], rd[0])
     ctx.close()
