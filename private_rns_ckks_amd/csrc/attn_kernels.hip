@@ -208,6 +208,8 @@ __global__ __launch_bounds__(256) void mix_kernel(MixArgs a) {
   const RedConst pc = red_const((ConstPrime)a.prime, i);
   const uint64_t off = ((uint64_t)i << a.log_n) + c, lim = (uint64_t)a.nl << a.log_n;
   uint64_t r0 = 0, r1 = 0, r2 = 0, e0 = 0, e1 = 0;
+  AccT<WIDE> m0{}, m1{}, m2{};
+  int since = 0;
   for (int j = 0; j < a.n_k; ++j) {
     const uint64_t* x = a.a + ((uint64_t)row * a.n_k + j) * 2 * lim + off;
     const uint64_t* v = a.v + ((uint64_t)g * a.n_k + j) * 2 * lim + off;
@@ -219,7 +221,19 @@ __global__ __launch_bounds__(256) void mix_kernel(MixArgs a) {
     }
     e0 = add_mod(e0, a0, pc.q);
     e1 = add_mod(e1, a1, pc.q);
-    tensor_add<WIDE>(split_word<WIDE>(a0), split_word<WIDE>(a1), v[0], v[lim], pc, r0, r1, r2);
+    const Split<WIDE> a0s = split_word<WIDE>(a0), a1s = split_word<WIDE>(a1);
+    const Split<WIDE> v0 = split_word<WIDE>(v[0]), v1 = split_word<WIDE>(v[lim]);
+    acc_mac<WIDE>(m0, a0s, v0);
+    acc_mac<WIDE>(m1, a0s, v1);
+    acc_mac<WIDE>(m1, a1s, v0);
+    acc_mac<WIDE>(m2, a1s, v1);
+    if (++since == 4 || j + 1 == a.n_k) {  // m1 holds the 8 products its columns take
+      r0 = add_mod(r0, acc_reduce<WIDE>(m0, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+      r1 = add_mod(r1, acc_reduce<WIDE>(m1, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+      r2 = add_mod(r2, acc_reduce<WIDE>(m2, pc.q, pc.r64, pc.r64p, pc.inv1), pc.q);
+      m0 = m1 = m2 = AccT<WIDE>{};
+      since = 0;
+    }
   }
   uint64_t* o = a.num + (uint64_t)b * 3 * lim + off;
   o[0] = drop_out(r0, a.drop, a.nl, i, nullptr, 0, pc.q);
