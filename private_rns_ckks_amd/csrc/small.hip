@@ -26,7 +26,8 @@ namespace {
 
 using namespace nttc;
 
-// A workgroup's T threads hold W words each; a transform runs in rounds of
+// A workgroup's T threads hold W words each (4: with 8, and a third fewer
+// rounds, a step of 5 limbs takes 226 us instead of 211); a transform runs in rounds of
 // LOGW stages in registers with an exchange through LDS between them, the
 // round at stride 1 taking the LAST stages that are left.
 template <int LOGN>
@@ -130,6 +131,18 @@ __device__ __forceinline__ void from_lds(uint64_t (&x)[Ring<LOGN>::W], const uin
   }
 }
 
+// Between the writes of one round's layout and the reads of another's, of which
+// the round at DONE has the larger blocks.  Blocks of 64 W words whose rounds
+// use one group of W words per thread belong to one wave, which waits for its
+// own writes; others for the workgroup's.  The writes after the reads need no
+// wait: a thread writes the words it has read.  A stage of radix 8 on 4 limbs at
+// N = 2^12 takes 49.1 us with two workgroup barriers an exchange, 46.3 us so.
+template <int LOGN, int DONE, int R>
+__device__ __forceinline__ void exchange_wait() {
+  if constexpr (R == Ring<LOGN>::LOGW && (Ring<LOGN>::N >> DONE) <= 64 * Ring<LOGN>::W) wave_lds_wait();
+  else __syncthreads();
+}
+
 // Forward transform: x enters in the first round's layout (word k at thread +
 // k T) and leaves in the last one's: word ((thread + g T) << LAST) + k.  t: the
 // round's twiddles; the next round's load while this one computes.
@@ -140,9 +153,8 @@ __device__ __forceinline__ void forward_rounds(uint64_t (&x)[Ring<LOGN>::W], con
   if constexpr (NEXT < LOGN) {
     const RoundTw<LOGN, RN> tn = round_twiddles<LOGN, RN, NEXT>(tw);
     forward_round<LOGN, R, AR>(x, t, q);
-    if (DONE > 0) __syncthreads();  // the previous exchange has been read
     to_lds<LOGN, R, DONE>(x, lds);
-    __syncthreads();
+    exchange_wait<LOGN, DONE, RN>();
     from_lds<LOGN, RN, NEXT>(x, lds);
     forward_rounds<LOGN, AR, NEXT, RN>(x, tn, lds, tw, q);
   } else {
@@ -158,9 +170,8 @@ __device__ __forceinline__ void inverse_rounds(uint64_t (&x)[Ring<LOGN>::W], con
   if constexpr (DONE > 0) {
     const RoundTw<LOGN, LOGW> tn = round_twiddles<LOGN, LOGW, DONE - LOGW>(tw);
     inverse_round<LOGN, R, AR>(x, t, q);
-    if (DONE + R < LOGN) __syncthreads();
     to_lds<LOGN, R, DONE>(x, lds);
-    __syncthreads();
+    exchange_wait<LOGN, DONE - LOGW, R>();
     from_lds<LOGN, LOGW, DONE - LOGW>(x, lds);
     inverse_rounds<LOGN, AR, DONE - LOGW, LOGW>(x, tn, lds, tw, q);
   } else {
