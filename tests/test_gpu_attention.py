@@ -443,6 +443,78 @@ def test_two_contexts_on_two_streams(lib, orc, sets):
     made[1][0].close()
 
 
+def test_calls_in_a_row_without_waiting(lib, orc, sets):
+    """Mixes and chunks on one stream with nothing waited for between them: the steps on the internal stream
+    start after the call before has finished with the context's buffers."""
+    torch = torch_cuda()
+    ctx, P = sets("mid")
+    announce("calls in a row")
+    st, ref_st = steps(lib, P, [2])
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    lv, n, made = 5, 6, []
+    for i in range(4):
+        c = {t: words(P, i, "row" + t, n, (2, 1, 2)) for t in "avqkx"}
+        p = {t: words(P, i, "row" + t, n, (2, 1)) for t in "mwr"}
+        car, s_in = words(P, i, "rowc", n - 2, (1,)), words(P, i, "rows", n - 2, (1, 2))
+        made.append((c, p, car, s_in, {t: to_dev(x) for t, x in {**c, **p}.items()}, to_dev(car), to_dev(s_in),
+                     empty_dev((1, 2, lv - 1, P.N)), empty_dev((1, 2, lv, P.N)), empty_dev((2, 1, 2, lv - 2, P.N)),
+                     empty_dev((1, 2, lv - 2, P.N))))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for c, p, car, s_in, d, d_car, d_s, num, den, y, end in made:
+            lib.ckks_attn_mix(ctx, d["a"], 1, d["v"], 2, 1, d["m"], 1, lv, d_rlk, st, num, den)
+            lib.ckks_linattn_chunk(ctx, d["q"], d["k"], d["x"], 2, 1, d["w"], d["r"], d_car, 1, d_s, lv, d_rlk, st, y,
+                                   end)
+    side.synchronize()
+    for i, (c, p, car, s_in, d, d_car, d_s, num, den, y, end) in enumerate(made):
+        rn, rd = orc.attn_mix(P, lv, c["a"][None, None, :, 0], c["v"][None, :, 0], p["m"][None, :, 0], rlk, *ref_st)
+        same(num, rn[0], "num %d" % i)
+        same(den, rd[0], "den %d" % i)
+        ry, rs = orc.linattn_chunk(P, lv, c["q"], c["k"], c["x"], p["w"], p["r"], car, s_in, rlk, *ref_st)
+        same(y, ry, "y %d" % i)
+        same(end, rs, "state %d" % i)
+
+
+def test_one_buffer_as_several_operands(lib, orc, sets):
+    """Inputs may be one another: self-products, and one key as the relinearisation's and a rotation's."""
+    ctx, P = sets("small")
+    announce("one buffer as several operands")
+    gal, host = [[P.galois(1)]], [[key(P, 3, "both")]]
+    d_key = to_dev(host[0][0])
+    st = lib.RotateSum(gal, [[d_key]])
+    x = words(P, 3, "self", 6, (2, 2))
+    dx = to_dev(x)
+    out = empty_dev((1, 2, 2, 2, 5, P.N))
+    lib.ckks_attn_scores(ctx, dx, 2, dx, 2, 1, 5, d_key, st, out)
+    same(out, orc.attn_scores(P, 5, x[None], x[None], host[0][0], gal, host))
+    y, s_out = empty_dev((2, 2, 4, P.N)), empty_dev((2, 2, 5, P.N))
+    pt = words(P, 3, "selfpt", 6, (1,))
+    lib.ckks_linattn_step(ctx, dx, dx, dx, 2, to_dev(pt), 1, dx, 5, d_key, st, y, s_out)
+    ref = orc.linattn_step(P, 5, x, x, x, pt, x, host[0][0], gal, host)
+    same(y, ref[0])
+    same(s_out, ref[1])
+
+
+def test_traced_families(lib, orc, sets):
+    """The families of the attention kernels count their launches, on the internal stream too."""
+    ctx, P = sets("mid")
+    announce("traced families")
+    st, _ = steps(lib, P, [2, 2])
+    rlk = to_dev(key(P, 0, "rlk"))
+    a, v = to_dev(words(P, 1, "ta", 4, (1, 2))), to_dev(words(P, 1, "tv", 4, (1, 2)))
+    num, den = empty_dev((1, 2, 3, P.N)), empty_dev((1, 2, 4, P.N))
+    counts = {}
+    for family in ("sum_ip", "attn_mac"):
+        lib.ckks_trace_begin(ctx, family)
+        lib.ckks_attn_mix(ctx, a, 1, v, 1, 1, None, 0, 3, rlk, st, num, den)
+        t = lib.ckks_trace_end(ctx)
+        counts[family] = t["launches"]
+        assert t["work_units"] > 0
+    assert counts == {"sum_ip": 4, "attn_mac": 1}
+
+
 def test_captured_step_replays(lib, orc):
     """A step captured into a graph after one eager call: every replay equals the eager words, with new
     inputs, with eager work of the same context between the replays, and after a larger call has grown the
