@@ -26,18 +26,21 @@ int key_ip(Ctx* c, hipStream_t s, int level, int n, const uint64_t* E, uint64_t 
 int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
                int batch, int level, const ckks_sum_steps& st, uint64_t* ws);
 
-// out[b] = p[row] * in[b] on both components, limbs 0..nl-1; b = t * ng +
-// g reads in + (t * n_grp + g)*in_bstride and
-// row t * n_row + (g0 + g) % n_row.
-struct PlainMulArgs {
+// rescale(p[row] * in[b]) by the top limb `level`; b = t * ng + g (first + the
+// launch's item) reads in + (t * n_grp + g)*in_bstride and row t * n_row +
+// (g0 + g) % n_row.
+struct PlainMul {
   const uint64_t* in;  // component stride in_comp
-  const uint64_t* p;   // [..][nl][N]
-  uint64_t* out;       // item b at + b*out_bstride, [2][nl][N]
+  const uint64_t* p;   // [..][level+1][N]
+  uint64_t* out;       // item b at + b*out_bstride, [2][level][N]
   uint64_t in_bstride, in_comp, out_bstride;
-  const PrimeConst* prime;
-  int log_n, nl, ng, n_grp, n_row, g0;
+  int level, ng, n_grp, n_row, g0, first;
 };
-int launch_plain_mul(Ctx* c, hipStream_t s, const PlainMulArgs& a, int batch);
+// Limb `level` of the product, [2][N] per item at out + b*out_bstride.
+int launch_plain_mul(Ctx* c, hipStream_t s, const PlainMul& m, uint64_t* out, uint64_t out_bstride, int batch);
+// The rest (rescale.hip): v = iNTT of that limb, w scratch [2][level][N], per
+// words between items of either.
+int rescale_mul_fused(Ctx* c, hipStream_t s, const PlainMul& m, const uint64_t* v, uint64_t* w, uint64_t per, int batch);
 
 // What the products below do to their output for ks_rescale: parts 0 and 1 of
 // the limbs that stay after `drop` rescales are multiplied by the inverses of

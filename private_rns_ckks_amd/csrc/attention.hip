@@ -134,6 +134,24 @@ struct Tail {
                       out + b0 * 2 * limb(level - drop), 2 * limb(level - drop), ws);
     return rc;
   }
+  uint64_t mul_words(int n, int level) const { return (uint64_t)c->N * (4 + 2 * level) * std::min(n, kMaxChunk); }
+  // rescale(p in), n items; per item of the workspace the dropped limb's
+  // product, its inverse transform, the converted limbs
+  int mul_rescale(PlainMul m, int n) const {
+    const uint64_t N = c->N, per = N * (4 + 2 * m.level);
+    const int chunk = (int)std::max<uint64_t>(1, std::min<uint64_t>(kMaxChunk, ws_words / per));
+    NttJobs jobs;
+    for (int comp = 0; comp < 2; ++comp) jobs.add(comp, comp, m.level);
+    int rc = CKKS_OK;
+    for (m.first = 0; m.first < n && rc == CKKS_OK; m.first += chunk) {
+      const int k = std::min(chunk, n - m.first);
+      if ((rc = launch_plain_mul(c, s, m, ws, per, k)) ||
+          (rc = ntt_run(c, s, ws, ws + 2 * N, per, per, k, jobs, true, true)) ||
+          (rc = rescale_mul_fused(c, s, m, ws + 2 * N, ws + 4 * N, per, k)))
+        break;
+    }
+    return rc;
+  }
   int rescale(const uint64_t* R, uint64_t* Z, int n, int level) const {
     return rescale_batch(c, s, R, 2 * limb(level), Z, 2 * limb(level - 1), n, level, ws, ws_words);
   }
@@ -388,17 +406,16 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
     return rc;
   if (n_grp == 0) return CKKS_OK;
   CaptureScope cap(c, s);
-  // per (token, group): X (then the state's product), R = r q and C its
-  // rescale, S the states, Z the outputs before the sum; per group: the prefix
-  // sums carried from one block of tokens to the next
-  const uint64_t mid = 2ull * l * N, per = 3 * lim + (r ? ct + mid : 0) + sct + yct;
-  const int gb = block_items(per + 3 * lim + sct, n_grp);
+  // per (token, group): X (then the state's product), C the rescaled r q, S
+  // the states, Z the outputs before the sum; per group: the prefix sums carried
+  // from one block of tokens to the next
+  const uint64_t mid = 2ull * l * N, per = 3 * lim + (r ? mid : 0) + sct + yct;
+  const int gb = block_items(per + 3 * lim, n_grp);
   const int tb = std::min(block_items((per + 3 * lim) * gb, n_tok), std::max(1, 8192 / gb));  // one launch's items
   const uint64_t nb = (uint64_t)gb * tb;
-  if ((rc = ensure_aux(c, per * nb + (3 * lim + sct) * gb))) return rc;
-  uint64_t *X = c->aux, *S = X + 3 * lim * nb, *Z = S + sct * nb, *R = Z + yct * nb, *C = R + (r ? ct * nb : 0),
-           *P = C + (r ? mid * nb : 0), *V = P + 3 * lim * gb;
-  const uint64_t side_words = std::max(r ? t.rescale_words((int)nb, l) : 0, carry ? t.rescale_words(gb, l - 2) : 0);
+  if ((rc = ensure_aux(c, per * nb + 3 * lim * gb))) return rc;
+  uint64_t *X = c->aux, *S = X + 3 * lim * nb, *Z = S + sct * nb, *C = Z + yct * nb, *P = C + (r ? mid * nb : 0);
+  const uint64_t side_words = std::max(r ? t.mul_words((int)nb, l) : 0, carry ? t.mul_words(gb, l - 2) : 0);
   if ((rc = t.reserve(std::max({t.relin_words((int)nb, l, 2), t.relin_words((int)nb, l - 2, 1),
                                 t.sum_words((int)nb, l - 3)}),
                       side_words)))
@@ -429,22 +446,9 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
       const uint64_t* qt = q + at * ct;
       if (r) {  // rescale(r q) beside the states
         Side side(t, side_words);
-        PlainMulArgs pm;
-        memset(&pm, 0, sizeof(pm));
-        pm.in = qt;
-        pm.in_bstride = ct;
-        pm.in_comp = lim;
-        pm.p = r + (uint64_t)t0 * n_row * lim;
-        pm.out = R;
-        pm.out_bstride = ct;
-        pm.prime = c->d_prime;
-        pm.log_n = (int)c->log_n;
-        pm.nl = l + 1;
-        pm.ng = ng;
-        pm.n_grp = n_grp;
-        pm.n_row = n_row;
-        pm.g0 = g0;
-        if ((rc = side.rc) || (rc = launch_plain_mul(c, side.tail.s, pm, n)) || (rc = side.tail.rescale(R, C, n, l)))
+        if ((rc = side.rc) ||
+            (rc = side.tail.mul_rescale(
+                 {qt, r + (uint64_t)t0 * n_row * lim, C, ct, lim, mid, l, ng, n_grp, n_row, g0, 0}, n)))
           return rc;
         if ((rc = launch_scan(c, s, sc)) || (rc = t.relin_rescale(X, S, n, l, 2)) || (rc = side.join())) return rc;
         if ((rc = state_times_q(t, S, C, mid, mid / 2, 1, 1, X, n, l - 2))) return rc;
@@ -458,22 +462,10 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
         CKKS_HIP_CHECK(hipMemcpyAsync(state_out + g0 * sct, last, sct * ng * 8, hipMemcpyDeviceToDevice, s));
       if (end && carry) {  // rescale(carry S) beside the outputs
         Side side(t, side_words);
-        PlainMulArgs pm;
-        memset(&pm, 0, sizeof(pm));
-        pm.in = last;
-        pm.in_bstride = sct;
-        pm.in_comp = sct / 2;
-        pm.p = carry;
-        pm.out = V;
-        pm.out_bstride = sct;
-        pm.prime = c->d_prime;
-        pm.log_n = (int)c->log_n;
-        pm.nl = l - 1;
-        pm.ng = pm.n_grp = ng;
-        pm.n_row = n_row;
-        pm.g0 = g0;
-        if ((rc = side.rc) || (rc = launch_plain_mul(c, side.tail.s, pm, ng)) ||
-            (rc = side.tail.rescale(V, state_out + g0 * yct, ng, l - 2)) || (rc = outputs(t, X, Z, y, at, nt, ng, n_grp, l)) ||
+        if ((rc = side.rc) ||
+            (rc = side.tail.mul_rescale({last, carry, state_out + g0 * yct, sct, sct / 2, yct, l - 2, ng, ng, n_row, g0, 0},
+                                        ng)) ||
+            (rc = outputs(t, X, Z, y, at, nt, ng, n_grp, l)) ||
             (rc = side.join()))
           return rc;
       } else if ((rc = outputs(t, X, Z, y, at, nt, ng, n_grp, l))) {

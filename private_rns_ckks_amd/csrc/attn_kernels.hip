@@ -37,21 +37,28 @@ __device__ __forceinline__ uint64_t drop_out(uint64_t x, const DropOut& d, int n
   return add ? add_mod(x, add[add_off], q) : x;
 }
 
-// A plaintext row times both components.  Memory: 2 items of 24 limbs at N =
-// 2^16, 126 MB in 25 us (5.0 TB/s).
+struct TopMulArgs {
+  PlainMul m;
+  uint64_t* out;
+  uint64_t out_bstride;
+  const PrimeConst* prime;
+  int log_n;
+};
+
+// The limb of a product with a plaintext row that its rescale drops; the other
+// limbs' products are formed where the rescale reads them.
 template <bool WIDE>
-__global__ __launch_bounds__(256) void plain_mul_kernel(PlainMulArgs a) {
+__global__ __launch_bounds__(256) void plain_mul_kernel(TopMulArgs a) {
   const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
-  const int i = blockIdx.y, b = blockIdx.z;
-  const RedConst pc = red_const((ConstPrime)a.prime, i);
-  const uint64_t off = ((uint64_t)i << a.log_n) + c, lim = (uint64_t)a.nl << a.log_n;
-  const int t = b / a.ng, g = b % a.ng;
-  const uint64_t row = (uint64_t)t * a.n_row + (a.g0 + g) % a.n_row;
-  const Split<WIDE> p = split_word<WIDE>(a.p[row * lim + off]);
-  const uint64_t* x = a.in + ((uint64_t)t * a.n_grp + g) * a.in_bstride + off;
-  uint64_t* o = a.out + b * a.out_bstride + off;
+  const int l = a.m.level, b = blockIdx.z, t = (a.m.first + b) / a.m.ng, g = (a.m.first + b) % a.m.ng;
+  const RedConst pc = red_const((ConstPrime)a.prime, l);
+  const uint64_t off = ((uint64_t)l << a.log_n) + c, lim = (uint64_t)(l + 1) << a.log_n;
+  const uint64_t row = (uint64_t)t * a.m.n_row + (a.m.g0 + g) % a.m.n_row;
+  const Split<WIDE> p = split_word<WIDE>(a.m.p[row * lim + off]);
+  const uint64_t* x = a.m.in + ((uint64_t)t * a.m.n_grp + g) * a.m.in_bstride + off;
+  uint64_t* o = a.out + b * a.out_bstride + c;
   o[0] = mul_red<WIDE>(p, split_word<WIDE>(x[0]), pc);
-  o[lim] = mul_red<WIDE>(p, split_word<WIDE>(x[a.in_comp]), pc);
+  o[1ull << a.log_n] = mul_red<WIDE>(p, split_word<WIDE>(x[a.m.in_comp]), pc);
 }
 
 // (x0, x1) x (y0, y1) = (x0 y0, x0 y1 + x1 y0, x1 y1), plus a row times a
@@ -269,9 +276,13 @@ __global__ __launch_bounds__(256) void mix_kernel(MixArgs a) {
   CKKS_HIP_CHECK(hipGetLastError());                                                                         \
   return CKKS_OK
 
-int launch_plain_mul(Ctx* c, hipStream_t s, const PlainMulArgs& a, int batch) {
-  TraceScope ts(c, s, "attn_mac", (double)batch * a.nl * 4 * c->N);
-  ATTN_LAUNCH(plain_mul_kernel, batch);
+int launch_plain_mul(Ctx* c, hipStream_t s, const PlainMul& m, uint64_t* out, uint64_t out_bstride, int batch) {
+  const TopMulArgs a{m, out, out_bstride, c->d_prime, (int)c->log_n};
+  TraceScope ts(c, s, "attn_mac", (double)batch * 4 * c->N);
+  hipLaunchKernelGGL(c->wide ? plain_mul_kernel<true> : plain_mul_kernel<false>, dim3(c->N / 256, 1, batch), dim3(256),
+                     0, s, a);
+  CKKS_HIP_CHECK(hipGetLastError());
+  return CKKS_OK;
 }
 
 int launch_pair(Ctx* c, hipStream_t s, const PairArgs& a, int batch) {

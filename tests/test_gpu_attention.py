@@ -366,6 +366,21 @@ def test_blocks_of_items_and_tokens(lib, orc, sets):
     assert torch.equal(first, y2)
 
 
+def test_chunk_of_more_items_than_a_launch(lib, orc, sets):
+    """66 tokens of 2 groups with read weights and a carry, each group its own rows: products, rescales and
+    relinearisations go in several launches."""
+    ctx, P = sets("small")
+    announce("chunk of 132 items")
+    st, ref_st = steps(lib, P, [2])
+    rlk = key(P, 0, "rlk")
+    T, G = 66, 2
+    d = chunk_case(P, 3, T, G, 2, True, True, True, 6)
+    y, out = run_chunk(lib, ctx, P, d, 3, T, G, 2, rlk, st)
+    ref = orc.linattn_chunk(P, 3, d["q"], d["k"], d["v"], d["w"], d["r"], d["carry"], d["state"], rlk, *ref_st)
+    same(y, ref[0])
+    same(out, ref[1])
+
+
 def test_small_blocks(lib, orc, sets, monkeypatch):
     """Intermediates limited to 1 MiB: every call runs in blocks of one or two items, a chunk's tokens in
     several blocks that carry the prefix sums, its groups in several blocks whose outputs interleave."""
