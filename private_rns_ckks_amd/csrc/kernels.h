@@ -106,9 +106,9 @@ int drop_col_pass(Ctx* c, hipStream_t s, uint64_t* A, uint64_t* W, uint64_t per,
 // ks_rescale take there: `per` is the distance between items of the workspace.
 // The rule for n items: N <= 2^12 and n limbs of n * (level + 1) * N <= 2^21
 // words, past which one workgroup per limb loses to the two-pass kernels' finer
-// tiles.  A stage of radix 8: 34 against 56 us for 1 item of 5 limbs at N =
-// 2^10, 68 against 129 us for 16 items of 12 limbs at N = 2^11, 97 against 146
-// us for 32 items of 4 limbs at N = 2^12; 459 against 421 us for 128 items of 8
+// tiles.  A stage of radix 8: 32 against 56 us for 1 item of 5 limbs at N =
+// 2^10, 67 against 129 us for 16 items of 12 limbs at N = 2^11, 91 against 146
+// us for 32 items of 4 limbs at N = 2^12; 438 against 427 us for 128 items of 8
 // limbs there.  At N = 2^13 one item of 5 limbs took 98 us against 68.
 inline bool small_ring(const Ctx* c, int level, int n) {
   return c->log_n <= 12 && (uint64_t)n * (level + 1) * c->N <= (1u << 21);
