@@ -182,7 +182,7 @@ class Side {
  public:
   Side(const Tail& t, uint64_t side_words) : tail(t), c_(t.c), s_(t.s) {
     rc = start();
-    tail.s = c_->lane[0];
+    if (open_) tail.s = c_->lane[0];
     tail.ws = t.ws + t.ws_words;
     tail.ws_words = side_words;
   }
@@ -199,6 +199,7 @@ class Side {
 
  private:
   int start() {
+    if (internal_lanes() < 2) return CKKS_OK;  // on the caller's stream, one after the other
     int r = ensure_lanes(c_);
     if (r) return r;
     CKKS_HIP_CHECK(hipEventRecord(c_->fork_ev, s_));

@@ -19,6 +19,10 @@ int rescale_batch(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride,
                   int batch, int level, uint64_t* ws, uint64_t ws_words, const uint64_t* add0 = nullptr,
                   const uint64_t* acc = nullptr);
 
+// Internal streams a call may use at once (CKKS_LANES); 1: none, everything runs
+// on the caller's.
+int internal_lanes();
+
 // device buffers are read and written with 16-byte vector accesses
 inline bool misaligned(const void* p) { return ((uintptr_t)p & 15) != 0; }
 

@@ -37,6 +37,12 @@ int g_chunk_default() {
   return v;
 }
 
+}  // namespace
+
+int internal_lanes() { return g_lanes_default(); }
+
+namespace {
+
 uint32_t inv_mod_2n(uint32_t g, uint32_t two_n) {
   uint32_t x = g;  // Newton iteration for the inverse of an odd number modulo a power of two
   for (int i = 0; i < 5; ++i) x *= 2 - g * x;
