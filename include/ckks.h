@@ -442,9 +442,14 @@ int ckks_attn_mix(ckks_ctx* ctx, const uint64_t* d_a, int n_q, const uint64_t* d
  *   S_t   = state_in + rescale(rescale(relin(X_t)))               level-2
  *   y_t   = Sum(rescale(relin(rescale(r_t q_t) x S_t)))           level-3
  *   state_out = rescale(carry S_{n_tok-1})  (level-3), or S_{n_tok-1} (level-2)
- * With decay gamma per head, w_u = gamma^-u, r_t = gamma^t and carry =
- * gamma^n_tok give S_t = gamma^t state_in + sum gamma^(t-u) k_u v_u as read by
- * y_t, at two levels however long the chunk is.
+ * With decay gamma per head, w_u = gamma^-(u+1), r_t = gamma^(t+1) and carry =
+ * gamma^n_tok: y_t reads r_t S_t = gamma^(t+1) state_in + sum_{u <= t}
+ * gamma^(t-u) k_u v_u, the state that ckks_linattn_step with d_decay = gamma
+ * forms token by token from state_in, the state after the token before the
+ * chunk; state_out is that state after token n_tok-1, which the next chunk or
+ * step takes.  Decays that change from token to token: w_u = 1 / (d_0 .. d_u),
+ * r_t = d_0 .. d_t, carry = d_0 .. d_(n_tok-1).  The state takes two levels
+ * (carried on: three) however many tokens the chunk has.
  *   d_q, d_k, d_v  [n_tok][n_grp][2][level+1][N]
  *   d_w, d_r       [n_tok][n_row][level+1][N] plaintexts; d_r may be NULL
  *                  (q_t's limbs 0..level-2 as they are)

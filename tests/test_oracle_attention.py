@@ -19,6 +19,8 @@ sqrt(N h) sigma < 2^11 in units of one coefficient (N = 2^10, h = 64, sigma =
 a decode sums N coefficients in quadrature (2^5): 2^(11 + 10 + 5 - 48) = 2^-22
 of a unit value, and the outputs' largest value is at least 1."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -27,6 +29,7 @@ import ckks_synth as S
 from helpers import encrypt_slots, galois_key, params, rel_err, relin_key, secret
 
 TOL = 2.0 ** -20
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 class Scheme:
@@ -257,3 +260,47 @@ def test_binding_refuses_before_the_library(lib):
 def test_sum_steps_structure_matches_the_header(lib):
     assert ctypes.sizeof(lib.ckks_sum_steps) == 32
     assert [f[0] for f in lib.ckks_sum_steps._fields_] == ["n_stage", "radix", "galois_elts", "d_evks"]
+
+
+# ---------------------------------------------------------------- the documented weights
+
+def header_weights():
+    """Exponents of gamma that include/ckks.h gives the chunk's plaintexts, as functions of (u or t, n_tok)."""
+    text = " ".join(line.strip(" *\n") for line in open(os.path.join(ROOT, "include", "ckks.h")))
+    m = re.search(r"w_u = gamma\^(\S+), r_t = gamma\^(\S+) and carry = gamma\^(\w+)", text)
+    assert m, "include/ckks.h no longer states the weights of a chunk"
+    code = [compile(e, "ckks.h", "eval") for e in m.groups()]
+    return [lambda i, n, c=c: eval(c, {"u": i, "t": i, "n_tok": n}) for c in code]
+
+
+def test_a_prompt_by_the_documented_weights_continues_in_single_tokens(orc, sch):
+    """A chunk with the header's w, r and carry, then steps with d_decay = gamma: one recurrence from the state
+    before the prompt to the last token, the state that the chunk hands over among its values."""
+    n, F, heads, T, lv = sch.n, 8, 4, 3, 7
+    q, k, v, g = linear_attention(n, F, heads, 12, T + 2)
+    q_mod = [float(x) for x in sch.P.q]
+    gal, keys = sch.steps(n // F, [2, 4])
+    start = S.uniform_slots(S.stream(12, "state"), n, False).real
+    s_state = sch.scale ** 3 / q_mod[lv] / q_mod[lv - 1]
+    ct = lambda x, tag: np.stack([sch.enc(a, lv, tag + str(i))[None] for i, a in enumerate(x)])
+    e_w, e_r, e_carry = header_weights()
+    w = np.stack([sch.pt(g ** float(e_w(t, T)), lv)[None] for t in range(T)])
+    r = np.stack([sch.pt(g ** float(e_r(t, T)), lv)[None] for t in range(T)])
+    carry = np.stack([sch.pt(g ** float(e_carry(None, T)), lv - 2)])
+    y, cur = orc.linattn_chunk(sch.P, lv, ct(q[:T], "pq"), ct(k[:T], "pk"), ct(v[:T], "pv"), w, r, carry,
+                               sch.enc(start, lv - 2, "pst", s_state)[None], sch.rlk, gal, keys)
+    ref_y, ref = recurrence(q[:T], k[:T], v[:T], g, F, start)
+    s_y = sch.scale ** 2 / q_mod[lv] * s_state / q_mod[lv - 2]
+    for t in range(T):
+        assert rel_err(sch.dec(y[t, 0], s_y), ref_y[t]) < TOL
+    s_in, lv2 = s_state * sch.scale / q_mod[lv - 2], lv - 3
+    assert rel_err(sch.dec(cur[0], s_in), ref) < TOL
+    for t in range(T, T + 2):
+        dec = np.stack([sch.pt(g, lv2, sch.scale ** 2 / s_in)])
+        one = lambda x, tag: sch.enc(x[t], lv2, "p" + tag + str(t))[None]
+        yt, cur = orc.linattn_step(sch.P, lv2, one(q, "q"), one(k, "k"), one(v, "v"), dec, cur, sch.rlk, gal, keys)
+        s_in = sch.scale ** 2 / q_mod[lv2]
+        ref_yt, ref = recurrence(q[t: t + 1], k[t: t + 1], v[t: t + 1], g, F, ref)
+        assert rel_err(sch.dec(yt[0], sch.scale * s_in / q_mod[lv2 - 1]), ref_yt[0]) < TOL
+        assert rel_err(sch.dec(cur[0], s_in), ref) < TOL
+        lv2 -= 1
