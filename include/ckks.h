@@ -450,6 +450,15 @@ int ckks_attn_mix(ckks_ctx* ctx, const uint64_t* d_a, int n_q, const uint64_t* d
  * step takes.  Decays that change from token to token: w_u = 1 / (d_0 .. d_u),
  * r_t = d_0 .. d_t, carry = d_0 .. d_(n_tok-1).  The state takes two levels
  * (carried on: three) however many tokens the chunk has.
+ * How long a chunk may be: S_t is held up to gamma^-n_tok times larger than
+ * the state it stands for, h = n_tok log2(1 / gamma) bits for the smallest
+ * gamma (18.5 for 0.875 and 96 tokens).  They are taken twice: from the
+ * modulus (the largest slot of S_t times its scale stays below q_0 .. q_(l-2)
+ * / 2, and of state_out's product before its rescale likewise), and from the
+ * precision: the errors of r_t q_t (the rescale's, and r_t's and carry's
+ * rounding to their scale) are multiplied by S_t, so outputs and carried
+ * state keep h bits less than those of single steps.  A longer prompt goes in
+ * several chunks, each from the state_out of the one before.
  *   d_q, d_k, d_v  [n_tok][n_grp][2][level+1][N]
  *   d_w, d_r       [n_tok][n_row][level+1][N] plaintexts; d_r may be NULL
  *                  (q_t's limbs 0..level-2 as they are)

@@ -304,3 +304,29 @@ def test_a_prompt_by_the_documented_weights_continues_in_single_tokens(orc, sch)
         assert rel_err(sch.dec(yt[0], sch.scale * s_in / q_mod[lv2 - 1]), ref_yt[0]) < TOL
         assert rel_err(sch.dec(cur[0], s_in), ref) < TOL
         lv2 -= 1
+
+
+@pytest.mark.parametrize("strongest", [0.875, 0.5])
+def test_a_chunk_loses_the_bits_of_its_decays(orc, sch, strongest):
+    """The documented length of a chunk: with S_t up to gamma^-T larger than the state, the outputs of T tokens
+    keep log2(gamma^-T) bits less than TOL gives for values of order 1: the errors that TOL bounds (2^-22 of a unit)
+    meet a factor of at most gamma^-T (the sum's 2^10 terms, which TOL allows for, cover the state's size of a few
+    units).  At 0.875 that is 1.5 bits, at 0.5 it is 8."""
+    n, F, heads, T, lv = sch.n, 8, 4, 8, 5
+    q, k, v, _ = linear_attention(n, F, heads, 13, T)
+    gamma = np.linspace(strongest, 1.0, heads)
+    g = np.broadcast_to(gamma[None, :, None], (F, heads, n // F // heads)).reshape(n)
+    q_mod = [float(x) for x in sch.P.q]
+    gal, keys = sch.steps(n // F, [8])
+    ct = lambda x, tag: np.stack([sch.enc(a, lv, tag + str(i))[None] for i, a in enumerate(x)])
+    e_w, e_r, e_carry = header_weights()
+    w = np.stack([sch.pt(g ** float(e_w(t, T)), lv)[None] for t in range(T)])
+    r = np.stack([sch.pt(g ** float(e_r(t, T)), lv)[None] for t in range(T)])
+    carry = np.stack([sch.pt(g ** float(e_carry(None, T)), lv - 2)])
+    y, cur = orc.linattn_chunk(sch.P, lv, ct(q, "lq"), ct(k, "lk"), ct(v, "lv"), w, r, carry, None, sch.rlk, gal, keys)
+    s_state = sch.scale ** 3 / q_mod[lv] / q_mod[lv - 1]
+    s_y = sch.scale ** 2 / q_mod[lv] * s_state / q_mod[lv - 2]
+    ref_y, ref = recurrence(q, k, v, g, F, np.zeros(n))
+    for t in range(T):
+        assert rel_err(sch.dec(y[t, 0], s_y), ref_y[t]) < TOL * strongest ** -(t + 1)
+    assert rel_err(sch.dec(cur[0], s_state * sch.scale / q_mod[lv - 2]), ref) < TOL * strongest ** -T
