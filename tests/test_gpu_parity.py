@@ -811,3 +811,53 @@ def test_repeatable(lib, orc, c3small):
     lib.ckks_rotate(ctx, d, o1, 4, level, gs, keys)
     lib.ckks_rotate(ctx, d, o2, 4, level, gs, keys)
     assert np.array_equal(to_host(o1), to_host(o2))
+
+
+# Key switches that raise more limbs than one launch of transforms lists
+# (160), on every call that raises digits by the two passes: 14 digits of one
+# limb (196 transforms at the top level), 8 digits of 5 (320, two full
+# launches), 64 digits of one (4096), and a ring past the one-workgroup
+# transforms' limit.
+MANY_TRANSFORMS = [
+    # log_n, L, q_bits, K, p_bits, dnum, levels
+    (10, 14, 50, 1, 60, 14, (13, 12)),
+    (10, 40, 50, 5, 60, 8, (39, 28)),
+    (10, 64, 54, 1, 60, 64, (63,)),
+    (13, 14, 54, 1, 60, 14, (13,)),
+]
+
+
+@pytest.mark.parametrize("shape", MANY_TRANSFORMS, ids=lambda s: "logn%d_L%d_K%d_dnum%d" % (s[0], s[1], s[3], s[5]))
+def test_more_transforms_than_a_launch_lists(lib, orc, shape):
+    log_n, L, q_bits, K, p_bits, dnum, levels = shape
+    ctx, P = make_pair(lib, orc, log_n, L, q_bits, K, p_bits, dnum)
+    keys = [S.uniform_limbs(S.stream(b, "gpu/many/k"), P.mods, P.N, lead=(P.dnum, 2)) for b in range(2)]
+    d_keys = [to_dev(k) for k in keys]
+    gs = [P.galois(1), P.galois(P.N // 2 - 5)]
+    for level in levels:
+        nq = level + 1
+        assert P.beta(level) * (nq + K) - nq > 160
+        announce("many transforms %s level=%d" % (shape[:6], level))
+        ct = S.uniform_limbs(S.stream(level, "gpu/many/ct"), P.q[:nq], P.N, lead=(2, 2))
+        d_ct = to_dev(ct)
+        out = empty_dev((2, nq, P.N))
+        lib.ckks_keyswitch(ctx, d_ct[0, 1].contiguous(), d_keys[0], out, level)
+        assert np.array_equal(to_host(out), orc.keyswitch(P, level, ct[0, 1], keys[0])), "keyswitch"
+        out = empty_dev(ct.shape)
+        lib.ckks_rotate(ctx, d_ct, out, 2, level, gs, d_keys)
+        assert np.array_equal(to_host(out), orc.rotate_batch(P, level, ct, gs, keys)), "rotate"
+        out = empty_dev((1, 2) + ct.shape[1:])
+        lib.ckks_rotate_hoisted(ctx, d_ct[:1].contiguous(), 1, level, gs, d_keys, out)
+        assert np.array_equal(to_host(out)[0], orc.rotate_hoisted(P, level, ct[0], gs, keys)), "hoisted"
+        out = empty_dev((1, 2, level, P.N))
+        lib.ckks_mul_relin_rescale(ctx, d_ct[:1].contiguous(), d_ct[1:].contiguous(), d_keys[0], out, 1, level)
+        assert np.array_equal(to_host(out), orc.mul_relin_rescale(P, level, ct[:1], ct[1:], keys[0])), "product"
+        out = empty_dev(ct.shape)
+        lib.ckks_rotate_sum(ctx, d_ct, out, 2, level, lib.RotateSum([gs], [d_keys]))
+        for b in range(2):
+            assert np.array_equal(to_host(out)[b], orc.rotate_sum(P, level, ct[b], [gs], [keys])), "sum"
+        out = empty_dev((1, 1, 1, 2, level, P.N))
+        lib.ckks_attn_scores(ctx, d_ct[:1].contiguous(), 1, d_ct[1:].contiguous(), 1, 1, level, d_keys[0], None, out)
+        ref = orc.attn_scores(P, level, ct[None, :1], ct[None, 1:], keys[0], [], [])
+        assert np.array_equal(to_host(out), ref), "scores"
+    ctx.close()
