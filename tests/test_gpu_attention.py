@@ -856,3 +856,32 @@ def test_full_size(lib, orc, op):
         same(y, ref[0])
         same(out, ref[1])
     ctx.close()
+
+
+# ---------------------------------------------------------------- forms that the cases above do not reach
+
+SETS["q57low"] = (10, 6, 57, 3, 60, 2)
+
+
+@pytest.mark.parametrize("name,level,T,read,carry,top,mb", [
+    ("small", 5, 40, False, True, False, 8), ("small", 5, 40, True, True, True, 8), ("small", 4, 53, False, False, False, 8),
+    ("q57low", 5, 33, True, False, True, 8), ("wide61", 4, 70, True, True, True, 13), ("wide", 5, 20, True, True, False, 0),
+    ("wide61", 7, 17, False, True, True, 0), ("small", 3, 1040, False, False, False, 0)])
+def test_segmented_prefix_sums(lib, orc, sets, monkeypatch, name, level, T, read, carry, top, mb):
+    """A long chunk of one group: the tokens' prefix sums in segments, with the sums carried from one block of
+    tokens to the next (mb MiB of intermediates, or 1024 tokens, a block), and with primes above 2^60."""
+    ctx, P = sets(name)
+    announce("segments %s level=%d T=%d read=%d carry=%d top=%d mb=%d" % (name, level, T, read, carry, top, mb))
+    block = 1024
+    if mb:
+        monkeypatch.setenv("CKKS_BLOCK_MB", str(mb))
+        limbs = 3 * (level + 1) + (2 * level if read else 0) + 2 * (level - 1) + 2 * (level - 2) + 3 * (level + 1)
+        block = (mb << 17) // (limbs * P.N)
+    assert min(T, block) >= 16 and (T < block or T - block >= 16)  # segments need 16 tokens
+    st, ref_st = steps(lib, P, [2])
+    rlk = key(P, 0, "rlk", top)
+    d = chunk_case(P, level, T, 1, 1, read, carry, True, 40 + T, top)
+    y, out = run_chunk(lib, ctx, P, d, level, T, 1, 1, rlk, st)
+    ref = orc.linattn_chunk(P, level, d["q"], d["k"], d["v"], d["w"], d["r"], d["carry"], d["state"], rlk, *ref_st)
+    same(y, ref[0], "y")
+    same(out, ref[1], "state")
