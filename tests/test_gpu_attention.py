@@ -885,3 +885,52 @@ def test_segmented_prefix_sums(lib, orc, sets, monkeypatch, name, level, T, read
     ref = orc.linattn_chunk(P, level, d["q"], d["k"], d["v"], d["w"], d["r"], d["carry"], d["state"], rlk, *ref_st)
     same(y, ref[0], "y")
     same(out, ref[1], "state")
+
+
+SETS.update({"full": (16, 6, 54, 2, 60, 3), "full57": (16, 4, 57, 2, 60, 2), "fullwide": (16, 4, 62, 2, 61, 2)})
+
+
+@pytest.mark.parametrize("batch,radices", [(2, [3]), (3, [2]), (4, [3]), (5, [2]), (8, [2, 2])])
+def test_full_ring_sums(lib, orc, sets, batch, radices):
+    """N = 2^16: one group of 2 to 4 items a thread of the inner product, and several groups."""
+    ctx, P = sets("full")
+    announce("full ring sum batch=%d" % batch)
+    st, (gal, keys) = steps(lib, P, radices)
+    x = words(P, batch, "fs", 6, (batch, 2))
+    out = empty_dev(x.shape)
+    lib.ckks_rotate_sum(ctx, to_dev(x), out, batch, 5, st)
+    same(out, np.stack([orc.rotate_sum(P, 5, c, gal, keys) for c in x]))
+
+
+@pytest.mark.parametrize("name,level", [("full", 5), ("full57", 3), ("fullwide", 3)])
+def test_full_ring_attention(lib, orc, sets, name, level):
+    """N = 2^16: scores; a masked mix with its normaliser; a chunk with read weights, carry and state; a step:
+    each size's own kernels, on lazy, 57-bit and 62-bit primes."""
+    ctx, P = sets(name)
+    announce("full ring %s" % name)
+    st, ref_st = steps(lib, P, [2])
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    n = level + 1
+    q, k = words(P, 1, "fq", n, (1, 2, 2)), words(P, 1, "fk", n, (1, 1, 2))
+    s = empty_dev((1, 2, 1, 2, level, P.N))
+    lib.ckks_attn_scores(ctx, to_dev(q), 2, to_dev(k), 1, 1, level, d_rlk, st, s)
+    same(s, orc.attn_scores(P, level, q, k, rlk, *ref_st), "scores")
+    a, v, m = words(P, 2, "fa", n, (1, 2, 2, 2)), words(P, 2, "fv", n, (1, 2, 2)), words(P, 2, "fm", n, (1, 2))
+    num, den = empty_dev((1, 2, 2, level - 1, P.N)), empty_dev((1, 2, 2, level, P.N))
+    lib.ckks_attn_mix(ctx, to_dev(a), 2, to_dev(v), 2, 1, to_dev(m), 1, level, d_rlk, st, num, den)
+    ref = orc.attn_mix(P, level, a, v, m, rlk, *ref_st)
+    same(num, ref[0], "num")
+    same(den, ref[1], "den")
+    d = chunk_case(P, level, 2, 1, 1, True, True, True, 3)
+    y, out = run_chunk(lib, ctx, P, d, level, 2, 1, 1, rlk, st)
+    ref = orc.linattn_chunk(P, level, d["q"], d["k"], d["v"], d["w"], d["r"], d["carry"], d["state"], rlk, *ref_st)
+    same(y, ref[0], "chunk y")
+    same(out, ref[1], "chunk state")
+    q, k, v, s_in = (words(P, 4, "f" + t, n, (2, 2)) for t in "qkvs")
+    dec = words(P, 4, "fd", n, (2,))
+    y, out = empty_dev((2, 2, level - 1, P.N)), empty_dev((2, 2, level, P.N))
+    lib.ckks_linattn_step(ctx, to_dev(q), to_dev(k), to_dev(v), 2, to_dev(dec), 2, to_dev(s_in), level, d_rlk, st, y, out)
+    ref = orc.linattn_step(P, level, q, k, v, dec, s_in, rlk, *ref_st)
+    same(y, ref[0], "step y")
+    same(out, ref[1], "step state")
