@@ -4,6 +4,10 @@ through the C interface: every output word must be equal, so there are no
 tolerances.  Words are uniform residues (what encryption makes them), the top
 of the residue range where lazy arithmetic comes closest to overflowing, or
 real encryptions."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -12,6 +16,7 @@ from gpu_util import announce, config_pair, empty_dev, make_pair, misaligned_dev
 from helpers import encrypt_slots, galois_key, relin_key, secret
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 # (log_n, L, q_bits, K, p_bits, dnum)
 SETS = {
@@ -934,3 +939,153 @@ def test_full_ring_attention(lib, orc, sets, name, level):
     ref = orc.linattn_step(P, level, q, k, v, dec, s_in, rlk, *ref_st)
     same(y, ref[0], "step y")
     same(out, ref[1], "step state")
+
+
+ONE_LANE = """
+import sys
+import numpy as np
+import torch
+import private_rns_ckks_amd as L
+
+f = dict(np.load(sys.argv[1]))
+dev = lambda k: torch.from_numpy(f[k].view(np.int64)).to("cuda")
+log_n, dnum, lv = (int(f[k]) for k in ("log_n", "dnum", "lv"))
+ctx = L.Context(log_n, f["q_mods"], f["p_mods"], dnum)
+N = 1 << log_n
+t = {k: dev(k) for k in ("a", "v", "m", "q", "k", "x", "w", "r", "carry", "s", "rlk", "evk")}
+st = L.RotateSum([[int(f["g"])]], [[t["evk"]]])
+new = lambda *shape: torch.full(shape, -1, dtype=torch.int64, device="cuda")
+num, den = new(2, 2, lv - 1, N), new(2, 2, lv, N)
+y, end = new(2, 2, lv - 2, N), new(1, 2, lv - 2, N)
+
+
+def mix(groups, d):
+    L.ckks_attn_mix(ctx, t["a"], 1, t["v"], 1, groups, t["m"], 1, lv, t["rlk"], st, num, d)
+
+
+def chunk():
+    L.ckks_linattn_chunk(ctx, t["q"], t["k"], t["x"], 2, 1, t["w"], t["r"], t["carry"], 1, t["s"], lv, t["rlk"], st, y, end)
+
+
+for _ in range(2):
+    mix(2, den)
+    chunk()
+torch.cuda.synchronize()
+out = {"num": num, "den": den, "y": y, "end": end}
+out = {k: o.cpu().numpy() for k, o in out.items()}
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+    mix(2, den)
+    chunk()
+for i in range(3):
+    for o in (num, den, y, end):
+        o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for k, o in (("num", num), ("den", den), ("y", y), ("end", end)):
+        assert np.array_equal(o.cpu().numpy(), out[k]), (k, i)
+fresh = L.Context(log_n, f["q_mods"], f["p_mods"], dnum)  # no call of it has created the internal streams
+ctx = fresh
+mix(2, None)
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+try:
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        mix(1, den)
+    out["captured"] = np.array(1)
+except L.CKKSError:
+    out["captured"] = np.array(0)
+np.savez(sys.argv[2], **out)
+print("ONE_LANE ok", flush=True)
+"""
+
+
+@pytest.mark.parametrize("lanes", ["1", "2"])
+def test_number_of_lanes(lib, orc, sets, tmp_path, lanes):
+    """CKKS_LANES, read once a process: with 1 the calls that run steps side by side keep them on the caller's
+    stream (a capture before any internal stream exists succeeds), with 2 on an internal stream (that capture is
+    refused); the same words either way, captured ones too."""
+    ctx, P = sets("small")
+    announce("attention calls with CKKS_LANES=%s" % lanes)
+    lv, n = 5, 6
+    rlk, evk, g = key(P, 0, "rlk"), key(P, 0, "lane"), P.galois(3)
+    c = {t: words(P, 1, "lane" + t, n, (2, 2)) for t in "avqkx"}
+    p = {t: words(P, 1, "lane" + t, n, (2,)) for t in "wr"}
+    m = words(P, 1, "lanem", n, (1,))
+    carry, s_in = words(P, 1, "lanec", n - 2, (1,)), words(P, 1, "lanes", n - 2, (1, 2))
+    np.savez(tmp_path / "in.npz", log_n=P.log_n, dnum=P.dnum, lv=lv, q_mods=np.array(P.q), p_mods=np.array(P.p), rlk=rlk,
+             evk=evk, g=g, m=m, carry=carry, s=s_in, **c, **p)
+    env = dict(os.environ, CKKS_LANES=lanes)
+    r = subprocess.run([sys.executable, "-c", ONE_LANE, str(tmp_path / "in.npz"), str(tmp_path / "out.npz")], env=env,
+                       cwd=ROOT, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "ONE_LANE ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+    got = {k: v.view(np.uint64) for k, v in np.load(tmp_path / "out.npz").items()}
+    gal, keys = [[g]], [[evk]]
+    rn, rd = orc.attn_mix(P, lv, c["a"][:, None, None], c["v"][:, None], m[:, None], rlk, gal, keys)
+    ry, rs = orc.linattn_chunk(P, lv, c["q"][:, None], c["k"][:, None], c["x"][:, None], p["w"][:, None], p["r"][:, None],
+                               carry, s_in, rlk, gal, keys)
+    assert np.array_equal(got["num"], rn[:, 0]) and np.array_equal(got["den"], rd[:, 0])
+    assert np.array_equal(got["y"], ry[:, 0]) and np.array_equal(got["end"], rs)
+    assert int(got["captured"]) == (1 if lanes == "1" else 0)
+
+
+def test_inputs_written_late_on_the_callers_stream(lib, orc, sets):
+    """Inputs that a side stream writes only after long work of its own: the calls, enqueued before that, return
+    without waiting for it and read the words it writes."""
+    torch = torch_cuda()
+    ctx, P = sets("mid")
+    announce("late inputs")
+    st, ref_st = steps(lib, P, [2])
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    lv, n = 5, 6
+    names = ("a", "v", "q", "k", "x")
+    host = {t: words(P, 2, "late" + t, n, (2, 2)) for t in names}
+    pt = {t: words(P, 2, "late" + t, n, (2,)) for t in ("m", "w", "r")}
+    carry, s_in = words(P, 2, "latec", n - 2, (1,)), words(P, 2, "lates", n - 2, (1, 2))
+    src = {t: to_dev(x) for t, x in host.items()}
+    d = {t: torch.zeros_like(x) for t, x in src.items()}
+    p = {t: to_dev(x) for t, x in pt.items()}
+    d_c, d_s = to_dev(carry), to_dev(s_in)
+    outs = [empty_dev((2, 2, n, P.N)), empty_dev((1, 2, lv - 1, P.N)), empty_dev((1, 2, lv, P.N)),
+            empty_dev((2, 2, lv - 2, P.N)), empty_dev((1, 2, lv - 2, P.N)), empty_dev((1, 2, 2, 2, lv, P.N)),
+            empty_dev((2, 2, lv - 1, P.N)), empty_dev((2, 2, lv, P.N))]
+
+    def calls():
+        lib.ckks_rotate_sum(ctx, d["a"], outs[0], 2, lv, st)
+        lib.ckks_attn_mix(ctx, d["a"], 1, d["v"], 2, 1, p["m"], 1, lv, d_rlk, st, outs[1], outs[2])
+        lib.ckks_linattn_chunk(ctx, d["q"], d["k"], d["x"], 2, 1, p["w"], p["r"], d_c, 1, d_s, lv, d_rlk, st, outs[3],
+                               outs[4])
+        lib.ckks_attn_scores(ctx, d["q"], 2, d["k"], 2, 1, lv, d_rlk, st, outs[5])
+        lib.ckks_linattn_step(ctx, d["q"], d["k"], d["x"], 2, None, 0, None, lv, d_rlk, st, outs[6], outs[7])
+
+    side = torch.cuda.Stream()
+    m = torch.ones((4096, 4096), device="cuda")
+    with torch.cuda.stream(side):  # sizes the buffers, creates the internal streams, loads the kernels
+        torch.mm(m, m)
+        calls()
+    torch.cuda.synchronize()
+    busy = torch.cuda.Event()
+    with torch.cuda.stream(side):
+        for _ in range(200):  # some 200 ms
+            acc = torch.mm(m, m)
+        for t in names:
+            d[t].copy_(src[t])
+        busy.record()
+        calls()
+        waited = busy.query()
+    side.synchronize()
+    assert not waited, "a call waited for the stream's earlier work"
+    assert float(acc[0, 0]) == 4096.0
+    same(outs[0], np.stack([orc.rotate_sum(P, lv, c, *ref_st) for c in host["a"]]), "sum")
+    rn, rd = orc.attn_mix(P, lv, host["a"][None, None], host["v"][None], pt["m"][None], rlk, *ref_st)
+    same(outs[1], rn[0], "num")
+    same(outs[2], rd[0], "den")
+    ry, rs = orc.linattn_chunk(P, lv, host["q"][:, None], host["k"][:, None], host["x"][:, None], pt["w"][:, None],
+                               pt["r"][:, None], carry, s_in, rlk, *ref_st)
+    same(outs[3], ry[:, 0], "y")
+    same(outs[4], rs, "state")
+    same(outs[5], orc.attn_scores(P, lv, host["q"][None], host["k"][None], rlk, *ref_st), "scores")
+    ry, rs = orc.linattn_step(P, lv, host["q"], host["k"], host["x"], None, None, rlk, *ref_st)
+    same(outs[6], ry, "step y")
+    same(outs[7], rs, "step state")
