@@ -1089,3 +1089,102 @@ def test_inputs_written_late_on_the_callers_stream(lib, orc, sets):
     ry, rs = orc.linattn_step(P, lv, host["q"], host["k"], host["x"], None, None, rlk, *ref_st)
     same(outs[6], ry, "step y")
     same(outs[7], rs, "step state")
+
+
+# Primes of several sizes in one context, as a chain of rescales has them: the
+# conversions and rescales then cross sizes in both directions.
+MIXED = {
+    "mixed": (2, [60, 40, 54, 30, 57, 45], [60, 50, 36]),
+    "mixedwide": (2, [62, 40, 61, 30, 54, 60], [61, 62, 50]),
+}
+
+
+def mixed_pair(lib, orc, log_n, dnum, q_bits, p_bits):
+    taken = set()
+
+    def pick(bits):
+        m = next(v for v in lib.ckks_find_primes(log_n, bits, 9) if v not in taken)
+        taken.add(m)
+        return m
+
+    q, p = [pick(b) for b in q_bits], [pick(b) for b in p_bits]
+    return lib.Context(log_n, q, p, dnum), orc.Params(log_n, q, p, dnum)
+
+
+@pytest.mark.parametrize("top", [False, True])
+@pytest.mark.parametrize("log_n", [10, 13])
+@pytest.mark.parametrize("name", list(MIXED))
+def test_primes_of_several_sizes(lib, orc, name, log_n, top):
+    ctx, P = mixed_pair(lib, orc, log_n, *MIXED[name])
+    announce("mixed primes %s log_n=%d top=%d" % (name, log_n, top))
+    st, ref_st = steps(lib, P, [3, 2], top=top)
+    rlk = key(P, 0, "rlk", top)
+    d_rlk = to_dev(rlk)
+    for lv in (5, 4, 3):
+        n = lv + 1
+        a, v, m = words(P, lv, "ma", n, (2, 1, 2, 2), top), words(P, lv, "mv", n, (2, 2, 2), top), words(P, lv, "mm", n, (1, 2), top)
+        num, den = empty_dev((2, 1, 2, lv - 1, P.N)), empty_dev((2, 1, 2, lv, P.N))
+        lib.ckks_attn_mix(ctx, to_dev(a), 1, to_dev(v), 2, 2, to_dev(m), 1, lv, d_rlk, st, num, den)
+        ref = orc.attn_mix(P, lv, a, v, m, rlk, *ref_st)
+        same(num, ref[0], "num %d" % lv)
+        same(den, ref[1], "den %d" % lv)
+        d = chunk_case(P, lv, 2, 1, 1, True, True, True, lv, top)
+        y, out = run_chunk(lib, ctx, P, d, lv, 2, 1, 1, rlk, st)
+        ref = orc.linattn_chunk(P, lv, d["q"], d["k"], d["v"], d["w"], d["r"], d["carry"], d["state"], rlk, *ref_st)
+        same(y, ref[0], "y %d" % lv)
+        same(out, ref[1], "state %d" % lv)
+        dec, s_in = words(P, lv, "mdec", n, (1,), top), words(P, lv, "ms", n, (1, 2), top)
+        y, out = empty_dev((1, 2, lv - 1, P.N)), empty_dev((1, 2, lv, P.N))
+        q, k, x = (to_dev(d[t][0]) for t in "qkv")
+        lib.ckks_linattn_step(ctx, q, k, x, 1, to_dev(dec), 1, to_dev(s_in), lv, d_rlk, st, y, out)
+        ref = orc.linattn_step(P, lv, d["q"][0], d["k"][0], d["v"][0], dec, s_in, rlk, *ref_st)
+        same(y, ref[0], "step y %d" % lv)
+        same(out, ref[1], "step state %d" % lv)
+        s = empty_dev((2, 1, 2, 2, lv, P.N))
+        lib.ckks_attn_scores(ctx, to_dev(a[:, :, 0]), 1, to_dev(v), 2, 2, lv, d_rlk, st, s)
+        same(s, orc.attn_scores(P, lv, a[:, :, 0], v, rlk, *ref_st), "scores %d" % lv)
+    ctx.close()
+
+
+@pytest.mark.parametrize("shape,n_item", [((10, 20, 54, 5, 60, 4), 128), ((11, 20, 54, 5, 60, 4), 70),
+                                          ((12, 24, 54, 8, 60, 3), 24), ((10, 20, 61, 5, 62, 4), 128)])
+def test_many_items_on_small_rings(lib, orc, shape, n_item):
+    """More limbs than the one-workgroup transforms take: small rings on the two-pass kernels, with one and two
+    dropped limbs; the first, a middle and the last item against the oracle."""
+    ctx, P = make_pair(lib, orc, *shape)
+    lv = P.L - 1
+    announce("%d items on a small ring %s" % (n_item, shape))
+    assert n_item * (lv - 1) * P.N > 1 << 21
+    st, ref_st = steps(lib, P, [2])
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    q, k = words(P, 1, "sq", lv + 1, (1, n_item, 2)), words(P, 1, "sk", lv + 1, (1, 1, 2))
+    m = words(P, 1, "sm", lv + 1, (1, 1))
+    d_q, d_k = to_dev(q), to_dev(k)
+    pick = [0, n_item // 2, n_item - 1]
+    s = empty_dev((1, n_item, 1, 2, lv, P.N))
+    lib.ckks_attn_scores(ctx, d_q, n_item, d_k, 1, 1, lv, d_rlk, st, s)
+    same(s[:, pick], orc.attn_scores(P, lv, q[:, pick], k, rlk, *ref_st), "scores")
+    num, den = empty_dev((1, n_item, 2, lv - 1, P.N)), empty_dev((1, n_item, 2, lv, P.N))
+    lib.ckks_attn_mix(ctx, d_q, n_item, d_k, 1, 1, to_dev(m), 1, lv, d_rlk, st, num, den)
+    ref = orc.attn_mix(P, lv, q[:, pick, None], k, m, rlk, *ref_st)
+    same(num[:, pick], ref[0], "num")
+    same(den[:, pick], ref[1], "den")
+    ctx.close()
+
+
+@pytest.mark.parametrize("name,level,batch,features,radices", [
+    ("small", 5, 2, 16, [4, 4]), ("c3", 12, 1, 64, [8, 8]), ("mid", 7, 5, 64, [8, 8]), ("mid14", 4, 1, 128, [2, 32, 2]),
+    ("full", 5, 4, 64, [8, 8])])
+def test_sums_of_the_outermost_index(lib, orc, sets, name, level, batch, features, radices):
+    """The layout with the summed index outermost: rotations by multiples of n / F, whose automorphisms keep a word
+    inside F adjacent ones."""
+    ctx, P = sets(name)
+    stride = P.N // 2 // features
+    assert int(np.prod(radices)) == features
+    announce("sum at stride n / %d on %s" % (features, name))
+    st, (gal, keys) = steps(lib, P, radices, stride=stride)
+    x = words(P, level, "outer", level + 1, (batch, 2))
+    out = empty_dev(x.shape)
+    lib.ckks_rotate_sum(ctx, to_dev(x), out, batch, level, st)
+    same(out, np.stack([orc.rotate_sum(P, level, c, gal, keys) for c in x]))
