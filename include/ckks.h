@@ -366,9 +366,10 @@ int ckks_ctmatvec(ckks_ctx* ctx, const uint64_t* d_x, int n_in, const uint64_t* 
  * and ckks_linattn_chunk with read weights or a carry also use one of the
  * context's internal streams, which their first call creates; the work on it
  * starts and ends with the call's place on the caller's stream.  A call no
- * larger than an earlier one with the same optional operands allocates and
- * creates nothing and may be captured into a graph; any other returns
- * CKKS_EHIP while its stream is capturing if it would have to.  Buffers a
+ * larger than an earlier one with the same optional operands (no more limbs,
+ * groups, items, tokens or stages in any count) allocates and creates nothing
+ * and may be captured into a graph; any other returns CKKS_EHIP while its
+ * stream is capturing if it would have to.  Buffers a
  * capture has recorded stay allocated until the context is destroyed, so a
  * captured call stays valid while larger calls follow.  Replays use the
  * context like calls do: one at a time. */

@@ -1,11 +1,23 @@
 // The sum over a packed axis (sumrot.hip) and the slotwise kernels of the
 // attention calls (attn_kernels.hip), used by their host side (attention.hip).
 #pragma once
+#include <algorithm>
+
 #include "ops.h"
 
 namespace ckks {
 
 constexpr int kMaxSumRot = CKKS_SUM_MAX_RADIX - 1;  // rotations of one stage
+
+// Words reserved for steps that hold as many of a call's `items` (`per` words
+// each) as fit `limit`, one at least.  It never falls when items or per grow,
+// as the words of the items that fit would (a buffer of 4 items of 28 limbs is
+// smaller than one of 5 items of 23): a call with fewer limbs or items than an
+// earlier one finds its buffers large enough, which captures rely on.
+inline uint64_t held_words(uint64_t per, uint64_t items, uint64_t limit) {
+  return std::min(per * items, std::max(limit, per));
+}
+constexpr uint64_t kStepWords = 1ull << 28;  // a step's workspace: 2 GiB
 
 // Words of workspace sum_stages needs for `batch` items at `level`.
 size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage);

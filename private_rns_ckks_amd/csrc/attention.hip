@@ -23,8 +23,14 @@ uint64_t block_words() {
   return (uint64_t)(mb > 0 ? mb : 4096) << 17;
 }
 
+constexpr uint64_t kBlockItems = 1024;
 int block_items(uint64_t per_item, uint64_t items) {
-  return (int)std::max<uint64_t>(1, std::min<uint64_t>({items, block_words() / per_item, 1024}));
+  return (int)std::max<uint64_t>(1, std::min<uint64_t>({items, block_words() / per_item, kBlockItems}));
+}
+
+// Words of the operand buffer for such blocks of a call's `items`.
+uint64_t block_reserve(uint64_t per_item, uint64_t items) {
+  return held_words(per_item, std::min(items, kBlockItems), block_words());
 }
 
 // Tells the context's buffers that this call's stream is being captured:
@@ -102,16 +108,19 @@ struct Tail {
   uint64_t* ws;  // reserved words of the context's workspace
   uint64_t ws_words;
 
-  // Words of workspace each step takes; relinearisations go in launches of as
-  // many items as 2 GiB hold (the items of a launch share the key).
+  // Words of workspace that each step reserves for a call of n items;
+  // relinearisations go in launches of as many items as fit (the items of a
+  // launch share the key).
   int relin_items(int n, int level, int drop) const {
-    const uint64_t fit = (1ull << 28) / ks_rescale_ws_words(c, level, drop);
+    const uint64_t fit = kStepWords / ks_rescale_ws_words(c, level, drop);
     return (int)std::max<uint64_t>(1, std::min<uint64_t>({fit, (uint64_t)kMaxChunk, (uint64_t)n}));
   }
   uint64_t relin_words(int n, int level, int drop) const {
-    return ks_rescale_ws_words(c, level, drop) * relin_items(n, level, drop);
+    return held_words(ks_rescale_ws_words(c, level, drop), std::min(n, kMaxChunk), kStepWords);
   }
-  uint64_t rescale_words(int n, int level) const { return (uint64_t)c->N * (2 + 2 * level) * std::min(n, kMaxChunk); }
+  uint64_t rescale_words(int n, int level) const {
+    return held_words((uint64_t)c->N * (2 + 2 * level), std::min(n, kMaxChunk), kStepWords);
+  }
   uint64_t sum_words(int n, int level) const {
     return st.n_stage ? sum_ws_words(c, level, n, st.n_stage) : 0;
   }
@@ -134,7 +143,9 @@ struct Tail {
                       out + b0 * 2 * limb(level - drop), 2 * limb(level - drop), ws);
     return rc;
   }
-  uint64_t mul_words(int n, int level) const { return (uint64_t)c->N * (4 + 2 * level) * std::min(n, kMaxChunk); }
+  uint64_t mul_words(int n, int level) const {
+    return held_words((uint64_t)c->N * (4 + 2 * level), std::min(n, kMaxChunk), kStepWords);
+  }
   // rescale(p in), n items; per item of the workspace the dropped limb's
   // product, its inverse transform, the converted limbs
   int mul_rescale(PlainMul m, int n) const {
@@ -250,8 +261,8 @@ int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, 
   CaptureScope cap(c, s);
   const uint64_t per = 3 * lim + zct;
   const int block = block_items(per, items);
-  if ((rc = ensure_aux(c, per * block))) return rc;
-  if ((rc = t.reserve(std::max(t.relin_words(block, l, 1), t.sum_words(block, l - 1))))) return rc;
+  if ((rc = ensure_aux(c, block_reserve(per, items)))) return rc;
+  if ((rc = t.reserve(std::max(t.relin_words(items, l, 1), t.sum_words(items, l - 1))))) return rc;
   uint64_t *X = c->aux, *Z = X + 3 * lim * block;
   for (int b0 = 0; b0 < items; b0 += block) {
     const int n = std::min(block, items - b0);
@@ -305,11 +316,11 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
   CaptureScope cap(c, s);
   const uint64_t per = 3 * lim + 2 * lim + 2 * mid;
   const int block = block_items(per, rows);
-  if ((rc = ensure_aux(c, per * block))) return rc;
+  if ((rc = ensure_aux(c, block_reserve(per, rows)))) return rc;
   uint64_t *X = c->aux, *D = X + 3 * lim * block, *Z = D + 2 * lim * block, *Y = Z + mid * block;
   const int ld = mask ? l - 1 : l;  // den's level
-  const uint64_t side_words = den ? std::max(mask ? t.rescale_words(block, l) : 0, t.sum_words(block, ld)) : 0;
-  if ((rc = t.reserve(std::max(t.relin_words(block, l, drop), t.sum_words(block, l - drop)), side_words))) return rc;
+  const uint64_t side_words = den ? std::max(mask ? t.rescale_words(rows, l) : 0, t.sum_words(rows, ld)) : 0;
+  if ((rc = t.reserve(std::max(t.relin_words(rows, l, drop), t.sum_words(rows, l - drop)), side_words))) return rc;
   for (int b0 = 0; b0 < rows; b0 += block) {
     const int n = std::min(block, rows - b0);
     MixArgs m;
@@ -412,13 +423,15 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
   // from one block of tokens to the next
   const uint64_t mid = 2ull * l * N, per = 3 * lim + (r ? mid : 0) + sct + yct;
   const int gb = block_items(per + 3 * lim, n_grp);
-  const int tb = std::min(block_items((per + 3 * lim) * gb, n_tok), std::max(1, 8192 / gb));  // one launch's items
+  constexpr int kLaunch = 8192;  // items of one launch
+  const int tb = std::min(block_items((per + 3 * lim) * gb, n_tok), std::max(1, kLaunch / gb));
   const uint64_t nb = (uint64_t)gb * tb;
-  if ((rc = ensure_aux(c, per * nb + 3 * lim * gb))) return rc;
+  const uint64_t most = per * std::min<uint64_t>(items, kLaunch) + 3 * lim * std::min<uint64_t>(n_grp, kBlockItems);
+  if ((rc = ensure_aux(c, std::min(most, std::max(block_words(), per + 3 * lim))))) return rc;
   uint64_t *X = c->aux, *S = X + 3 * lim * nb, *Z = S + sct * nb, *C = Z + yct * nb, *P = C + (r ? mid * nb : 0);
-  const uint64_t side_words = std::max(r ? t.mul_words((int)nb, l) : 0, carry ? t.mul_words(gb, l - 2) : 0);
-  if ((rc = t.reserve(std::max({t.relin_words((int)nb, l, 2), t.relin_words((int)nb, l - 2, 1),
-                                t.sum_words((int)nb, l - 3)}),
+  const int all = (int)items;
+  const uint64_t side_words = std::max(r ? t.mul_words(all, l) : 0, carry ? t.mul_words(n_grp, l - 2) : 0);
+  if ((rc = t.reserve(std::max({t.relin_words(all, l, 2), t.relin_words(all, l - 2, 1), t.sum_words(all, l - 3)}),
                       side_words)))
     return rc;
   for (int g0 = 0; g0 < n_grp; g0 += gb) {
@@ -503,8 +516,8 @@ int linattn_step(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v
   CaptureScope cap(c, s);
   const uint64_t per = 3 * lim + yct;
   const int block = block_items(per, n_grp);
-  if ((rc = ensure_aux(c, per * block))) return rc;
-  if ((rc = t.reserve(std::max({t.relin_words(block, l, 1), t.relin_words(block, l - 1, 1), t.sum_words(block, l - 2)}))))
+  if ((rc = ensure_aux(c, block_reserve(per, n_grp)))) return rc;
+  if ((rc = t.reserve(std::max({t.relin_words(n_grp, l, 1), t.relin_words(n_grp, l - 1, 1), t.sum_words(n_grp, l - 2)}))))
     return rc;
   uint64_t *X = c->aux, *Z = X + 3 * lim * block;
   for (int b0 = 0; b0 < n_grp; b0 += block) {

@@ -441,16 +441,16 @@ static size_t group_words(const Ctx* c, int level, int n, int n_stage) {
   return n * (stage_words(c, level) + (n_stage > 1 ? 4 * (size_t)(level + 1) * c->N : 0));
 }
 
-// Items of a group: the launches' limit, or what 2 GiB hold (17 at N = 2^16
-// and 24 + 8 limbs).  Large groups share each key word among more items; two
+// Items of a group: the launches' limit, or what 2 GiB hold (at N = 2^16 and
+// 24 + 8 limbs 17 with one stage, 12 with more).  Large groups share each key word among more items; two
 // half groups on two streams measured 0-14 % slower (keys are read twice).
 static int sum_group(const Ctx* c, int level, int batch, int n_stage) {
-  const size_t fit = (1ull << 28) / group_words(c, level, 1, n_stage);
+  const size_t fit = kStepWords / group_words(c, level, 1, n_stage);
   return (int)std::max<size_t>(1, std::min<size_t>({fit, (size_t)kMaxChunk, (size_t)batch}));
 }
 
 size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage) {
-  return group_words(c, level, sum_group(c, level, batch, n_stage), n_stage);
+  return held_words(group_words(c, level, 1, n_stage), std::min(batch, kMaxChunk), kStepWords);
 }
 
 int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,

@@ -1188,3 +1188,78 @@ def test_sums_of_the_outermost_index(lib, orc, sets, name, level, batch, feature
     out = empty_dev(x.shape)
     lib.ckks_rotate_sum(ctx, to_dev(x), out, batch, level, st)
     same(out, np.stack([orc.rotate_sum(P, level, c, gal, keys) for c in x]))
+
+
+def sized_calls(lib, P, st_two, st_one, d_rlk, lv, items):
+    """The five calls on about `items` ciphertexts at `lv`: (name, function of a context, outputs)."""
+    n, N = lv + 1, P.N
+    w = lambda tag, limbs, *lead: to_dev(words(P, lv + 10 * items, "size" + tag, limbs, lead))
+    x = {t: w(t, n, items, 2) for t in "qkva"}
+    pt = {t: w("p" + t, n, items) for t in "mwrd"}
+    made = []
+    o = [empty_dev((items, 2, n, N))]
+    made.append(("sum", lambda c, o=o: lib.ckks_rotate_sum(c, x["q"], o[0], items, lv, st_two), o))
+    o = [empty_dev((items, 2, n, N))]
+    made.append(("sum of one stage", lambda c, o=o: lib.ckks_rotate_sum(c, x["q"], o[0], items, lv, st_one), o))
+    o = [empty_dev((items, 2, lv, N))]
+    made.append(("scores", lambda c, o=o: lib.ckks_attn_scores(c, x["q"], items, x["k"], 1, 1, lv, d_rlk, st_two, o[0]), o))
+    o = [empty_dev((items, 2, lv - 1, N)), empty_dev((items, 2, lv, N))]
+    made.append(("mix", lambda c, o=o: lib.ckks_attn_mix(c, x["a"], 1, x["v"], 1, items, pt["m"], items, lv, d_rlk, st_two,
+                                                         o[0], o[1]), o))
+    o = [empty_dev((items, 2, lv - 1, N)), empty_dev((items, 2, lv, N))]
+    s_in = w("s", n, items, 2)
+    made.append(("step", lambda c, o=o: lib.ckks_linattn_step(c, x["q"], x["k"], x["v"], items, pt["d"], 1, s_in, lv, d_rlk,
+                                                              st_two, o[0], o[1]), o))
+    if lv >= 3:
+        for G in (1, 2):
+            T = items // G
+            if not T:
+                continue
+            o = [empty_dev((T, G, 2, lv - 2, N)), empty_dev((G, 2, lv - 2, N))]
+            carry, c_in = w("c", lv - 1, 1), w("cs", lv - 1, G, 2)
+            made.append(("chunk of %d groups" % G, lambda c, o=o, T=T, G=G, carry=carry, c_in=c_in: lib.ckks_linattn_chunk(
+                c, x["q"], x["k"], x["v"], T, G, pt["w"], pt["r"], carry, 1, c_in, lv, d_rlk, st_two, o[0], o[1]), o))
+    return made
+
+
+@pytest.mark.parametrize("mb", [1, 3])
+def test_calls_no_larger_than_earlier_ones_can_be_captured(lib, orc, monkeypatch, mb):
+    """After one call of each kind at the top level, the same kinds with fewer limbs or items need nothing new,
+    also where blocks of a limited size hold more of the smaller items: each is captured and replayed."""
+    torch = torch_cuda()
+    monkeypatch.setenv("CKKS_BLOCK_MB", str(mb))
+    ref_ctx, P = make_pair(lib, orc, *SETS["small"])
+    announce("captures after larger calls, %d MiB" % mb)
+    two, one = steps(lib, P, [2, 2])[0], steps(lib, P, [2])[0]
+    d_rlk = to_dev(key(P, 0, "rlk"))
+    kinds = [c[0] for c in sized_calls(lib, P, two, one, d_rlk, 5, 12)]
+    failed = []
+    for kind in kinds:
+        ctx = make_pair(lib, orc, *SETS["small"])[0]
+        first = "sum" if kind.startswith("sum") else kind
+        dict((c[0], c[1]) for c in sized_calls(lib, P, two, one, d_rlk, 5, 12))[first](ctx)
+        for lv in (5, 4, 3, 2):
+            for items in (12, 9, 5, 2):
+                call = next((c for c in sized_calls(lib, P, two, one, d_rlk, lv, items) if c[0] == kind), None)
+                if call is None:
+                    continue
+                call[1](ref_ctx)
+                torch.cuda.synchronize()
+                ref = [o.clone() for o in call[2]]
+                for o in call[2]:
+                    o.zero_()
+                torch.cuda.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                try:
+                    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+                        call[1](ctx)
+                except lib.CKKSError as e:
+                    failed.append("%s level=%d items=%d: %s" % (kind, lv, items, e))
+                    continue
+                graph.replay()
+                torch.cuda.synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(call[2], ref)), (kind, lv, items)
+                del graph
+        ctx.close()
+    assert not failed, "\n".join(failed)
+    ref_ctx.close()
