@@ -362,7 +362,11 @@ int ckks_ctmatvec(ckks_ctx* ctx, const uint64_t* d_x, int n_in, const uint64_t* 
  * sums over nothing decrypt to zero (there is no division).
  *
  * Buffers and streams: intermediates live in the context's buffers, grown on
- * demand; growing synchronises the device.  ckks_attn_mix with a normaliser
+ * demand; growing synchronises the device.  A call holds 4 GiB of operands and
+ * a workspace of 2 GiB (two for ckks_attn_mix and ckks_linattn_chunk) at most,
+ * or a single item's if that is more; the environment variable CKKS_BLOCK_MB,
+ * read at each call, lowers both limits to that many MiB, or raises the first.
+ * ckks_attn_mix with a normaliser
  * and ckks_linattn_chunk with read weights or a carry also use one of the
  * context's internal streams, which their first call creates; the work on it
  * starts and ends with the call's place on the caller's stream.  A call no

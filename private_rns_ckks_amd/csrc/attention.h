@@ -17,10 +17,10 @@ constexpr int kMaxSumRot = CKKS_SUM_MAX_RADIX - 1;  // rotations of one stage
 inline uint64_t held_words(uint64_t per, uint64_t items, uint64_t limit) {
   return std::min(per * items, std::max(limit, per));
 }
-constexpr uint64_t kStepWords = 1ull << 28;  // a step's workspace: 2 GiB
 
-// Words of workspace sum_stages needs for `batch` items at `level`.
-size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage);
+// Words of workspace sum_stages needs for `batch` items at `level`, in groups
+// that fit `limit` words.
+size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage, uint64_t limit);
 
 // Inner products of n items' raised digits (E: item b at E + b*E_stride,
 // [beta][next][N]; own: the NTT-form input [nq][N], own_stride apart) with the
@@ -34,9 +34,9 @@ int key_ip(Ctx* c, hipStream_t s, int level, int n, const uint64_t* E, uint64_t 
            const uint64_t* const* evk);
 
 // `batch` ciphertexts (item b at in + b*in_stride) through every stage of the
-// checked plan into out + b*out_stride.  ws holds sum_ws_words.
+// checked plan into out + b*out_stride.  ws holds sum_ws_words (same limit).
 int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
-               int batch, int level, const ckks_sum_steps& st, uint64_t* ws);
+               int batch, int level, const ckks_sum_steps& st, uint64_t* ws, uint64_t limit);
 
 // rescale(p[row] * in[b]) by the top limb `level`; b = t * ng + g (first + the
 // launch's item) reads in + (t * n_grp + g)*in_bstride and row t * n_row +

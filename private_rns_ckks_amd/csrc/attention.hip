@@ -1,7 +1,6 @@
 // Entry points of the attention calls: argument checks, and the composition of
 // slotwise products (attn_kernels.hip), relinearisation and rescale (ops.hip)
-// and the sum over a packed axis (sumrot.hip).  Items go in blocks whose
-// intermediates fit block_words().
+// and the sum over a packed axis (sumrot.hip).  Items go in blocks (Hold).
 #include <stdlib.h>
 #include <string.h>
 
@@ -14,24 +13,29 @@ namespace ckks {
 
 namespace {
 
-// Words of intermediates a call holds at once: CKKS_BLOCK_MB of memory, by
-// default 4 GiB of the card's 288 (some 40 items at N = 2^16 and 24 limbs,
-// enough to fill the chip many times).
-uint64_t block_words() {
-  const char* e = getenv("CKKS_BLOCK_MB");
-  const long mb = e ? atol(e) : 0;
-  return (uint64_t)(mb > 0 ? mb : 4096) << 17;
-}
+constexpr uint64_t kBlockItems = 1024;  // items of a block at most
 
-constexpr uint64_t kBlockItems = 1024;
-int block_items(uint64_t per_item, uint64_t items) {
-  return (int)std::max<uint64_t>(1, std::min<uint64_t>({items, block_words() / per_item, kBlockItems}));
-}
-
-// Words of the operand buffer for such blocks of a call's `items`.
-uint64_t block_reserve(uint64_t per_item, uint64_t items) {
-  return held_words(per_item, std::min(items, kBlockItems), block_words());
-}
+// What a call may hold at once, read once a call: the words of a block of
+// items, CKKS_BLOCK_MB of memory, by default 4 GiB of the card's 288 (some 40
+// items at N = 2^16 and 24 limbs, enough to fill the chip many times); and of
+// each stream's workspace, 2 GiB but no more than that.  One item is always
+// held.
+struct Hold {
+  uint64_t block, step;
+  Hold() {
+    const char* e = getenv("CKKS_BLOCK_MB");
+    const long mb = e ? atol(e) : 0;
+    block = (uint64_t)(mb > 0 ? std::min(mb, 1l << 30) : 4096) << 17;
+    step = std::min<uint64_t>(block, 1ull << 28);
+  }
+  int items(uint64_t per_item, uint64_t n) const {
+    return (int)std::max<uint64_t>(1, std::min<uint64_t>({n, block / per_item, kBlockItems}));
+  }
+  // Words of the operand buffer for such blocks of a call's n items.
+  uint64_t reserve(uint64_t per_item, uint64_t n) const {
+    return held_words(per_item, std::min(n, kBlockItems), block);
+  }
+};
 
 // Tells the context's buffers that this call's stream is being captured:
 // growing then is an error, and buffers a capture has recorded are kept.
@@ -101,6 +105,7 @@ struct Tail {
   hipStream_t s;
   const uint64_t* rlk;
   ckks_sum_steps st;
+  Hold hold;
 
   uint64_t limb(int l) const { return (uint64_t)(l + 1) * c->N; }
   DropOut drop_out(int drop) const { return DropOut{c->d_rescale, (int)c->L, drop}; }
@@ -112,17 +117,17 @@ struct Tail {
   // relinearisations go in launches of as many items as fit (the items of a
   // launch share the key).
   int relin_items(int n, int level, int drop) const {
-    const uint64_t fit = kStepWords / ks_rescale_ws_words(c, level, drop);
+    const uint64_t fit = hold.step / ks_rescale_ws_words(c, level, drop);
     return (int)std::max<uint64_t>(1, std::min<uint64_t>({fit, (uint64_t)kMaxChunk, (uint64_t)n}));
   }
   uint64_t relin_words(int n, int level, int drop) const {
-    return held_words(ks_rescale_ws_words(c, level, drop), std::min(n, kMaxChunk), kStepWords);
+    return held_words(ks_rescale_ws_words(c, level, drop), std::min(n, kMaxChunk), hold.step);
   }
   uint64_t rescale_words(int n, int level) const {
-    return held_words((uint64_t)c->N * (2 + 2 * level), std::min(n, kMaxChunk), kStepWords);
+    return held_words((uint64_t)c->N * (2 + 2 * level), std::min(n, kMaxChunk), hold.step);
   }
   uint64_t sum_words(int n, int level) const {
-    return st.n_stage ? sum_ws_words(c, level, n, st.n_stage) : 0;
+    return st.n_stage ? sum_ws_words(c, level, n, st.n_stage, hold.step) : 0;
   }
 
   // `main` words for this stream's steps, `side` more for Side's.
@@ -144,7 +149,7 @@ struct Tail {
     return rc;
   }
   uint64_t mul_words(int n, int level) const {
-    return held_words((uint64_t)c->N * (4 + 2 * level), std::min(n, kMaxChunk), kStepWords);
+    return held_words((uint64_t)c->N * (4 + 2 * level), std::min(n, kMaxChunk), hold.step);
   }
   // rescale(p in), n items; per item of the workspace the dropped limb's
   // product, its inverse transform, the converted limbs
@@ -176,7 +181,7 @@ struct Tail {
       CKKS_HIP_CHECK(hipMemcpyAsync(out, Z, ct * n * 8, hipMemcpyDeviceToDevice, s));
       return CKKS_OK;
     }
-    return sum_stages(c, s, Z, ct, out, ct, n, level, st, ws);
+    return sum_stages(c, s, Z, ct, out, ct, n, level, st, ws, hold.step);
   }
 };
 
@@ -232,7 +237,7 @@ int rotate_sum(Ctx* c, const uint64_t* in, uint64_t* out, int batch, int level, 
   const uint64_t ct = 2ull * (level + 1) * c->N;
   if ((rc = check_count(batch))) return rc;
   std::vector<Range> ins = {{in, ct * batch}};
-  Tail t{c, s, nullptr, {}, nullptr, 0};
+  Tail t{c, s, nullptr, {}, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges({{out, ct * batch}}, ins))) return rc;
   if (t.st.n_stage == 0) return set_error(CKKS_EINVAL, "a sum needs at least one stage");
   if (batch == 0) return CKKS_OK;
@@ -255,13 +260,13 @@ int attn_scores(Ctx* c, const uint64_t* q, int n_q, const uint64_t* k, int n_k, 
   const int items = n_grp * n_q * n_k, l = level;
   const uint64_t N = c->N, lim = (uint64_t)(l + 1) * N, zct = 2ull * l * N;
   std::vector<Range> ins = {{q, 2 * lim * n_grp * n_q}, {k, 2 * lim * n_grp * n_k}, {rlk, key_words(c)}};
-  Tail t{c, s, rlk, {}, nullptr, 0};
+  Tail t{c, s, rlk, {}, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges({{out, zct * items}}, ins))) return rc;
   if (items == 0) return CKKS_OK;
   CaptureScope cap(c, s);
   const uint64_t per = 3 * lim + zct;
-  const int block = block_items(per, items);
-  if ((rc = ensure_aux(c, block_reserve(per, items)))) return rc;
+  const int block = t.hold.items(per, items);
+  if ((rc = ensure_aux(c, t.hold.reserve(per, items)))) return rc;
   if ((rc = t.reserve(std::max(t.relin_words(items, l, 1), t.sum_words(items, l - 1))))) return rc;
   uint64_t *X = c->aux, *Z = X + 3 * lim * block;
   for (int b0 = 0; b0 < items; b0 += block) {
@@ -310,13 +315,13 @@ int attn_mix(Ctx* c, const uint64_t* a, int n_q, const uint64_t* v, int n_k, int
   if (mask) ins.push_back({mask, lim * n_mask * n_k});
   std::vector<Range> outs = {{num, nct * rows}};
   if (den) outs.push_back({den, dct * rows});
-  Tail t{c, s, rlk, {}, nullptr, 0};
+  Tail t{c, s, rlk, {}, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) || (rc = check_ranges(outs, ins))) return rc;
   if (rows == 0) return CKKS_OK;
   CaptureScope cap(c, s);
   const uint64_t per = 3 * lim + 2 * lim + 2 * mid;
-  const int block = block_items(per, rows);
-  if ((rc = ensure_aux(c, block_reserve(per, rows)))) return rc;
+  const int block = t.hold.items(per, rows);
+  if ((rc = ensure_aux(c, t.hold.reserve(per, rows)))) return rc;
   uint64_t *X = c->aux, *D = X + 3 * lim * block, *Z = D + 2 * lim * block, *Y = Z + mid * block;
   const int ld = mask ? l - 1 : l;  // den's level
   const uint64_t side_words = den ? std::max(mask ? t.rescale_words(rows, l) : 0, t.sum_words(rows, ld)) : 0;
@@ -412,7 +417,7 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
   if (r) ins.push_back({r, lim * n_tok * n_row});
   if (carry) ins.push_back({carry, sct / 2 * n_row});
   if (state_in) ins.push_back({state_in, sct * n_grp});
-  Tail t{c, s, rlk, {}, nullptr, 0};
+  Tail t{c, s, rlk, {}, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) ||
       (rc = check_ranges({{y, yct * items}, {state_out, oct * n_grp}}, ins)))
     return rc;
@@ -422,12 +427,12 @@ int linattn_chunk(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* 
   // the states, Z the outputs before the sum; per group: the prefix sums carried
   // from one block of tokens to the next
   const uint64_t mid = 2ull * l * N, per = 3 * lim + (r ? mid : 0) + sct + yct;
-  const int gb = block_items(per + 3 * lim, n_grp);
+  const int gb = t.hold.items(per + 3 * lim, n_grp);
   constexpr int kLaunch = 8192;  // items of one launch
-  const int tb = std::min(block_items((per + 3 * lim) * gb, n_tok), std::max(1, kLaunch / gb));
+  const int tb = std::min(t.hold.items((per + 3 * lim) * gb, n_tok), std::max(1, kLaunch / gb));
   const uint64_t nb = (uint64_t)gb * tb;
   const uint64_t most = per * std::min<uint64_t>(items, kLaunch) + 3 * lim * std::min<uint64_t>(n_grp, kBlockItems);
-  if ((rc = ensure_aux(c, std::min(most, std::max(block_words(), per + 3 * lim))))) return rc;
+  if ((rc = ensure_aux(c, std::min(most, std::max(t.hold.block, per + 3 * lim))))) return rc;
   uint64_t *X = c->aux, *S = X + 3 * lim * nb, *Z = S + sct * nb, *C = Z + yct * nb, *P = C + (r ? mid * nb : 0);
   const int all = (int)items;
   const uint64_t side_words = std::max(r ? t.mul_words(all, l) : 0, carry ? t.mul_words(n_grp, l - 2) : 0);
@@ -508,15 +513,15 @@ int linattn_step(Ctx* c, const uint64_t* q, const uint64_t* k, const uint64_t* v
   std::vector<Range> ins = {{q, ct * n_grp}, {k, ct * n_grp}, {v, ct * n_grp}, {rlk, key_words(c)}};
   if (decay) ins.push_back({decay, lim * n_row});
   if (state_in) ins.push_back({state_in, in_ct * n_grp});
-  Tail t{c, s, rlk, {}, nullptr, 0};
+  Tail t{c, s, rlk, {}, {}, nullptr, 0};
   if ((rc = check_steps(c, steps, ins, &t.st)) ||
       (rc = check_ranges({{y, yct * n_grp}, {state_out, sct * n_grp}}, ins)))
     return rc;
   if (n_grp == 0) return CKKS_OK;
   CaptureScope cap(c, s);
   const uint64_t per = 3 * lim + yct;
-  const int block = block_items(per, n_grp);
-  if ((rc = ensure_aux(c, block_reserve(per, n_grp)))) return rc;
+  const int block = t.hold.items(per, n_grp);
+  if ((rc = ensure_aux(c, t.hold.reserve(per, n_grp)))) return rc;
   if ((rc = t.reserve(std::max({t.relin_words(n_grp, l, 1), t.relin_words(n_grp, l - 1, 1), t.sum_words(n_grp, l - 2)}))))
     return rc;
   uint64_t *X = c->aux, *Z = X + 3 * lim * block;

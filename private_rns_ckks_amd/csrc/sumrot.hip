@@ -441,22 +441,22 @@ static size_t group_words(const Ctx* c, int level, int n, int n_stage) {
   return n * (stage_words(c, level) + (n_stage > 1 ? 4 * (size_t)(level + 1) * c->N : 0));
 }
 
-// Items of a group: the launches' limit, or what 2 GiB hold (at N = 2^16 and
-// 24 + 8 limbs 17 with one stage, 12 with more).  Large groups share each key word among more items; two
+// Items of a group: the launches' limit, or what the words' limit holds (2 GiB
+// at N = 2^16 and 24 + 8 limbs: 17 with one stage, 12 with more).  Large groups share each key word among more items; two
 // half groups on two streams measured 0-14 % slower (keys are read twice).
-static int sum_group(const Ctx* c, int level, int batch, int n_stage) {
-  const size_t fit = kStepWords / group_words(c, level, 1, n_stage);
+static int sum_group(const Ctx* c, int level, int batch, int n_stage, uint64_t limit) {
+  const size_t fit = limit / group_words(c, level, 1, n_stage);
   return (int)std::max<size_t>(1, std::min<size_t>({fit, (size_t)kMaxChunk, (size_t)batch}));
 }
 
-size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage) {
-  return held_words(group_words(c, level, 1, n_stage), std::min(batch, kMaxChunk), kStepWords);
+size_t sum_ws_words(const Ctx* c, int level, int batch, int n_stage, uint64_t limit) {
+  return held_words(group_words(c, level, 1, n_stage), std::min(batch, kMaxChunk), limit);
 }
 
 int sum_stages(Ctx* c, hipStream_t s, const uint64_t* in, uint64_t in_stride, uint64_t* out, uint64_t out_stride,
-               int batch, int level, const ckks_sum_steps& st, uint64_t* ws) {
+               int batch, int level, const ckks_sum_steps& st, uint64_t* ws, uint64_t limit) {
   const uint64_t ct = 2ull * (level + 1) * c->N;
-  const int group = sum_group(c, level, batch, st.n_stage);
+  const int group = sum_group(c, level, batch, st.n_stage, limit);
   for (int b0 = 0; b0 < batch; b0 += group) {
     const int n = std::min(group, batch - b0);
     // the stages between the first and the last alternate between two buffers

@@ -1263,3 +1263,44 @@ def test_calls_no_larger_than_earlier_ones_can_be_captured(lib, orc, monkeypatch
         ctx.close()
     assert not failed, "\n".join(failed)
     ref_ctx.close()
+
+
+def test_block_limit_bounds_the_memory_of_a_call(lib, orc, sets, monkeypatch):
+    """CKKS_BLOCK_MB limits the operand buffer and each of the (at most two) workspaces of a call: with 16 MiB, sums
+    and mixes of 40 ciphertexts grow a new context by 3 x 16 MiB at most, where they would take over 200."""
+    torch = torch_cuda()
+    shape = SETS["mid"]
+    ctx, P = sets("mid")
+    announce("memory under a block limit")
+    st, (gal, keys) = steps(lib, P, [2, 2])
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    n, B = 6, 40
+    a, v = words(P, 1, "lima", n, (B, 2)), words(P, 1, "limv", n, (B, 2))
+    m = words(P, 1, "limm", n, (1,))
+    d_a, d_v, d_m = to_dev(a), to_dev(v), to_dev(m)
+    o, num, den = empty_dev((B, 2, n, P.N)), empty_dev((B, 2, n - 2, P.N)), empty_dev((B, 2, n - 1, P.N))
+
+    def calls(c):
+        lib.ckks_rotate_sum(c, d_a, o, B, n - 1, st)
+        lib.ckks_attn_mix(c, d_a, 1, d_v, 1, B, d_m, 1, n - 1, d_rlk, st, num, den)
+
+    calls(ctx)  # loads the kernels, creates the device's streams
+    fresh = make_pair(lib, orc, *shape)[0]
+    lib.ckks_attn_mix(fresh, d_a, 1, d_v, 1, 1, d_m, 1, n - 1, d_rlk, st, num, den)
+    torch.cuda.synchronize()
+    for t in (o, num, den):
+        t.zero_()
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    monkeypatch.setenv("CKKS_BLOCK_MB", "16")
+    calls(fresh)
+    torch.cuda.synchronize()
+    grown = before - torch.cuda.mem_get_info()[0]
+    assert grown <= (3 * 16 + 6) << 20, grown  # allocations come in 2 MiB
+    for b in (0, 1, B - 1):
+        same(o[b], orc.rotate_sum(P, n - 1, a[b], gal, keys), "sum")
+        ref = orc.attn_mix(P, n - 1, a[b, None, None, None], v[b, None, None], m[:, None], rlk, gal, keys)
+        same(num[b], ref[0][0, 0], "num")
+        same(den[b], ref[1][0, 0], "den")
+    fresh.close()
