@@ -1304,3 +1304,48 @@ def test_block_limit_bounds_the_memory_of_a_call(lib, orc, sets, monkeypatch):
         same(num[b], ref[0][0, 0], "num")
         same(den[b], ref[1][0, 0], "den")
     fresh.close()
+
+
+@pytest.mark.parametrize("T,G,R,read,carry,state,radices", [
+    (3, 5, 2, True, True, True, [2]), (4, 3, 3, False, True, False, []), (2, 6, 1, True, False, True, []),
+    (7, 2, 2, False, False, False, [2, 2]), (1, 9, 4, True, True, False, [])])
+def test_groups_and_tokens_in_small_blocks(lib, orc, sets, monkeypatch, T, G, R, read, carry, state, radices):
+    """1 MiB of intermediates: a chunk's groups in several blocks with a carried state, with and without a sum."""
+    monkeypatch.setenv("CKKS_BLOCK_MB", "1")
+    ctx, P = sets("small")
+    announce("small blocks T=%d G=%d R=%d read=%d carry=%d state=%d %s" % (T, G, R, read, carry, state, radices))
+    st, ref_st = steps(lib, P, radices)
+    rlk = key(P, 0, "rlk")
+    d = chunk_case(P, 5, T, G, R, read, carry, state, 60 + T)
+    y, out = run_chunk(lib, ctx, P, d, 5, T, G, R, rlk, st if radices else None)
+    ref = orc.linattn_chunk(P, 5, d["q"], d["k"], d["v"], d["w"], d["r"], d["carry"], d["state"], rlk, *ref_st)
+    same(y, ref[0], "y")
+    same(out, ref[1], "state")
+
+
+@pytest.mark.parametrize("M", [0, 2])
+def test_unsummed_calls_in_small_blocks(lib, orc, sets, monkeypatch, M):
+    """1 MiB of intermediates and no sum: blocks of scores, mixes (masked or not) and steps write their outputs in
+    place."""
+    monkeypatch.setenv("CKKS_BLOCK_MB", "1")
+    ctx, P = sets("small")
+    announce("unsummed small blocks M=%d" % M)
+    rlk = key(P, 0, "rlk")
+    d_rlk = to_dev(rlk)
+    a, v, m = words(P, 8, "ua", 6, (3, 3, 2, 2)), words(P, 8, "uv", 6, (3, 2, 2)), words(P, 8, "um", 6, (max(M, 1), 2))
+    low = 2 if M else 1
+    num, den = empty_dev((3, 3, 2, 6 - low, P.N)), empty_dev((3, 3, 2, 7 - low, P.N))
+    lib.ckks_attn_mix(ctx, to_dev(a), 3, to_dev(v), 2, 3, to_dev(m) if M else None, M, 5, d_rlk, None, num, den)
+    ref = orc.attn_mix(P, 5, a, v, m if M else None, rlk, [], [])
+    same(num, ref[0], "num")
+    same(den, ref[1], "den")
+    s = empty_dev((3, 3, 2, 2, 5, P.N))
+    lib.ckks_attn_scores(ctx, to_dev(a[:, :, 0]), 3, to_dev(v), 2, 3, 5, d_rlk, None, s)
+    same(s, orc.attn_scores(P, 5, a[:, :, 0], v, rlk, [], []), "scores")
+    q, k, w = (words(P, 9, "u" + x, 6, (9, 2)) for x in "qkx")
+    dec, s_in = (words(P, 9, "ud", 6, (M,)), words(P, 9, "us", 6, (9, 2))) if M else (None, words(P, 9, "us", 5, (9, 2)))
+    y, out = empty_dev((9, 2, 4, P.N)), empty_dev((9, 2, 5, P.N))
+    lib.ckks_linattn_step(ctx, to_dev(q), to_dev(k), to_dev(w), 9, dev(dec), M, to_dev(s_in), 5, d_rlk, None, y, out)
+    ref = orc.linattn_step(P, 5, q, k, w, dec, s_in, rlk, [], [])
+    same(y, ref[0], "y")
+    same(out, ref[1], "state")
