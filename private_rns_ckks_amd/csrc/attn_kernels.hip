@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void plain_mul_kernel(TopMulArgs a) {
 // (x0, x1) x (y0, y1) = (x0 y0, x0 y1 + x1 y0, x1 y1), plus a row times a
 // second ciphertext (the decayed state) in the same column sums; parts 0 and 1
 // leave ready for the rescales to come (drop_out).  8 products of 24 limbs at N
-// = 2^16 move 503 MB in 117-125 us (4.0-4.3 TB/s): memory, with five loads a
+// = 2^16 move 503 MB in 125-127 us (4.0 TB/s): memory, with five loads a
 // thread in flight; two words a thread take the same time.
 template <bool WIDE>
 __global__ __launch_bounds__(256) void pair_kernel(PairArgs a) {
@@ -124,7 +124,7 @@ __device__ __forceinline__ void weigh_add(const Split<WIDE>& w, uint64_t k0, uin
 // out[t] = sum of (w_j k_j) x v_j over j <= t: the running sums stay in
 // registers (canonical words: every prefix is a result), each operand is read
 // once and each prefix written once.  3 tokens of 2 groups of 24 limbs at N =
-// 2^16 move 650 MB in 160 us beside the products r q (4.1 TB/s).
+// 2^16 move 650 MB in 144-150 us beside the products r q (4.3-4.5 TB/s).
 template <bool WIDE>
 __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a) {
   const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
