@@ -74,6 +74,8 @@ enum {
 /* flags */
 #define CKKS_ROT_ACCUMULATE 1u /* ckks_rotate: out = in + Rot(in) */
 #define CKKS_NO_RESCALE 2u     /* ckks_mul_relin_rescale / ckks_ptmatvec: keep level l */
+#define CKKS_W_TRANSPOSED 4u   /* ckks_matmul_i8: d_w is [n_in][n_out] */
+#define CKKS_SCALE_IN 8u       /* ckks_matmul_i8: the channel scales are the inputs' */
 
 typedef struct ckks_ctx ckks_ctx;
 
@@ -136,7 +138,9 @@ typedef struct {
  * "moddown_conv", "rescale", "tensor", "ptmac", "ctmac", "add",
  * "const_mul", "term_mac" (polynomial evaluation's constant multiples),
  * "ip_gather", "sum_ip" (inner product of a stage of ckks_rotate_sum),
- * "attn_mac" (slotwise products of the attention calls).  NULL or "" stops tracing.
+ * "attn_mac" (slotwise products of the attention calls), "matmul_i8" (products
+ * of ckks_matmul_i8; a multiply-accumulate of a word and a byte counts 1),
+ * "layernorm" (slotwise products of the layer norm calls).  NULL or "" stops tracing.
  * Tracing adds two event records per traced launch and nothing else. */
 int ckks_trace_begin(ckks_ctx* ctx, const char* kernel);
 /* Waits for the recorded events, returns the totals and stops tracing. */
@@ -494,6 +498,113 @@ int ckks_linattn_step(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, c
                       const uint64_t* d_decay, int n_row, const uint64_t* d_state_in, int level,
                       const uint64_t* d_rlk, const ckks_sum_steps* steps, uint64_t* d_y, uint64_t* d_state_out,
                       ckks_stream_t stream);
+
+/* ---- linear layers and layer norms, a ciphertext a feature ----------------------
+ *
+ * A block of tokens as one ciphertext for each feature, the tokens along the
+ * slots (N/2 of them, of one sequence or several): x[b][i] is feature i of block
+ * b.  Sums over features are sums of ciphertexts, so a linear layer and a layer
+ * norm need no rotation; the calls of nonlinear layers (ckks_poly_eval_tree)
+ * take the features as their batch.  Slots without a token hold anything; a
+ * token row of zeros, or gradients of zero, keep them out of the results.
+ *
+ * Real constants (scales, weights, biases) are host doubles, rounded to the
+ * integer llround(v) next to them; from 2^62 on v is an integer itself.  They
+ * enter the words exactly, so results are the operations below word for word.
+ * An array may be shorter-lived than the work: it is read before the call
+ * returns, and a captured graph replays its constants.
+ *
+ * Buffers, streams and captures as in the attention calls, whose limits
+ * (CKKS_BLOCK_MB) hold here too; no internal stream is used. */
+
+/* Source: AEGIS summary, "Methodology", item 2 (each device multiplies its
+ * encrypted activations by its slices of the weights, locally).
+ * Product of encrypted features with a matrix of 8-bit integers:
+ *   acc[b][j] = sum_i w[j][i] (k_i x[b][i])        k_i with CKKS_SCALE_IN, else 1
+ *   y[b][j]   = rescale^d(tok[b % n_tok] k_j acc[b][j]) + round(bias[j] s_y)
+ *   k         = round(scales[.] q_level)
+ * d = (scales != NULL) + (d_tok != NULL) rescales, none without either.
+ *   d_x     [n_blk][n_in][2][level+1][N]
+ *   d_w     [n_out][n_in] bytes, with CKKS_W_TRANSPOSED [n_in][n_out]
+ *   scales  [n_out], with CKKS_SCALE_IN [n_in], or NULL: none
+ *   d_tok   [n_tok][level+1][N] plaintexts (a scale for each token), 1 <= n_tok
+ *           <= n_blk, or NULL with n_tok 0.  A zero removes a token.
+ *   bias    [n_out] or NULL; added to every slot, also to removed tokens'
+ *   d_y     [n_blk][n_out][2][level+1-d][N], at scale s_y = *out_scale:
+ *           scale; with d_tok alone scale tok_scale / q_level; with both
+ *           scale tok_scale / q_(level-1)
+ * The input's gradient of a layer y = diag(scales) w x is the same call on the
+ * outputs' gradients with CKKS_W_TRANSPOSED | CKKS_SCALE_IN, and n_in, n_out
+ * exchanged.  The noise of y is that of x, up to 128 n_in times as large.
+ * 1 <= n_in <= 65536; CKKS_ERANGE below level d; CKKS_EINVAL for a constant of
+ * 2^62 or more.  Needs no key and works with K = 0. */
+int ckks_matmul_i8(ckks_ctx* ctx, const uint64_t* d_x, int n_blk, int n_in, const int8_t* d_w, int n_out, int level,
+                   double scale, const double* scales, const uint64_t* d_tok, int n_tok, double tok_scale,
+                   const double* bias, unsigned flags, uint64_t* d_y, double* out_scale, ckks_stream_t stream);
+
+/* Layer norm over the features of each token, in two calls with the caller's
+ * polynomial for 1 / sqrt between them (ckks_poly_eval_tree on d_var; the pages
+ * replace nonlinear steps by polynomials, AEGIS summary, "Methodology", and fix
+ * none).  First half, per block b with F = n_feat, exact in every word:
+ *   S      = sum_i x_i
+ *   var    = rescale(rescale(relin(k (F sum_i x_i (x) x_i - S (x) S)))) + round(eps scale)
+ *   k      = round(q_l q_(l-1) / (F F) / scale)       l = level
+ * F sum x^2 - S^2 = F^2 variance, so var holds variance + eps at scale `scale`,
+ * two levels down, for one relinearisation a block.
+ *   d_x    [n_blk][n_feat][2][level+1][N] at `scale`
+ *   d_sum  [n_blk][2][level+1][N], for ckks_layernorm
+ *   d_var  [n_blk][2][level-1][N]
+ * The sums need log2(F F) bits above a feature's square: F^2 times the largest
+ * variance times scale^2 k stays below q_0 .. q_l / 2.  1 <= n_feat <= 65536;
+ * CKKS_ERANGE below level 2; CKKS_EINVAL when k rounds to 0 or a constant
+ * reaches 2^126. */
+int ckks_layernorm_var(ckks_ctx* ctx, const uint64_t* d_x, int n_blk, int n_feat, int level, double scale, double eps,
+                       const uint64_t* d_rlk, uint64_t* d_sum, uint64_t* d_var, ckks_stream_t stream);
+
+/* Second half: with r = rstd[b], t = rstd_level,
+ *   y_i = rescale(rescale(relin(k_i (F x_i - S) (x) r))) + round(beta_i scale)
+ *   k_i = round(gamma_i (q_t q_(t-1) / (F rstd_scale)))
+ * that is gamma_i (x_i - mean) rstd + beta_i, at scale `scale`.
+ *   d_x, d_sum    as in ckks_layernorm_var (read at limbs 0..t)
+ *   d_rstd        [n_blk][2][rstd_level+1][N] at rstd_scale, 2 <= rstd_level <= level
+ *   gamma, beta   [n_feat], or NULL: 1, 0.  With both NULL y is the normalised
+ *                 input that ckks_layernorm_grad takes; gamma and beta may then
+ *                 enter the next ckks_matmul_i8 as its inputs' scales and bias.
+ *   d_y           [n_blk][n_feat][2][rstd_level-1][N]
+ * One relinearisation a feature.  Errors as above. */
+int ckks_layernorm(ckks_ctx* ctx, const uint64_t* d_x, const uint64_t* d_sum, int n_blk, int n_feat, int level,
+                   double scale, const uint64_t* d_rstd, int rstd_level, double rstd_scale, const double* gamma,
+                   const double* beta, const uint64_t* d_rlk, uint64_t* d_y, ckks_stream_t stream);
+
+/* Backward pass, from the outputs' gradients dy (scale s), the normalised input
+ * xhat and r = rstd of the forward pass, l = level:
+ *   k_i      = round(gamma_i (q_(l-3) q_(l-4) / (F rstd_scale)))
+ *   G        = sum_i k_i dy_i
+ *   H        = rescale(rescale(relin(sum_i k_i dy_i (x) xhat_i)))             level l-2
+ *   R        = rescale(relin(c r (x) H)),                                     level l-3
+ *   c        = round(q_l / xhat_scale * q_(l-1) / xhat_scale * q_(l-2))
+ *   dx_i     = rescale(rescale(relin(r (x) (F k_i dy_i - G) - xhat_i (x) R)))   level l-5
+ *   dgamma_i = Sum(rescale(relin(sum_b dy_i[b] (x) xhat_i[b])))                 level l-1
+ *   dbeta_i  = Sum(sum_b dy_i[b])                                             level l
+ * that is dx = rstd (g - mean(g) - xhat mean(g xhat)) with g = gamma dy, at
+ * scale s (c makes both products' scales equal); dgamma at s xhat_scale / q_l;
+ * dbeta at s.  Sum runs over the tokens of a ciphertext (`steps`, as in the
+ * attention calls; NULL or no stages: the tokens' terms as they are).  Slots
+ * without a token need dy = 0.
+ *   d_dy      [n_blk][n_feat][2][level+1][N]
+ *   d_xhat    [n_blk][n_feat][2][xhat_level+1][N], level <= xhat_level
+ *   d_rstd    [n_blk][2][rstd_level+1][N], level <= rstd_level
+ *   gamma     [n_feat] or NULL: 1
+ *   d_dx      [n_blk][n_feat][2][level-4][N]      each may be NULL, but not
+ *   d_dgamma  [n_feat][2][level][N]               all of them
+ *   d_dbeta   [n_feat][2][level+1][N]
+ * xhat and rstd are read at limbs 0..level.  With n_blk 0, dgamma and dbeta are
+ * zero.  CKKS_ERANGE below level 5 with d_dx, 1 with d_dgamma; CKKS_EINVAL when c
+ * or k (before gamma) rounds to 0 or a constant reaches 2^126. */
+int ckks_layernorm_grad(ckks_ctx* ctx, const uint64_t* d_dy, int n_blk, int n_feat, int level, const uint64_t* d_xhat,
+                        int xhat_level, double xhat_scale, const uint64_t* d_rstd, int rstd_level, double rstd_scale,
+                        const double* gamma, const uint64_t* d_rlk, const ckks_sum_steps* steps, uint64_t* d_dx,
+                        uint64_t* d_dgamma, uint64_t* d_dbeta, ckks_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -81,6 +81,7 @@ def lib():
             "orc_poly_mul": (None, [u64p, u64p, u64p, c_int, c_int, u64p]),
             "orc_poly_add": (None, [u64p, u64p, u64p, c_int, c_int, u64p]),
             "orc_poly_sub": (None, [u64p, u64p, u64p, c_int, c_int, u64p]),
+            "orc_int_matmul": (None, [u64p, i8p, u64p, c_int, c_int, c_int, c_int, c_int, u64p]),
             "orc_from_signed": (None, [i64p, u64p, c_int, c_int, u64p]),
             "orc_modup": (None, [pp, c_int, c_int, u64p, u64p]),
             "orc_moddown": (None, [pp, c_int, u64p, u64p]),
@@ -566,6 +567,138 @@ def linattn_step(P: Params, level: int, q, k, v, decay, state, rlk, galois, evks
         ys.append(rotate_sum(P, level - 2, y, galois, evks))
         ss.append(s)
     return np.stack(ys), np.stack(ss)
+
+
+# ---------------------------------------------------------------------------
+# Linear layers and layer norms, a ciphertext a feature (readings: the pages
+# give no packing; doubles combine as written, constants are the integers next
+# to them)
+# ---------------------------------------------------------------------------
+
+def whole(v):
+    """The integer next to v, halves away from zero; from 2^52 on v is one."""
+    return int(v) if abs(v) >= 2.0 ** 52 else int(np.sign(v)) * int(np.floor(abs(v) + 0.5))
+
+
+def ct_times(P: Params, a, k):
+    """Ciphertext (any number of parts) times an integer."""
+    pt = np.stack([np.full(P.N, k % m, dtype=np.uint64) for m in P.q[: a.shape[1]]])
+    return ct_scale(P, a, pt)
+
+
+def ct_sub(P: Params, a, b):
+    return ct_add(P, a, ct_times(P, b, -1))
+
+
+def ct_plus(P: Params, a, k):
+    """Integer k (in NTT form: the same in every word) added to component 0."""
+    pt = np.stack([np.full(P.N, k % m, dtype=np.uint64) for m in P.q[: a.shape[1]]])
+    return np.stack([poly_add(P, a[0], pt)] + list(a[1:]))
+
+
+def ct_sum(P: Params, items):
+    acc = items[0]
+    for v in items[1:]:
+        acc = ct_add(P, acc, v)
+    return acc
+
+
+def int_matmul(P: Params, x, w):
+    """x [n_in] ciphertexts, w [n_out][n_in] int8 -> sum_i w[j][i] x[i]."""
+    x, w = _arr(x), np.ascontiguousarray(w, dtype=np.int8)
+    out = np.empty((w.shape[0],) + x.shape[1:], dtype=np.uint64)
+    lib().orc_int_matmul(_u64(x), w.ctypes.data_as(ctypes.POINTER(ctypes.c_int8)), _u64(out), x.shape[0], w.shape[0],
+                         x.shape[1], x.shape[2], P.log_n, _u64(P._mods))
+    return out
+
+
+def matmul_i8(P: Params, level: int, x, w, scale, scales=None, scale_in=False, tok=None, tok_scale=1.0, bias=None):
+    """x [B][n_in] ciphertexts, w [n_out][n_in] int8, tok [T] plaintexts or None
+    -> (y [B][n_out], its scale)."""
+    out_scale = scale
+    if tok is not None:
+        out_scale = out_scale * tok_scale / float(P.q[level - 1 if scales is not None else level])
+    k = None if scales is None else [whole(float(v) * float(P.q[level])) for v in scales]
+    ys = []
+    for b, xb in enumerate(x):
+        if k is not None and scale_in:
+            xb = np.stack([ct_times(P, v, m) for v, m in zip(xb, k)])
+        row = []
+        for j, y in enumerate(int_matmul(P, xb, w)):
+            lv = level
+            if k is not None and not scale_in:
+                y = ct_times(P, y, k[j])
+            if tok is not None:
+                y = ct_scale(P, y, tok[b % len(tok)])
+            for _ in range((k is not None) + (tok is not None)):
+                y, lv = rescale(P, lv, y), lv - 1
+            row.append(y if bias is None else ct_plus(P, y, whole(float(bias[j]) * out_scale)))
+        ys.append(row)
+    return np.array(ys), out_scale
+
+
+def layernorm_var(P: Params, level: int, x, scale, eps, rlk):
+    """x [B][F] ciphertexts -> (sums [B], variance + eps [B] at x's scale)."""
+    f = x.shape[1]
+    k = whole(float(P.q[level]) * float(P.q[level - 1]) / (float(f) * float(f)) / scale)
+    sums, var = [], []
+    for xb in x:
+        s = ct_sum(P, list(xb))
+        sq = ct_sum(P, [tensor(P, level, v, v) for v in xb])
+        d = ct_sub(P, ct_times(P, sq, f), tensor(P, level, s, s))
+        v = relin(P, level, ct_times(P, d, k), rlk)
+        sums.append(s)
+        var.append(ct_plus(P, rescale(P, level - 1, rescale(P, level, v)), whole(eps * scale)))
+    return np.stack(sums), np.stack(var)
+
+
+def _low(a, level):
+    return np.ascontiguousarray(a[..., : level + 1, :])
+
+
+def layernorm(P: Params, x, s, rstd, scale, rstd_scale, gamma, beta, rlk):
+    """x [B][F], s and rstd [B] ciphertexts -> gamma (x - mean) rstd + beta [B][F]."""
+    t, f = rstd.shape[-2] - 1, x.shape[1]
+    kappa = float(P.q[t]) * float(P.q[t - 1]) / (float(f) * rstd_scale)
+    ys = []
+    for xb, sb, r in zip(x, s, rstd):
+        row = []
+        for i, v in enumerate(xb):
+            d = ct_sub(P, ct_times(P, _low(v, t), f), _low(sb, t))
+            d = ct_times(P, d, whole((1.0 if gamma is None else float(gamma[i])) * kappa))
+            y = rescale(P, t - 1, rescale(P, t, relin(P, t, tensor(P, t, d, r), rlk)))
+            row.append(y if beta is None else ct_plus(P, y, whole(float(beta[i]) * scale)))
+        ys.append(row)
+    return np.array(ys)
+
+
+def layernorm_grad(P: Params, level: int, dy, xhat, rstd, xhat_scale, rstd_scale, gamma, rlk, galois, evks,
+                   parts=("dx", "dgamma", "dbeta")):
+    """dy, xhat [B][F], rstd [B] ciphertexts -> {"dx": [B][F], "dgamma": [F], "dbeta": [F]}."""
+    l, f, out = level, dy.shape[1], {}
+    if "dx" in parts:
+        q = [float(v) for v in P.q]
+        kappa = q[l - 3] * q[l - 4] / (float(f) * rstd_scale)
+        c = whole(q[l] / xhat_scale * q[l - 1] / xhat_scale * q[l - 2])
+        out["dx"] = []
+        for db, xb, r in zip(dy, xhat, rstd):
+            g = [ct_times(P, d, whole((1.0 if gamma is None else float(gamma[i])) * kappa)) for i, d in enumerate(db)]
+            h = relin(P, l, ct_sum(P, [tensor(P, l, u, _low(v, l)) for u, v in zip(g, xb)]), rlk)
+            h = rescale(P, l - 1, rescale(P, l, h))
+            rh = rescale(P, l - 2, relin(P, l - 2, ct_times(P, tensor(P, l - 2, _low(r, l - 2), h), c), rlk))
+            total, row, b = _low(ct_sum(P, g), l - 3), [], l - 3
+            for u, v in zip(g, xb):
+                d = ct_sub(P, ct_times(P, _low(u, b), f), total)
+                d = ct_sub(P, tensor(P, b, _low(r, b), d), tensor(P, b, _low(v, b), rh))
+                row.append(rescale(P, b - 1, rescale(P, b, relin(P, b, d, rlk))))
+            out["dx"].append(row)
+        out["dx"] = np.array(out["dx"])
+    if "dgamma" in parts:
+        d = [ct_sum(P, [tensor(P, l, u[i], _low(v[i], l)) for u, v in zip(dy, xhat)]) for i in range(f)]
+        out["dgamma"] = np.stack([rotate_sum(P, l - 1, rescale(P, l, relin(P, l, v, rlk)), galois, evks) for v in d])
+    if "dbeta" in parts:
+        out["dbeta"] = np.stack([rotate_sum(P, l, ct_sum(P, list(dy[:, i])), galois, evks) for i in range(f)])
+    return out
 
 
 # ---------------------------------------------------------------------------

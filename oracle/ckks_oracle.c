@@ -326,6 +326,25 @@ void orc_poly_sub(const uint64_t *a, const uint64_t *b, uint64_t *out, int nlimb
         for (uint64_t i = 0; i < n; i++) out[l * n + i] = submod(a[l * n + i], b[l * n + i], mods[l]);
 }
 
+/* Product with a matrix of small integers: out[j] = sum_i w[j][i] a[i] modulo
+ * each limb, a[n_in] and out[n_out] of `polys` polynomials of nlimb limbs each. */
+void orc_int_matmul(const uint64_t *a, const int8_t *w, uint64_t *out, int n_in, int n_out, int polys, int nlimb,
+                    int log_n, const uint64_t *mods)
+{
+    uint64_t n = (uint64_t)1 << log_n, item = (uint64_t)polys * nlimb * n;
+#pragma omp parallel for
+    for (int j = 0; j < n_out; j++)
+        for (uint64_t c = 0; c < item; c++) {
+            uint64_t m = mods[(c >> log_n) % nlimb], r = 0;
+            for (int i = 0; i < n_in; i++) {
+                int v = w[(uint64_t)j * n_in + i];
+                uint64_t t = mulmod(a[i * item + c], (uint64_t)(v < 0 ? -v : v), m);
+                r = v < 0 ? submod(r, t, m) : addmod(r, t, m);
+            }
+            out[j * item + c] = r;
+        }
+}
+
 /* Signed integer coefficient vector (length N) reduced into each limb. */
 void orc_from_signed(const int64_t *c, uint64_t *out, int nlimb, int log_n, const uint64_t *mods)
 {

@@ -98,6 +98,13 @@ int main(void)
     if (orc_poly_eval(&P, level, ya, 2, 1125899906842624.0, coeffs, 3, evk, out, &out_scale) != 0) return 22;
     if (!check_range(out, nq - 3, n, mod, 4) || !(out_scale > 0)) return 23;
 
+    /* integer matrix 3 x 2 on ciphertexts */
+    const int8_t im[6] = {-128, 127, 0, 5, -1, 1};
+    uint64_t *mo = malloc(sizeof(uint64_t) * 3 * ct);
+    orc_int_matmul(ya, im, mo, 2, 3, 2, nq, log_n, mod);
+    if (!check_range(mo, nq, n, mod, 6)) return 24;
+    free(mo);
+
     free(a);
     free(b);
     free(evk);

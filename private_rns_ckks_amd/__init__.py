@@ -11,6 +11,7 @@ missing: there is no fallback implementation.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -26,6 +27,8 @@ CKKS_EPARAM = -5
 CKKS_EINTERNAL = -6
 CKKS_ROT_ACCUMULATE = 1
 CKKS_NO_RESCALE = 2
+CKKS_W_TRANSPOSED = 4
+CKKS_SCALE_IN = 8
 
 EXPORTED = [
     "ckks_find_primes", "ckks_params_validate", "ckks_strerror", "ckks_last_error",
@@ -33,8 +36,8 @@ EXPORTED = [
     "ckks_ntt", "ckks_automorph", "ckks_keyswitch", "ckks_rotate", "ckks_rotate_noalloc", "ckks_rotate_hoisted",
     "ckks_rescale",
     "ckks_mul_relin_rescale", "ckks_poly_eval", "ckks_poly_eval_tree", "ckks_ptmatvec", "ckks_ctmatvec", "ckks_rotate_sum",
-    "ckks_attn_scores", "ckks_attn_mix", "ckks_linattn_chunk", "ckks_linattn_step", "ckks_trace_begin",
-    "ckks_trace_end", "ckks_probe_list", "ckks_probe_rate",
+    "ckks_attn_scores", "ckks_attn_mix", "ckks_linattn_chunk", "ckks_linattn_step", "ckks_matmul_i8", "ckks_layernorm_var", "ckks_layernorm",
+    "ckks_layernorm_grad", "ckks_trace_begin", "ckks_trace_end", "ckks_probe_list", "ckks_probe_rate",
 ]
 
 # Kernel whose launches take the largest share of a rotation batch (by
@@ -82,6 +85,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     vp, u64p, u32p = ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint32)
     i, u32 = ctypes.c_int, ctypes.c_uint32
+    f64, f64p = ctypes.c_double, ctypes.POINTER(ctypes.c_double)
     pp = ctypes.POINTER(vp)
     sp = ctypes.POINTER(ckks_sum_steps)
     sig = {
@@ -111,6 +115,10 @@ def _load():
         "ckks_attn_mix": (i, [vp, vp, i, vp, i, i, vp, i, i, vp, sp, vp, vp, vp]),
         "ckks_linattn_chunk": (i, [vp, vp, vp, vp, i, i, vp, vp, vp, i, vp, i, vp, sp, vp, vp, vp]),
         "ckks_linattn_step": (i, [vp, vp, vp, vp, i, vp, i, vp, i, vp, sp, vp, vp, vp]),
+        "ckks_matmul_i8": (i, [vp, vp, i, i, vp, i, i, f64, f64p, vp, i, f64, f64p, ctypes.c_uint, vp, f64p, vp]),
+        "ckks_layernorm_var": (i, [vp, vp, i, i, i, f64, f64, vp, vp, vp, vp]),
+        "ckks_layernorm": (i, [vp, vp, vp, i, i, i, f64, vp, i, f64, f64p, f64p, vp, vp, vp]),
+        "ckks_layernorm_grad": (i, [vp, vp, i, i, i, vp, i, f64, vp, i, f64, f64p, vp, sp, vp, vp, vp, vp]),
         "ckks_trace_begin": (i, [vp, ctypes.c_char_p]),
         "ckks_trace_end": (i, [vp, ctypes.POINTER(ckks_trace_stats)]),
         "ckks_probe_list": (i, [ctypes.c_char_p, i]),
@@ -492,6 +500,82 @@ def ckks_linattn_step(ctx, d_q, d_k, d_v, n_grp, d_decay, n_row, d_state_in, lev
         level, _dev(ctx, d_rlk, ctx.key_words, "d_rlk"), _steps(ctx, steps),
         _dev(ctx, d_y, _w(n_grp, 2, _drop(nl, 2), ctx.N), "d_y"),
         _dev(ctx, d_state_out, _w(n_grp, 2, ns, ctx.N), "d_state_out"), _stream(stream)), "ckks_linattn_step")
+
+
+def _doubles(vals, n, what):
+    """C array of n host doubles (None stays None); n None or negative skips the length check."""
+    if vals is None:
+        return None
+    a = array.array("d")
+    try:  # a float64 array goes over whole
+        m = memoryview(vals)
+        if m.format != "d" or not m.c_contiguous:
+            raise TypeError
+        a.frombytes(m.cast("B"))
+    except TypeError:
+        a.extend(float(v) for v in vals)
+    if n is not None and n >= 0:
+        _count(a, n, what)
+    return (ctypes.c_double * len(a)).from_buffer(a) if len(a) else (ctypes.c_double * 1)()
+
+
+def ckks_matmul_i8(ctx, d_x, n_blk, n_in, d_w, n_out, level, scale, d_y, scales=None, d_tok=None, n_tok=0, tok_scale=1.0,
+                   bias=None, flags=0, stream=None):
+    """Product of features with an int8 matrix; returns the output scale."""
+    nl = _lvl(ctx, level)
+    x = _dev(ctx, d_x, _w(n_blk, n_in, 2, nl, ctx.N), "d_x")
+    if d_w is None or not getattr(d_w, "is_cuda", False) or str(d_w.dtype) != "torch.int8":
+        raise ArgumentError("d_w must be an int8 device tensor")
+    if d_w.device.index is not None and d_w.device.index != ctx.device:
+        raise ArgumentError("d_w is on device %d, the context on device %d" % (d_w.device.index, ctx.device))
+    if not d_w.is_contiguous():
+        raise ArgumentError("tensor must be contiguous")
+    if n_in >= 0 and n_out >= 0 and d_w.numel() < n_in * n_out:
+        raise ArgumentError("d_w holds %d bytes; the call touches %d" % (d_w.numel(), n_in * n_out))
+    y = _dev(ctx, d_y, _w(n_blk, n_out, 2, _drop(nl, (scales is not None) + (d_tok is not None)), ctx.N), "d_y")
+    out_scale = ctypes.c_double(0.0)
+    _check(_lib.ckks_matmul_i8(ctx.handle, x, n_blk, n_in, ctypes.c_void_p(d_w.data_ptr()), n_out, level, float(scale),
+                               _doubles(scales, n_in if flags & CKKS_SCALE_IN else n_out, "scales"),
+                               _dev(ctx, d_tok, _w(n_tok, nl, ctx.N), "d_tok", optional=True), n_tok, float(tok_scale),
+                               _doubles(bias, n_out, "bias"), flags, y, ctypes.byref(out_scale), _stream(stream)),
+           "ckks_matmul_i8")
+    return out_scale.value
+
+
+def ckks_layernorm_var(ctx, d_x, n_blk, n_feat, level, scale, eps, d_rlk, d_sum, d_var, stream=None):
+    """Sums of the features and their variance plus eps (at scale `scale`, two levels down)."""
+    nl = _lvl(ctx, level)
+    _check(_lib.ckks_layernorm_var(ctx.handle, _dev(ctx, d_x, _w(n_blk, n_feat, 2, nl, ctx.N), "d_x"), n_blk, n_feat,
+                                   level, float(scale), float(eps), _dev(ctx, d_rlk, ctx.key_words, "d_rlk"),
+                                   _dev(ctx, d_sum, _w(n_blk, 2, nl, ctx.N), "d_sum"),
+                                   _dev(ctx, d_var, _w(n_blk, 2, _drop(nl, 2), ctx.N), "d_var"), _stream(stream)),
+           "ckks_layernorm_var")
+
+
+def ckks_layernorm(ctx, d_x, d_sum, n_blk, n_feat, level, scale, d_rstd, rstd_level, rstd_scale, gamma, beta, d_rlk, d_y,
+                   stream=None):
+    nl, nr = _lvl(ctx, level), _lvl(ctx, rstd_level)
+    _check(_lib.ckks_layernorm(ctx.handle, _dev(ctx, d_x, _w(n_blk, n_feat, 2, nl, ctx.N), "d_x"),
+                               _dev(ctx, d_sum, _w(n_blk, 2, nl, ctx.N), "d_sum"), n_blk, n_feat, level, float(scale),
+                               _dev(ctx, d_rstd, _w(n_blk, 2, nr, ctx.N), "d_rstd"), rstd_level, float(rstd_scale),
+                               _doubles(gamma, n_feat, "gamma"), _doubles(beta, n_feat, "beta"),
+                               _dev(ctx, d_rlk, ctx.key_words, "d_rlk"),
+                               _dev(ctx, d_y, _w(n_blk, n_feat, 2, _drop(nr, 2), ctx.N), "d_y"), _stream(stream)),
+           "ckks_layernorm")
+
+
+def ckks_layernorm_grad(ctx, d_dy, n_blk, n_feat, level, d_xhat, xhat_level, xhat_scale, d_rstd, rstd_level, rstd_scale,
+                        gamma, d_rlk, steps, d_dx=None, d_dgamma=None, d_dbeta=None, stream=None):
+    """Gradients of a layer norm's input, weight and bias; those left out are not computed."""
+    nl, nx, nr = _lvl(ctx, level), _lvl(ctx, xhat_level), _lvl(ctx, rstd_level)
+    _check(_lib.ckks_layernorm_grad(
+        ctx.handle, _dev(ctx, d_dy, _w(n_blk, n_feat, 2, nl, ctx.N), "d_dy"), n_blk, n_feat, level,
+        _dev(ctx, d_xhat, _w(n_blk, n_feat, 2, nx, ctx.N), "d_xhat"), xhat_level, float(xhat_scale),
+        _dev(ctx, d_rstd, _w(n_blk, 2, nr, ctx.N), "d_rstd"), rstd_level, float(rstd_scale),
+        _doubles(gamma, n_feat, "gamma"), _dev(ctx, d_rlk, ctx.key_words, "d_rlk"), _steps(ctx, steps),
+        _dev(ctx, d_dx, _w(n_blk, n_feat, 2, _drop(nl, 5), ctx.N), "d_dx", optional=True),
+        _dev(ctx, d_dgamma, _w(n_feat, 2, _drop(nl, 1), ctx.N), "d_dgamma", optional=True),
+        _dev(ctx, d_dbeta, _w(n_feat, 2, nl, ctx.N), "d_dbeta", optional=True), _stream(stream)), "ckks_layernorm_grad")
 
 
 def ckks_trace_begin(ctx, kernel):

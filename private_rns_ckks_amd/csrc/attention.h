@@ -54,6 +54,20 @@ int launch_plain_mul(Ctx* c, hipStream_t s, const PlainMul& m, uint64_t* out, ui
 // words between items of either.
 int rescale_mul_fused(Ctx* c, hipStream_t s, const PlainMul& m, const uint64_t* v, uint64_t* w, uint64_t per, int batch);
 
+// Rescales of n products by their top `drop` (1 or 2) limbs, in one transform:
+// `top` holds the dropped limbs q_(level+1-drop)..q_level ([2][drop][N] an item, used up), `out` the limbs
+// that stay times the inverses of the dropped primes ([2][level+1-drop][N] an
+// item, in place).  add (optional): a constant for component 0 of item b,
+// add[(i * n_add + (first + b) % n_add) * 2] in limb i.  ws holds 2 (level+1) N
+// words an item of a chunk, one at least.
+struct ProductRescale {
+  uint64_t *top, *out;
+  int n, level, drop;
+  const uint64_t* add;
+  int n_add, first;
+};
+int rescale_products(Ctx* c, hipStream_t s, const ProductRescale& p, uint64_t* ws, uint64_t ws_words);
+
 // What the products below do to their output for ks_rescale: parts 0 and 1 of
 // the limbs that stay after `drop` rescales are multiplied by the inverses of
 // the dropped primes and get `add` added (item's words [2][nl - drop][N], or

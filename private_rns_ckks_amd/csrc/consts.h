@@ -1,0 +1,37 @@
+// Real constants of a call as integers on the device: the host rounds them,
+// kernels take them modulo each prime with their Shoup quotients.
+#pragma once
+#include <math.h>
+
+#include "attention.h"
+
+namespace ckks {
+
+// m * 2^e: an integer next to a double.
+struct Whole {
+  int64_t m;
+  int e;
+};
+
+// round(x), halves away from zero, for |x| < 2^126; false when out of range or
+// not a number.  From 2^62 on x is an integer itself.
+inline bool whole(double x, Whole* out) {
+  if (!(fabs(x) < 0x1p126)) return false;
+  if (fabs(x) < 0x1p62) {
+    *out = Whole{(int64_t)llround(x), 0};
+    return true;
+  }
+  int e;
+  const double f = frexp(x, &e);  // 0.5 <= |f| < 1
+  *out = Whole{(int64_t)ldexp(f, 53), e - 53};
+  return true;
+}
+
+// Tables of n constants for the limbs i < nl, limb by limb:
+// table[(i * n + j) * 2] = {k_j mod q_i, Shoup quotient}.  With drop > 0, limbs
+// i <= nl - 1 - drop hold k_j (q_(nl-1) .. q_(nl-drop))^-1 instead, which turns
+// a product into the term that the rescales to come keep (DropOut).
+inline uint64_t const_words(int n, int nl) { return (uint64_t)n * nl * 2; }
+int launch_consts(Ctx* c, hipStream_t s, const Whole* k, int n, int nl, int drop, uint64_t* table);
+
+}  // namespace ckks

@@ -10,6 +10,8 @@
 //   out_i = c_i * [q_l^-1]_{q_i} - NTT(w_i)          (mod q_i)
 #include <string.h>
 
+#include <algorithm>
+
 #include "attention.h"
 #include "kernels.h"
 #include "ntt_core.h"
@@ -176,13 +178,19 @@ __global__ __launch_bounds__(kThreads) void rescale_mul_row_kernel(MulRowArgs a)
 // ---------------------------------------------------------------------------
 // The rescales of a key switch (ks_rescale).
 struct DropArgs {
-  uint64_t* A;  // item b: A + b*per, [2][comp_limbs][N]: dropped limbs q_(l-drop+1)..q_l first
+  uint64_t* A;  // item b: A + b*a_per, [2][comp_limbs][N]: dropped limbs q_(l-drop+1)..q_l first
   uint64_t* W;  // item b: W + b*per, [2][l+1][N]
-  uint64_t per;
+  uint64_t a_per, per;
   const uint64_t* tab;  // as RescalePassArgs
   const PrimeConst* prime;
   const uint64_t* tw;
   int log_n, level, L, drop, comp_limbs;
+  // rescales of products (rescale_products): their other limbs, in place, and
+  // what is added to component 0 of item b's: add[(i * n_add + (first + b) % n_add) * 2]
+  uint64_t* out;  // item b: out + b*out_bstride, [2][l+1-drop][N]
+  uint64_t out_bstride;
+  const uint64_t* add;
+  int n_add, first;
 };
 
 // The centred lift of x mod the dropped prime ql, modulo q.
@@ -192,20 +200,22 @@ __device__ __forceinline__ uint64_t lift_mod(uint64_t x, uint64_t half, uint64_t
 }
 
 // The values dropped, canonical, in place: v = iNTT(R)_l = A_l - w_l and, for
-// a second rescale, v' = (A_(l-1) - w_(l-1) - v) q_l^-1 mod q_(l-1).
+// a second rescale, v' = (A_(l-1) - w_(l-1) - v) q_l^-1 mod q_(l-1).  FRESH:
+// there is no w (a product's rescale, not a key switch's).
+template <bool FRESH>
 __global__ __launch_bounds__(256) void drop_values_kernel(DropArgs a) {
   const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
   const int comp = blockIdx.y, l = a.level;
-  uint64_t* v = a.A + blockIdx.z * a.per + ((uint64_t)(comp * a.comp_limbs) << a.log_n) + c;
+  uint64_t* v = a.A + blockIdx.z * a.a_per + ((uint64_t)(comp * a.comp_limbs) << a.log_n) + c;
   const uint64_t* w = a.W + blockIdx.z * a.per + ((uint64_t)(comp * (l + 1)) << a.log_n) + c;
   const uint64_t N = 1ull << a.log_n;
   const PrimeConst& pl = a.prime[l];
-  const uint64_t x = sub_mod(v[(a.drop - 1) * N], reduce64(w[l * N], pl.q, pl.inv1), pl.q);
-  v[(a.drop - 1) * N] = x;
+  const uint64_t x = FRESH ? v[(a.drop - 1) * N] : sub_mod(v[(a.drop - 1) * N], reduce64(w[l * N], pl.q, pl.inv1), pl.q);
+  if (!FRESH) v[(a.drop - 1) * N] = x;
   if (a.drop == 1) return;
   const PrimeConst& p = a.prime[l - 1];
   const uint64_t* rs = a.tab + ((uint64_t)l * a.L + l - 1) * 4;
-  uint64_t u = sub_mod(v[0], reduce64(w[(l - 1) * N], p.q, p.inv1), p.q);
+  uint64_t u = FRESH ? v[0] : sub_mod(v[0], reduce64(w[(l - 1) * N], p.q, p.inv1), p.q);
   u = sub_mod(u, lift_mod(x, (pl.q - 1) / 2, rs[2], p.q, p.inv1), p.q);
   v[0] = reduce_2q(mul_shoup(u, rs[0], rs[1], p.q), p.q);
 }
@@ -215,15 +225,16 @@ __global__ __launch_bounds__(256) void drop_values_kernel(DropArgs a) {
 // q_l gets -q_l mod q added and needs no reduction, since the Shoup product
 // takes any 64-bit word.  w is congruent, below 6q (below q for primes above
 // 2^60), a product below 2q, so the sums stay below 8 * 2^60 or 2^64.  The
-// result is left below 2q, as the first butterflies take it.
-template <int DROP>
+// result is left below 2q, as the first butterflies take it.  FRESH: w is zero
+// and not read.
+template <int DROP, bool FRESH>
 struct DropIO {
   typedef NoOps Ops;
   uint64_t* w;
   const uint64_t* v[DROP];
   uint64_t q, qinv[DROP], qinvp[DROP], neg[DROP], half[DROP];
   __device__ __forceinline__ uint64_t load(uint32_t j) const {
-    uint64_t x = w[j];
+    uint64_t x = FRESH ? 0 : w[j];
 #pragma unroll
     for (int d = 0; d < DROP; ++d) {
       const uint64_t y = v[d][j];
@@ -236,19 +247,19 @@ struct DropIO {
   __device__ __forceinline__ void store(uint32_t j, uint64_t x, const Ops&) const { w[j] = x; }
 };
 
-template <int RA, int RB, int LOGN, int DROP>
+template <int RA, int RB, int LOGN, int DROP, bool FRESH>
 __global__ __launch_bounds__(kThreads) void drop_col_kernel(DropArgs a) {
   constexpr int ROWS = 1 << (RA + RB);
   __shared__ uint64_t lds[lds_words<true, RB, ROWS>()];
   const int low = a.level + 1 - DROP;
   const int comp = blockIdx.y / low, i = blockIdx.y % low;
   const PrimeConst& pc = a.prime[i];
-  DropIO<DROP> io;
+  DropIO<DROP, FRESH> io;
   io.w = a.W + blockIdx.z * a.per + ((uint64_t)(comp * (a.level + 1) + i) << a.log_n);
 #pragma unroll
   for (int d = 0; d < DROP; ++d) {  // q_l first
     const uint64_t* rs = a.tab + ((uint64_t)(a.level - d) * a.L + i) * 4;
-    io.v[d] = a.A + blockIdx.z * a.per + ((uint64_t)(comp * a.comp_limbs + DROP - 1 - d) << a.log_n);
+    io.v[d] = a.A + blockIdx.z * a.a_per + ((uint64_t)(comp * a.comp_limbs + DROP - 1 - d) << a.log_n);
     io.qinv[d] = rs[0];
     io.qinvp[d] = rs[1];
     io.neg[d] = pc.q - rs[2];
@@ -260,7 +271,96 @@ __global__ __launch_bounds__(kThreads) void drop_col_kernel(DropArgs a) {
                                       fin);
 }
 
+// The row pass of products' rescale: what the limbs that stay keep is in `out`
+// already, times the inverses of the dropped primes.
+struct ProductCombineIO {
+  struct Ops {
+    uint64_t c;
+  };
+  const uint64_t* w;
+  uint64_t* out;
+  uint64_t q, add;
+  __device__ __forceinline__ uint64_t load(uint32_t j) const { return w[j]; }
+  __device__ __forceinline__ void after_load(uint32_t, uint64_t) const {}
+  __device__ __forceinline__ Ops fetch(uint32_t j) const { return Ops{out[j]}; }
+  __device__ __forceinline__ void store(uint32_t j, uint64_t x, const Ops& o) const {
+    out[j] = add_mod(sub_mod(o.c, x, q), add, q);
+  }
+};
+
+template <int RA, int RB, int LOGN>
+__global__ __launch_bounds__(kThreads) void product_row_kernel(DropArgs a) {
+  constexpr int ROWS = 1 << (RA + RB);
+  __shared__ uint64_t lds[lds_words<false, RB, ROWS>()];
+  const GridPos gp = row_grid_pos();
+  const int low = a.level + 1 - a.drop;
+  const int comp = gp.job / low, i = gp.job % low;
+  const PrimeConst& pc = a.prime[i];
+  ProductCombineIO io;
+  io.w = a.W + gp.item * a.per + ((uint64_t)(comp * (a.level + 1) + i) << a.log_n);
+  io.out = a.out + gp.item * a.out_bstride + ((uint64_t)gp.job << a.log_n);
+  io.q = pc.q;
+  io.add = a.add && comp == 0 ? a.add[((uint64_t)i * a.n_add + (a.first + gp.item) % a.n_add) * 2] : 0;
+  Finish fin{1, 0, 0, pc.inv1};
+  run_pass<RA, RB, false, false, LOGN>(io, lds, gp.tile, a.log_n, a.tw + ((uint64_t)i << (a.log_n + 1)), pc.q, fin);
+}
+
 }  // namespace
+
+int rescale_products(Ctx* c, hipStream_t s, const ProductRescale& p, uint64_t* ws, uint64_t ws_words) {
+  const uint32_t N = c->N;
+  const int log_n = (int)c->log_n, lc = logb_col(log_n), lr = logb_row(log_n), level = p.level, drop = p.drop;
+  const int low = level + 1 - drop;
+  const uint64_t a_per = 2ull * drop * N, w_per = 2ull * (level + 1) * N;
+  const int chunk = (int)std::max<uint64_t>(1, std::min<uint64_t>(kMaxChunk, ws_words / w_per));
+  auto fc = drop == 1 ? CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 1, true)
+                      : CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 2, true);
+  auto fr = CKKS_PICK_PASS(product_row_kernel, log_n, lr);
+  if (!fc || !fr) return set_error(CKKS_EINTERNAL, "unsupported N");
+  NttJobs jobs;
+  for (int comp = 0; comp < 2; ++comp)
+    for (int k = 0; k < drop; ++k) jobs.add(comp * drop + k, comp * drop + k, low + k);
+  DropArgs a;
+  memset(&a, 0, sizeof(a));
+  a.per = w_per;
+  a.tab = c->d_rescale;
+  a.prime = c->d_prime;
+  a.tw = c->d_tw_fwd;
+  a.log_n = log_n;
+  a.level = level;
+  a.L = (int)c->L;
+  a.drop = drop;
+  a.comp_limbs = drop;
+  a.out_bstride = 2ull * low * N;
+  a.add = p.add;
+  a.n_add = p.n_add;
+  for (int b0 = 0; b0 < p.n; b0 += chunk) {
+    const int n = std::min(chunk, p.n - b0);
+    uint64_t* A = p.top + b0 * a_per;
+    int rc = ntt_run(c, s, A, A, a_per, a_per, n, jobs, true, true);
+    if (rc) return rc;
+    DropArgs v = a;
+    v.A = A;
+    v.W = ws;
+    v.out = p.out + b0 * a.out_bstride;
+    v.first = p.first + b0;
+    v.a_per = a_per;
+    if (drop == 2) {
+      TraceScope ts(c, s, "rescale", (double)n * 2 * N);
+      hipLaunchKernelGGL(drop_values_kernel<true>, dim3(N / 256, 2, n), dim3(256), 0, s, v);
+      CKKS_HIP_CHECK(hipGetLastError());
+    }
+    {
+      TraceScope ts(c, s, "rescale", (double)n * 2 * low * ((double)(N / 2) * lc + drop * N));
+      hipLaunchKernelGGL(fc, dim3(pass_tiles(N, lc), 2 * low, n), dim3(kThreads), 0, s, v);
+      CKKS_HIP_CHECK(hipGetLastError());
+    }
+    TraceScope ts(c, s, "rescale", (double)n * 2 * low * ((double)(N / 2) * lr + N));
+    hipLaunchKernelGGL(fr, dim3(pass_tiles(N, lr), 2 * low, n), dim3(kThreads), 0, s, v);
+    CKKS_HIP_CHECK(hipGetLastError());
+  }
+  return CKKS_OK;
+}
 
 int rescale_mul_fused(Ctx* c, hipStream_t s, const PlainMul& m, const uint64_t* v, uint64_t* w, uint64_t per, int batch) {
   const uint32_t N = c->N;
@@ -298,9 +398,10 @@ int drop_col_pass(Ctx* c, hipStream_t s, uint64_t* A, uint64_t* W, uint64_t per,
   const uint32_t N = c->N;
   const int log_n = (int)c->log_n, lc = logb_col(log_n), low = level + 1 - drop;
   DropArgs a;
+  memset(&a, 0, sizeof(a));
   a.A = A;
   a.W = W;
-  a.per = per;
+  a.a_per = a.per = per;
   a.tab = c->d_rescale;
   a.prime = c->d_prime;
   a.tw = c->d_tw_fwd;
@@ -311,10 +412,11 @@ int drop_col_pass(Ctx* c, hipStream_t s, uint64_t* A, uint64_t* W, uint64_t per,
   a.comp_limbs = comp_limbs;
   {
     TraceScope ts(c, s, "rescale", (double)n_items * 2 * drop * N);
-    hipLaunchKernelGGL(drop_values_kernel, dim3(N / 256, 2, n_items), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(drop_values_kernel<false>, dim3(N / 256, 2, n_items), dim3(256), 0, s, a);
     CKKS_HIP_CHECK(hipGetLastError());
   }
-  auto fn = drop == 1 ? CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 1) : CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 2);
+  auto fn = drop == 1 ? CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 1, false)
+                       : CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 2, false);
   if (!fn) return set_error(CKKS_EINTERNAL, "unsupported N");
   TraceScope ts(c, s, "rescale", (double)n_items * 2 * low * ((double)(N / 2) * lc + drop * N));
   hipLaunchKernelGGL(fn, dim3(pass_tiles(N, lc), 2 * low, n_items), dim3(kThreads), 0, s, a);
