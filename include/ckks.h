@@ -550,7 +550,9 @@ int ckks_matmul_i8(ckks_ctx* ctx, const uint64_t* d_x, int n_blk, int n_in, cons
  *   var    = rescale(rescale(relin(k (F sum_i x_i (x) x_i - S (x) S)))) + round(eps scale)
  *   k      = round(q_l q_(l-1) / (F F) / scale)       l = level
  * F sum x^2 - S^2 = F^2 variance, so var holds variance + eps at scale `scale`,
- * two levels down, for one relinearisation a block.
+ * two levels down, for one relinearisation a block.  eps may be any number:
+ * eps - 1 hands the polynomial u = variance + eps - 1, small around a variance
+ * of 1, where (1 + u)^-1/2 has small coefficients.
  *   d_x    [n_blk][n_feat][2][level+1][N] at `scale`
  *   d_sum  [n_blk][2][level+1][N], for ckks_layernorm
  *   d_var  [n_blk][2][level-1][N]
