@@ -33,11 +33,12 @@ int matmul_i8(Ctx* c, const uint64_t* x, int n_blk, int n_in, const int8_t* w, i
   else if (tok)
     s_out = s_out * tok_scale / (double)c->mod[l];
   const bool in = flags & CKKS_SCALE_IN;
-  // the constants carry the dropped primes' inverses, so a token row alone needs one: 1
-  const int n_k = scales ? (in ? n_in : n_out) : drop;
-  std::vector<Whole> k(n_k, Whole{1, 0}), kb(bias ? n_out : 0);
-  for (int j = 0; scales && j < n_k; ++j)
-    if (!whole(scales[j] * (double)c->mod[l], &k[j]) || k[j].e)
+  // Constants of the outputs and, with CKKS_SCALE_IN, the inputs; the dropped
+  // primes' inverses go with either.
+  const int n_ki = in ? n_in : 0, n_k = scales && !in ? n_out : 1;
+  std::vector<Whole> ki(n_ki), k(n_k, Whole{1, 0}), kb(bias ? n_out : 0);
+  for (int j = 0; scales && j < (in ? n_ki : n_k); ++j)
+    if (Whole* v = in ? &ki[j] : &k[j]; !whole(scales[j] * (double)c->mod[l], v) || v->e)
       return set_error(CKKS_EINVAL, "a rounded channel scale reaches 2^62");
   for (size_t j = 0; j < kb.size(); ++j)
     if (!whole(bias[j] * s_out, &kb[j]) || kb[j].e) return set_error(CKKS_EINVAL, "a rounded bias reaches 2^62");
@@ -55,20 +56,25 @@ int matmul_i8(Ctx* c, const uint64_t* x, int n_blk, int n_in, const int8_t* w, i
   const int fit = (int)std::min<uint64_t>({items, kGroup, std::max<uint64_t>(1, drop ? hold.block / top : items)});
   const int gj = std::min(fit, n_out), gb = std::min(n_blk, std::max(1, fit / n_out));
   const uint64_t w_per = 2ull * nl * N;
-  const uint64_t pack_words = matmul_pack_words(n_in, n_out), kw = const_words(n_k, nl), bw = const_words((int)kb.size(), nl);
+  const uint64_t pack_words = matmul_pack_words(n_in, n_out), kw = const_words(n_k, nl), iw = const_words(n_ki, nl);
+  const uint64_t bw = const_words((int)kb.size(), nl);
   const uint64_t tops = drop ? held_words(top, std::min(items, kGroup), hold.block) : 0;
   const uint64_t step = drop ? held_words(w_per, std::min<uint64_t>(items, kMaxChunk), hold.step) : 0;
   auto even = [](uint64_t v) { return (v + 1) & ~1ull; };  // 16-byte parts
-  if ((rc = ensure_aux(c, tops + even(pack_words) + kw + bw)) || (drop && (rc = ensure_workspace(c, step)))) return rc;
-  uint64_t *T = c->aux, *pack = T + tops, *tk = pack + even(pack_words), *tb = tk + kw;
-  if (n_k && (rc = launch_consts(c, s, k.data(), n_k, nl, drop, tk))) return rc;
+  if ((rc = ensure_aux(c, tops + even(pack_words) + 2 * kw + iw + bw)) || (drop && (rc = ensure_workspace(c, step)))) return rc;
+  uint64_t *T = c->aux, *pack = T + tops, *tk = pack + even(pack_words), *ti = tk + 2 * kw, *tb = ti + iw;
+  if ((rc = launch_consts(c, s, k.data(), n_k, nl, in ? 0 : drop, tk))) return rc;
+  for (Whole& v : k) v.e = 32;
+  if ((rc = launch_consts(c, s, k.data(), n_k, nl, in ? 0 : drop, tk + kw))) return rc;
+  if (in && (rc = launch_consts(c, s, ki.data(), n_ki, nl, drop, ti))) return rc;
   if (!kb.empty() && (rc = launch_consts(c, s, kb.data(), n_out, nl, 0, tb))) return rc;
   MatArgs a;
   memset(&a, 0, sizeof(a));
   a.x = x;
   a.w = w;
-  a.kin = n_k && in ? tk : nullptr;
-  a.kout = n_k && !in ? tk : nullptr;
+  a.kin = in ? ti : nullptr;
+  a.kout = tk;
+  a.kout32 = tk + kw;
   a.bias = bias && drop == 0 ? tb : nullptr;
   a.n_kout = n_k;
   a.tok = tok;
