@@ -154,6 +154,7 @@ static int build_tables(Ctx* c) {
     uint64_t inv = m;  // Newton iteration: inverse of odd m modulo 2^64
     for (int it = 0; it < 6; ++it) inv *= 2 - m * inv;
     k.mprime = 0 - inv;
+    k.top = (uint64_t)(((host::u128)1 << (64 - __builtin_clzll(k.q) + 25)) / k.q);
   }
   int rc = upload((void**)&c->d_prime, pc.data(), pc.size() * sizeof(PrimeConst));
   if (rc) return rc;

@@ -20,7 +20,7 @@ struct PrimeConst {
   uint64_t ninv;   // N^-1 mod q
   uint64_t ninvp;  // Shoup quotient of ninv
   uint64_t mprime; // -q^-1 mod 2^64 (Montgomery reduction)
-  uint64_t pad;
+  uint64_t top;    // floor(2^(b+25) / q), b the bits of q: quotients of sums below 2^25 q
 };
 
 // Basis-conversion constants for ModUp of digit j at level l (device copy at

@@ -13,7 +13,7 @@ struct MatArgs {
   const uint64_t* x;     // [n_blk][n_in][2][nl][N]
   const int8_t* w;       // element (j, i) at j * w_row + i * w_col
   const uint64_t* kin;   // constants of the inputs (consts.h, n = n_in), or NULL
-  const uint64_t *kout, *kout32;  // of the outputs (n = n_kout: n_out or one for all), and those times 2^32
+  const uint64_t* kout;  // of the outputs (n = n_kout: n_out or one for all)
   const uint64_t* bias;  // added to component 0 (n = n_out; drop 0), or NULL
   const uint64_t* tok;   // [n_tok][nl][N], row b % n_tok, or NULL
   uint64_t* out;         // [2][nl - drop][N] an item

@@ -61,11 +61,9 @@ int matmul_i8(Ctx* c, const uint64_t* x, int n_blk, int n_in, const int8_t* w, i
   const uint64_t tops = drop ? held_words(top, std::min(items, kGroup), hold.block) : 0;
   const uint64_t step = drop ? held_words(w_per, std::min<uint64_t>(items, kMaxChunk), hold.step) : 0;
   auto even = [](uint64_t v) { return (v + 1) & ~1ull; };  // 16-byte parts
-  if ((rc = ensure_aux(c, tops + even(pack_words) + 2 * kw + iw + bw)) || (drop && (rc = ensure_workspace(c, step)))) return rc;
-  uint64_t *T = c->aux, *pack = T + tops, *tk = pack + even(pack_words), *ti = tk + 2 * kw, *tb = ti + iw;
+  if ((rc = ensure_aux(c, tops + even(pack_words) + kw + iw + bw)) || (drop && (rc = ensure_workspace(c, step)))) return rc;
+  uint64_t *T = c->aux, *pack = T + tops, *tk = pack + even(pack_words), *ti = tk + kw, *tb = ti + iw;
   if ((rc = launch_consts(c, s, k.data(), n_k, nl, in ? 0 : drop, tk))) return rc;
-  for (Whole& v : k) v.e = 32;
-  if ((rc = launch_consts(c, s, k.data(), n_k, nl, in ? 0 : drop, tk + kw))) return rc;
   if (in && (rc = launch_consts(c, s, ki.data(), n_ki, nl, drop, ti))) return rc;
   if (!kb.empty() && (rc = launch_consts(c, s, kb.data(), n_out, nl, 0, tb))) return rc;
   MatArgs a;
@@ -74,7 +72,6 @@ int matmul_i8(Ctx* c, const uint64_t* x, int n_blk, int n_in, const int8_t* w, i
   a.w = w;
   a.kin = in ? ti : nullptr;
   a.kout = tk;
-  a.kout32 = tk + kw;
   a.bias = bias && drop == 0 ? tb : nullptr;
   a.n_kout = n_k;
   a.tok = tok;

@@ -157,26 +157,43 @@ __device__ __forceinline__ void digits4(const uint64_t* x, uint32_t (&dig)[ND]) 
   }
 }
 
-// a w0 + b w1 mod q, canonical; below 2^56 (ND < 8) the cheaper quotients' 8q fits.
-template <int ND>
-__device__ __forceinline__ uint64_t join(uint64_t a, const ulonglong2& w0, uint64_t b, const ulonglong2& w1, uint64_t q) {
-  if (ND == 8) return reduce_4q(mul_shoup(a, w0.x, w0.y, q) + mul_shoup(b, w1.x, w1.y, q), q);
-  uint64_t v = mul_shoup_lazy_split(a, w0.x, w0.y, q);
-  if (ND > 4) v += mul_shoup_lazy_split(b, w1.x, w1.y, q);
-  v = v >= 4 * q ? v - 4 * q : v;
-  return reduce_4q(v, q);
-}
+// A sum S = lo + 2^32 hi of words below q times bytes, |S| < 2^23 q, modulo q: with
+// 2^24 q added (lo0, hi0; 2^56 go from hi to lo, which then is positive) it is U
+// 2^32 + its low dword, below 2^25 q.  h, its bits from b - 7 on (b those of q), is
+// below 2^32, and h 2^(b-7) / q = h m / 2^32 is less than 1 + 2^-6 below S / q, m =
+// floor(2^(b+25) / q) and h being cut off: the whole part leaves a remainder
+// below 3q.
+struct SumMod {
+  int64_t lo0, hi0;
+  uint64_t nq;
+  uint32_t m;
+  int sh;
+  bool big;  // b - 7 >= 32: h comes out of U
+  __device__ __forceinline__ explicit SumMod(uint64_t q, uint32_t quot) : nq(0 - q), m(quot) {
+    lo0 = (int64_t)((q & 0xff) << 24) + (1ll << 56);
+    hi0 = (int64_t)(q >> 8) - (1ll << 24);
+    const int b = 64 - __builtin_clzll(q);
+    big = b >= 39;
+    sh = big ? b - 39 : b - 7;
+  }
+  __device__ __forceinline__ uint64_t rem(int64_t lo, int64_t hi) const {
+    const uint64_t u = (uint64_t)hi + ((uint64_t)lo >> 32);
+    const uint32_t u1 = (uint32_t)(u >> 32), u0 = (uint32_t)u, l0 = (uint32_t)lo;
+    const uint32_t h = big ? __builtin_amdgcn_alignbit(u1, u0, sh) : __builtin_amdgcn_alignbit(u0, l0, sh);
+    const uint32_t e = __umulhi(h, m);
+    const uint64_t r = mad64(e, (uint32_t)nq, (uint64_t)u0 << 32 | l0);
+    return r + ((uint64_t)(e * (uint32_t)(nq >> 32)) << 32);
+  }
+};
 
 template <int ND, int WM, int WN, bool SCALED>
 __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const uint4* pack, int chunks, int row_blocks,
                                                               int col_blocks) {
   static_assert(WM * WN == 4, "four waves");
   constexpr int KS = 128 / WN, NC = KS / 32, W = 32 * WN, ROWS = 32 * WM;  // inputs and chunks of a step, a tile
-  __shared__ union {
-    uint4 dig[2][ND][KS / 16][W];
-    ulonglong2 sums[16][256];  // the epilogue's
-  } lds;
-  __shared__ ulonglong2 kc[ROWS][2];  // {k, Shoup}, {2^32 k, Shoup} of the tile's outputs
+  constexpr int AHEAD = ND < 8 && !SCALED ? 2 : 1;  // steps that words load ahead: as many as the registers hold
+  __shared__ uint4 dig[2][ND][KS / 16][W];
+  __shared__ ulonglong2 kc[ROWS];  // {k, Shoup} of the tile's outputs
   __shared__ ulonglong2 kin[2][SCALED ? KS : 1];
   // Workgroups go round the 8 XCDs: each takes a range of the words, the tiles
   // of the same words next to each other, so that its L2 reads them once.
@@ -197,46 +214,47 @@ __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const u
   for (int r = tid; r < ROWS; r += 256) {  // outputs past the last: those of the last
     const int j = a.n_kout > 1 ? a.j0 + min(rb * ROWS + r, a.nj - 1) : 0;
     const uint64_t at = ((uint64_t)i * a.n_kout + j) * 2;
-    kc[r][0] = *(const ulonglong2*)(a.kout + at);
-    kc[r][1] = *(const ulonglong2*)(a.kout32 + at);
+    kc[r] = *(const ulonglong2*)(a.kout + at);
   }
 
-  uint64_t raw[16];
-  v4i frag[NC], fnext[NC];
+  uint64_t raw[2][16];
+  v4i frag[2][NC];
   const v4i* wp = (const v4i*)pack + (uint64_t)(rb * WM + wm) * chunks * 64 + lane;
-  // a step's words and matrix; past the last step those of the last again
-  auto load = [&](int t, v4i (&f)[NC]) {
+  // a step's matrix and words; past the last step those of the last again
+  auto load_matrix = [&](int t, v4i (&f)[NC]) {
     t = min(t, steps - 1);
 #pragma unroll
     for (int c = 0; c < NC; ++c) f[c] = wp[(t * NC + c) * 64];
+  };
+  auto load = [&](int t, uint64_t (&v)[16]) {
+    t = min(t, steps - 1);
     const uint64_t* p = x + (uint64_t)group_start(t * (KS / 16) + grp, a.n_in) * ct + col;
 #pragma unroll
-    for (int k = 0; k < 16; ++k, p += ct) raw[k] = *p;
+    for (int k = 0; k < 16; ++k, p += ct) v[k] = *p;
   };
   // the constants of step t's inputs, by way of one thread each
   auto kin_load = [&](int t) {
     const int g = min(t, steps - 1) * (KS / 16) + tid / 16;
     return SCALED && tid < KS ? kin_i[group_start(g, a.n_in) + tid % 16] : ulonglong2{};
   };
-  auto convert = [&](int t, int buf) {
+  auto convert = [&](int t, uint64_t (&v)[16]) {
     uint32_t part[ND][4];
     if (SCALED) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const ulonglong2 w = kin[t & 1][grp * 16 + k];
-        raw[k] = ND == 8 ? reduce_2q(mul_shoup(raw[k], w.x, w.y, pc.q), pc.q)
-                         : reduce_4q(mul_shoup_lazy_split(raw[k], w.x, w.y, pc.q), pc.q);
+        v[k] = reduce_4q(mul_shoup_lazy_split(v[k], w.x, w.y, pc.q), pc.q);
       }
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       uint32_t o[ND];
-      digits4<ND>(raw + 4 * g, o);
+      digits4<ND>(v + 4 * g, o);
 #pragma unroll
       for (int d = 0; d < ND; ++d) part[d][g] = o[d];
     }
 #pragma unroll
-    for (int d = 0; d < ND; ++d) lds.dig[buf][d][grp][col] = make_uint4(part[d][0], part[d][1], part[d][2], part[d][3]);
+    for (int d = 0; d < ND; ++d) dig[t & 1][d][grp][col] = make_uint4(part[d][0], part[d][1], part[d][2], part[d][3]);
   };
 
   v16i acc[ND];
@@ -244,7 +262,9 @@ __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const u
   for (int d = 0; d < ND; ++d)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[d][r] = 0;
-  load(0, frag);
+  load_matrix(0, frag[0]);
+  load(0, raw[0]);
+  if (AHEAD == 2) load(1, raw[1]);
   if (SCALED) {
     const ulonglong2 k0 = kin_load(0), k1 = kin_load(1);
     if (tid < KS) {
@@ -253,43 +273,36 @@ __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const u
     }
     __syncthreads();
   }
-  convert(0, 0);
+  convert(0, raw[0]);
   __syncthreads();
-  for (int t = 0; t < steps; ++t) {
-    const int buf = t & 1;
-    load(t + 1, fnext);
+  // step t reads buffer t & 1 (here a constant), and lays step t + 1's digits,
+  // whose words are in `next`, in the other
+  auto step = [&](int t, int buf, uint64_t (&next)[16], uint64_t (&after)[16]) {
+    load_matrix(t + 1, frag[buf ^ 1]);
+    load(t + AHEAD, AHEAD == 2 ? after : next);
     const ulonglong2 kn = kin_load(t + 2);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
-        const v4i f = *(const v4i*)&lds.dig[buf][d][c * 2 + (lane >> 5)][wn * 32 + (lane & 31)];
-        acc[d] = __builtin_amdgcn_mfma_i32_32x32x32_i8(frag[c], f, acc[d], 0, 0, 0);
+        const v4i f = *(const v4i*)&dig[buf][d][c * 2 + (lane >> 5)][wn * 32 + (lane & 31)];
+        acc[d] = __builtin_amdgcn_mfma_i32_32x32x32_i8(frag[buf][c], f, acc[d], 0, 0, 0);
       }
     }
-    convert(t + 1, buf ^ 1);
-    if (SCALED) {
-      // step t + 2's constants take the place of step t's, which every thread
-      // read before the last barrier
-      if (tid < KS) kin[buf][tid] = kn;
-    }
+    convert(buf ^ 1, next);
+    // step t + 2's constants take the place of step t's, which every thread
+    // read before the last barrier
+    if (SCALED && tid < KS) kin[buf][tid] = kn;
     __syncthreads();
-#pragma unroll
-    for (int c = 0; c < NC; ++c) frag[c] = fnext[c];
+  };
+  int t = 0;  // no branch in the loop's body: the last steps load and lay out words again
+  for (; t + 1 < steps; t += 2) {
+    step(t, 0, raw[1], raw[0]);
+    step(t + 1, 1, raw[0], raw[1]);
   }
+  if (t < steps) step(t, 0, raw[1], raw[0]);
 
-  // sum_d acc_d 2^(8d) = lo + 2^32 hi, either below 2^55 in magnitude; a multiple
-  // of q from 2^55 on makes them positive
-  const int64_t offset = (int64_t)(((1ull << 55) / pc.q + 1) * pc.q);
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    int64_t lo = offset, hi = offset;
-#pragma unroll
-    for (int d = 0; d < 4; ++d) lo += (int64_t)acc[d][r] * (1 << (8 * d));
-#pragma unroll
-    for (int d = 4; d < ND; ++d) hi += (int64_t)acc[d][r] * (1 << (8 * (d - 4)));
-    lds.sums[r][tid] = make_ulonglong2((uint64_t)lo, (uint64_t)hi);
-  }
+  const SumMod mod(pc.q, (uint32_t)((ConstPrime)a.prime)[i].top);
   const int word = col0 + wn * 32 + (lane & 31);
   const uint64_t tok = a.tok ? a.tok[((uint64_t)((a.b0 + b) % a.n_tok) * a.nl + i << a.log_n) + word] : 0;
   const uint64_t* bias = a.bias && comp == 0 ? a.bias + (uint64_t)i * a.n_out * 2 : nullptr;
@@ -298,13 +311,16 @@ __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const u
   const uint64_t per = (uint64_t)(i < low ? 2 * low : 2 * a.drop) << a.log_n;
   const int row0 = wm * 32 + (lane >> 5) * 4;
   uint64_t* o = (i < low ? a.out : a.top) + at + word + ((uint64_t)b * a.nj + rb * ROWS) * per;
-  // through LDS (a thread's own words): the registers' indexes are constants
-  // above, and this loop's code stays small
-#pragma unroll 4
+#pragma unroll
   for (int r = 0; r < 16; ++r) {
     const int row = row0 + (r >> 2) * 8 + (r & 3), j = rb * ROWS + row;
-    const ulonglong2 v2 = lds.sums[r][tid];
-    uint64_t v = join<ND>(v2.x, kc[row][0], v2.y, kc[row][1], pc.q);
+    int64_t lo = mod.lo0, hi = mod.hi0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) lo += (int64_t)acc[d][r] * (1 << (8 * d));
+#pragma unroll
+    for (int d = 4; d < ND; ++d) hi += (int64_t)acc[d][r] * (1 << (8 * (d - 4)));
+    const ulonglong2 k = kc[row];
+    uint64_t v = reduce_4q(mul_shoup_lazy_split(mod.rem(lo, hi), k.x, k.y, pc.q), pc.q);
     if (a.tok) v = mul_mod(v, tok, pc.q, pc.r64, pc.r64p, pc.inv1);
     if (j < a.nj) {
       if (bias) v = add_mod(v, bias[2 * (a.j0 + j)], pc.q);
