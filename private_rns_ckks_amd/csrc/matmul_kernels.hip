@@ -157,6 +157,12 @@ __device__ __forceinline__ void digits4(const uint64_t* x, uint32_t (&dig)[ND]) 
   }
 }
 
+// a - m if that is not negative, else a, by the borrow.
+__device__ __forceinline__ uint64_t below(uint64_t a, uint64_t m) {
+  uint64_t t;
+  return __builtin_sub_overflow(a, m, &t) ? a : t;
+}
+
 // A sum S = lo + 2^32 hi of words below q times bytes, |S| < 2^23 q, modulo q: with
 // 2^24 q added (lo0, hi0; 2^56 go from hi to lo, which then is positive) it is U
 // 2^32 + its low dword, below 2^25 q.  h, its bits from b - 7 on (b those of q), is
@@ -186,12 +192,13 @@ struct SumMod {
   }
 };
 
-template <int ND, int WM, int WN, bool SCALED>
-__global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const uint4* pack, int chunks, int row_blocks,
+template <int ND, int WM, int WN, int MT, bool SCALED>
+__global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatArgs a, const uint4* pack, int chunks, int row_blocks,
                                                               int col_blocks) {
   static_assert(WM * WN == 4, "four waves");
-  constexpr int KS = 128 / WN, NC = KS / 32, W = 32 * WN, ROWS = 32 * WM;  // inputs and chunks of a step, a tile
-  constexpr int AHEAD = ND < 8 && !SCALED ? 2 : 1;  // steps that words load ahead: as many as the registers hold
+  static_assert(sizeof(uint4) * 2 * ND * 256 >= sizeof(uint64_t) * 16 * 256, "the epilogue's words fit the digits' place");
+  constexpr int KS = 128 / WN, NC = KS / 32, W = 32 * WN, ROWS = 32 * WM * MT;  // inputs and chunks of a step, a tile
+  constexpr int AHEAD = MT;  // steps that words load ahead: as many as the registers hold
   __shared__ uint4 dig[2][ND][KS / 16][W];
   __shared__ ulonglong2 kc[ROWS];  // {k, Shoup} of the tile's outputs
   __shared__ ulonglong2 kin[2][SCALED ? KS : 1];
@@ -218,13 +225,15 @@ __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const u
   }
 
   uint64_t raw[2][16];
-  v4i frag[2][NC];
-  const v4i* wp = (const v4i*)pack + (uint64_t)(rb * WM + wm) * chunks * 64 + lane;
+  v4i frag[2][NC][MT];
+  const v4i* wp = (const v4i*)pack + (uint64_t)(rb * WM + wm) * MT * chunks * 64 + lane;
   // a step's matrix and words; past the last step those of the last again
-  auto load_matrix = [&](int t, v4i (&f)[NC]) {
+  auto load_matrix = [&](int t, v4i (&f)[NC][MT]) {
     t = min(t, steps - 1);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) f[c] = wp[(t * NC + c) * 64];
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) f[c][m] = wp[(m * chunks + t * NC + c) * 64];
   };
   auto load = [&](int t, uint64_t (&v)[16]) {
     t = min(t, steps - 1);
@@ -237,31 +246,33 @@ __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const u
     const int g = min(t, steps - 1) * (KS / 16) + tid / 16;
     return SCALED && tid < KS ? kin_i[group_start(g, a.n_in) + tid % 16] : ulonglong2{};
   };
-  auto convert = [&](int t, uint64_t (&v)[16]) {
-    uint32_t part[ND][4];
+  // words 4g..4g+3 into their digits; then all 16 into buffer t & 1
+  uint32_t part[ND][4];
+  auto quarter = [&](int t, uint64_t (&v)[16], int g) {
     if (SCALED) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
+      for (int k = 4 * g; k < 4 * g + 4; ++k) {
         const ulonglong2 w = kin[t & 1][grp * 16 + k];
-        v[k] = reduce_4q(mul_shoup_lazy_split(v[k], w.x, w.y, pc.q), pc.q);
+        v[k] = below(below(mul_shoup_lazy_split(v[k], w.x, w.y, pc.q), 2 * pc.q), pc.q);
       }
     }
+    uint32_t o[ND];
+    digits4<ND>(v + 4 * g, o);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      uint32_t o[ND];
-      digits4<ND>(v + 4 * g, o);
-#pragma unroll
-      for (int d = 0; d < ND; ++d) part[d][g] = o[d];
-    }
+    for (int d = 0; d < ND; ++d) part[d][g] = o[d];
+  };
+  auto put = [&](int t) {
 #pragma unroll
     for (int d = 0; d < ND; ++d) dig[t & 1][d][grp][col] = make_uint4(part[d][0], part[d][1], part[d][2], part[d][3]);
   };
 
-  v16i acc[ND];
+  v16i acc[MT][ND];
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[d][r] = 0;
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[m][d][r] = 0;
   load_matrix(0, frag[0]);
   load(0, raw[0]);
   if (AHEAD == 2) load(1, raw[1]);
@@ -273,23 +284,49 @@ __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const u
     }
     __syncthreads();
   }
-  convert(0, raw[0]);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) quarter(0, raw[0], g);
+  put(0);
   __syncthreads();
   // step t reads buffer t & 1 (here a constant), and lays step t + 1's digits,
   // whose words are in `next`, in the other
   auto step = [&](int t, int buf, uint64_t (&next)[16], uint64_t (&after)[16]) {
-    load_matrix(t + 1, frag[buf ^ 1]);
+    load_matrix(t + 1, frag[buf ^ 1]);  // before the words: loads return in order
     load(t + AHEAD, AHEAD == 2 ? after : next);
     const ulonglong2 kn = kin_load(t + 2);
+    // a chunk's digits are read while the one before is multiplied
+    v4i f[2][ND];
+    auto digits = [&](int c) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) f[c & 1][d] = *(const v4i*)&dig[buf][d][c * 2 + (lane >> 5)][wn * 32 + (lane & 31)];
+    };
+    digits(0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
+      if (c + 1 < NC) digits(c + 1);
 #pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const v4i f = *(const v4i*)&dig[buf][d][c * 2 + (lane >> 5)][wn * 32 + (lane & 31)];
-        acc[d] = __builtin_amdgcn_mfma_i32_32x32x32_i8(frag[buf][c], f, acc[d], 0, 0, 0);
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m][d] = __builtin_amdgcn_mfma_i32_32x32x32_i8(frag[buf][c][m], f[c & 1][d], acc[m][d], 0, 0, 0);
+      if (AHEAD == 2) {  // the words are here: split them between the matrix instructions
+#pragma unroll
+        for (int g = c * 4 / NC; g < (c + 1) * 4 / NC; ++g) quarter(buf ^ 1, next, g);
+#pragma unroll
+        for (int d = 0; d < ND * MT; ++d) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction,
+          if (c + 1 < NC && d < ND) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read of the next chunk's,
+          __builtin_amdgcn_sched_group_barrier(0x002, (SCALED ? 34 : 9) * 4 / NC / MT, 0);  // and conversions
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    convert(buf ^ 1, next);
+    if (AHEAD == 1) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) quarter(buf ^ 1, next, g);
+    }
+    put(buf ^ 1);
     // step t + 2's constants take the place of step t's, which every thread
     // read before the last barrier
     if (SCALED && tid < KS) kin[buf][tid] = kn;
@@ -302,6 +339,11 @@ __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const u
   }
   if (t < steps) step(t, 0, raw[1], raw[0]);
 
+  // 2^(8d) out of the compiler's sight: one multiply-add a digit, not a sign
+  // extension, a shift and an addition
+  int place[4] = {1, 1 << 8, 1 << 16, 1 << 24};
+#pragma unroll
+  for (int d = 0; d < 4; ++d) asm("" : "+s"(place[d]));
   const SumMod mod(pc.q, (uint32_t)((ConstPrime)a.prime)[i].top);
   const int word = col0 + wn * 32 + (lane & 31);
   const uint64_t tok = a.tok ? a.tok[((uint64_t)((a.b0 + b) % a.n_tok) * a.nl + i << a.log_n) + word] : 0;
@@ -309,22 +351,32 @@ __global__ __launch_bounds__(256, 2) void matmul_tiles_kernel(MatArgs a, const u
   const int low = a.nl - a.drop;
   const uint64_t at = i < low ? ((uint64_t)(comp * low + i) << a.log_n) : ((uint64_t)(comp * a.drop + i - low) << a.log_n);
   const uint64_t per = (uint64_t)(i < low ? 2 * low : 2 * a.drop) << a.log_n;
-  const int row0 = wm * 32 + (lane >> 5) * 4;
-  uint64_t* o = (i < low ? a.out : a.top) + at + word + ((uint64_t)b * a.nj + rb * ROWS) * per;
+  const int row0 = wm * MT * 32 + (lane >> 5) * 4;
+  uint64_t* o = (i < low ? a.out : a.top) + at + word + ((uint64_t)b * a.nj + rb * ROWS + row0) * per;
+  uint64_t(*rems)[256] = (uint64_t(*)[256])dig;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int row = row0 + (r >> 2) * 8 + (r & 3), j = rb * ROWS + row;
-    int64_t lo = mod.lo0, hi = mod.hi0;
+  for (int m = 0; m < MT; ++m) {
+    // through LDS (a thread's own words): the registers' indexes are constants
+    // here, and the code of the rest stays small
 #pragma unroll
-    for (int d = 0; d < 4; ++d) lo += (int64_t)acc[d][r] * (1 << (8 * d));
+    for (int r = 0; r < 16; ++r) {
+      int64_t lo = mod.lo0, hi = mod.hi0;
 #pragma unroll
-    for (int d = 4; d < ND; ++d) hi += (int64_t)acc[d][r] * (1 << (8 * (d - 4)));
-    const ulonglong2 k = kc[row];
-    uint64_t v = reduce_4q(mul_shoup_lazy_split(mod.rem(lo, hi), k.x, k.y, pc.q), pc.q);
-    if (a.tok) v = mul_mod(v, tok, pc.q, pc.r64, pc.r64p, pc.inv1);
-    if (j < a.nj) {
-      if (bias) v = add_mod(v, bias[2 * (a.j0 + j)], pc.q);
-      o[row * per] = v;
+      for (int d = 0; d < 4; ++d) lo += (int64_t)acc[m][d][r] * place[d];
+#pragma unroll
+      for (int d = 4; d < ND; ++d) hi += (int64_t)acc[m][d][r] * place[d - 4];
+      rems[r][tid] = mod.rem(lo, hi);
+    }
+#pragma unroll 4
+    for (int r = 0; r < 16; ++r) {
+      const int up = m * 32 + (r >> 2) * 8 + (r & 3), j = rb * ROWS + row0 + up;
+      const ulonglong2 k = kc[row0 + up];
+      uint64_t v = below(below(mul_shoup_lazy_split(rems[r][tid], k.x, k.y, pc.q), 2 * pc.q), pc.q);
+      if (a.tok) v = mul_mod(v, tok, pc.q, pc.r64, pc.r64p, pc.inv1);
+      if (j < a.nj) {
+        if (bias) v = add_mod(v, bias[2 * (a.j0 + j)], pc.q);
+        o[up * per] = v;
+      }
     }
   }
 }
@@ -339,33 +391,35 @@ constexpr int kTileRows = 9;
 bool tiled(int n_in, int nj) { return nj >= kTileRows && n_in >= 16; }
 
 struct Tiles {
-  int wm, wn, row_blocks, chunks;
+  int wm, wn, mt, row_blocks, chunks;
   Tiles(int n_in, int nj) {
     wm = nj > 64 ? 4 : nj > 32 ? 2 : 1;
-    if (getenv("XWM")) wm = atoi(getenv("XWM"));
+    mt = nj > 128 ? 2 : 1;
     wn = 4 / wm;
-    row_blocks = (nj + 32 * wm - 1) / (32 * wm);
+    row_blocks = (nj + rows() - 1) / rows();
     const int nc = 4 / wn;
     chunks = ((n_in + 31) / 32 + nc - 1) / nc * nc;
   }
-  uint64_t words() const { return (uint64_t)row_blocks * wm * chunks * 128; }
+  int rows() const { return 32 * wm * mt; }
+  uint64_t lanes() const { return (uint64_t)row_blocks * wm * mt * chunks * 64; }
 };
 
 template <int ND, bool SCALED>
-auto pick_rows(int wm) {
-  return wm == 4   ? matmul_tiles_kernel<ND, 4, 1, SCALED>
-         : wm == 2 ? matmul_tiles_kernel<ND, 2, 2, SCALED>
-                   : matmul_tiles_kernel<ND, 1, 4, SCALED>;
+auto pick_rows(const Tiles& t) {
+  return t.mt == 2   ? matmul_tiles_kernel<ND, 4, 1, 2, SCALED>
+         : t.wm == 4 ? matmul_tiles_kernel<ND, 4, 1, 1, SCALED>
+         : t.wm == 2 ? matmul_tiles_kernel<ND, 2, 2, 1, SCALED>
+                     : matmul_tiles_kernel<ND, 1, 4, 1, SCALED>;
 }
 template <int ND>
-auto pick_tiles(int wm, bool scaled) {
-  return scaled ? pick_rows<ND, true>(wm) : pick_rows<ND, false>(wm);
+auto pick_tiles(const Tiles& t, bool scaled) {
+  return scaled ? pick_rows<ND, true>(t) : pick_rows<ND, false>(t);
 }
 
 }  // namespace
 
 uint64_t matmul_pack_words(int n_in, int nj) {
-  return std::max(Tiles(n_in, nj).words(), (uint64_t)((nj + kRows - 1) / kRows) * n_in);
+  return std::max(2 * Tiles(n_in, nj).lanes(), (uint64_t)((nj + kRows - 1) / kRows) * n_in);
 }
 
 int launch_matmul(Ctx* c, hipStream_t s, const MatArgs& a, uint64_t* pack) {
@@ -376,17 +430,17 @@ int launch_matmul(Ctx* c, hipStream_t s, const MatArgs& a, uint64_t* pack) {
     const uint64_t cols = (uint64_t)a.nb * 2 * a.nl * (c->N / (32 * t.wn));
     const uint64_t blocks = (cols + 7) / 8 * 8 * t.row_blocks;
     if (blocks > 0x7fffffff) return set_error(CKKS_EINTERNAL, "too many tiles");
-    const uint64_t lanes = (uint64_t)t.row_blocks * t.wm * t.chunks * 64;
+    const uint64_t lanes = t.lanes();
     hipLaunchKernelGGL(pack_tiles_kernel, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, a, t.chunks,
-                       t.row_blocks * t.wm, (uint4*)pack);
+                       t.row_blocks * t.wm * t.mt, (uint4*)pack);
     CKKS_HIP_CHECK(hipGetLastError());
     // nd signed bytes hold words up to 127 sum_d 2^(8d)
     auto fits = [q](int nd) { return q <= 0x7f7f7f7f7f7f7f7full >> (8 * (8 - nd)); };
-    auto fn = fits(4)   ? pick_tiles<4>(t.wm, a.kin)
-              : fits(5) ? pick_tiles<5>(t.wm, a.kin)
-              : fits(6) ? pick_tiles<6>(t.wm, a.kin)
-              : fits(7) ? pick_tiles<7>(t.wm, a.kin)
-                        : pick_tiles<8>(t.wm, a.kin);
+    auto fn = fits(4)   ? pick_tiles<4>(t, a.kin)
+              : fits(5) ? pick_tiles<5>(t, a.kin)
+              : fits(6) ? pick_tiles<6>(t, a.kin)
+              : fits(7) ? pick_tiles<7>(t, a.kin)
+                        : pick_tiles<8>(t, a.kin);
     TraceScope ts(c, s, "matmul_i8", (double)a.nb * a.nj * a.n_in * 2 * a.nl * c->N);
     hipLaunchKernelGGL(fn, dim3((uint32_t)blocks), dim3(256), 0, s, a, (const uint4*)pack, t.chunks, t.row_blocks,
                        (int)cols);

@@ -131,6 +131,12 @@ MATMULS = [
     ("wide", 1, 1, 128, 32, "in", 0, False, False), ("wide61", 2, 1, 40, 33, "out", 0, True, False),
     ("one", 0, 2, 37, 8, "none", 0, True, False), ("deep", 23, 1, 6, 4, "out", 1, True, False),
     ("q54", 2, 5, 3, 2, "out", 2, True, False),
+    # tiles of 64, 128 and 256 outputs, whole and ragged; inputs of one group and a step, and one more
+    ("q54", 1, 1, 16, 64, "out", 0, True, False), ("small", 2, 1, 17, 128, "out", 1, True, True),
+    ("q54", 1, 1, 128, 129, "out", 0, True, False), ("q54", 1, 2, 129, 256, "in", 0, False, True),
+    ("tiny", 1, 1, 300, 257, "in", 0, True, False), ("small", 1, 1, 256, 300, "out", 0, True, False),
+    ("q48", 0, 1, 385, 140, "none", 0, True, False), ("wide", 1, 1, 33, 200, "in", 0, True, False),
+    ("q56", 1, 1, 31, 150, "out", 0, False, False), ("q47", 2, 1, 20, 190, "out", 1, True, True),
 ]
 
 
