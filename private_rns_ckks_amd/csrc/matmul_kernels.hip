@@ -228,18 +228,16 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
   v4i frag[2][NC][MT];
   const v4i* wp = (const v4i*)pack + (uint64_t)(rb * WM + wm) * MT * chunks * 64 + lane;
   // a step's matrix and words; past the last step those of the last again
-  auto load_matrix = [&](int t, v4i (&f)[NC][MT]) {
+  auto load_matrix = [&](int t, int c, v4i (&f)[NC][MT]) {
     t = min(t, steps - 1);
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) f[c][m] = wp[(m * chunks + t * NC + c) * 64];
+    for (int m = 0; m < MT; ++m) f[c][m] = wp[(m * chunks + t * NC + c) * 64];
   };
-  auto load = [&](int t, uint64_t (&v)[16]) {
+  auto load = [&](int t, int k0, int k1, uint64_t (&v)[16]) {
     t = min(t, steps - 1);
     const uint64_t* p = x + (uint64_t)group_start(t * (KS / 16) + grp, a.n_in) * ct + col;
 #pragma unroll
-    for (int k = 0; k < 16; ++k, p += ct) v[k] = *p;
+    for (int k = k0; k < k1; ++k) v[k] = p[k * ct];
   };
   // the constants of step t's inputs, by way of one thread each
   auto kin_load = [&](int t) {
@@ -273,9 +271,10 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[m][d][r] = 0;
-  load_matrix(0, frag[0]);
-  load(0, raw[0]);
-  if (AHEAD == 2) load(1, raw[1]);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) load_matrix(0, c, frag[0]);
+  load(0, 0, 16, raw[0]);
+  if (AHEAD == 2) load(1, 0, 16, raw[1]);
   if (SCALED) {
     const ulonglong2 k0 = kin_load(0), k1 = kin_load(1);
     if (tid < KS) {
@@ -291,33 +290,46 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
   // step t reads buffer t & 1 (here a constant), and lays step t + 1's digits,
   // whose words are in `next`, in the other
   auto step = [&](int t, int buf, uint64_t (&next)[16], uint64_t (&after)[16]) {
-    load_matrix(t + 1, frag[buf ^ 1]);  // before the words: loads return in order
-    load(t + AHEAD, AHEAD == 2 ? after : next);
-    const ulonglong2 kn = kin_load(t + 2);
     // a chunk's digits are read while the one before is multiplied
     v4i f[2][ND];
     auto digits = [&](int c) {
 #pragma unroll
       for (int d = 0; d < ND; ++d) f[c & 1][d] = *(const v4i*)&dig[buf][d][c * 2 + (lane >> 5)][wn * 32 + (lane & 31)];
     };
+    const ulonglong2 kn = kin_load(t + 2);
+    if (AHEAD == 1) {
+      // one wave's loads and conversions run beside the other's matrix
+      // instructions.  The matrix first: loads return in order
+#pragma unroll
+      for (int c = 0; c < NC; ++c) load_matrix(t + 1, c, frag[buf ^ 1]);
+      load(t + 1, 0, 16, next);
+    }
     digits(0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       if (c + 1 < NC) digits(c + 1);
+      if (AHEAD == 2) {
+        // one wave a SIMD: loads (of the words two steps on), the conversion of
+        // the next step's words and the reads above go between the matrix
+        // instructions
+        load_matrix(t + 1, c, frag[buf ^ 1]);
+        load(t + 2, c * 16 / NC, (c + 1) * 16 / NC, after);
+#pragma unroll
+        for (int g = c * 4 / NC; g < (c + 1) * 4 / NC; ++g) quarter(buf ^ 1, next, g);
+      }
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
           acc[m][d] = __builtin_amdgcn_mfma_i32_32x32x32_i8(frag[buf][c][m], f[c & 1][d], acc[m][d], 0, 0, 0);
-      if (AHEAD == 2) {  // the words are here: split them between the matrix instructions
-#pragma unroll
-        for (int g = c * 4 / NC; g < (c + 1) * 4 / NC; ++g) quarter(buf ^ 1, next, g);
+      if (AHEAD == 2) {
 #pragma unroll
         for (int d = 0; d < ND * MT; ++d) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction,
-          if (c + 1 < NC && d < ND) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read of the next chunk's,
-          __builtin_amdgcn_sched_group_barrier(0x002, (SCALED ? 34 : 9) * 4 / NC / MT, 0);  // and conversions
+          if (c + 1 < NC && d < ND) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read,
+          if (d < MT + 16 / NC) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);      // a load,
+          __builtin_amdgcn_sched_group_barrier(0x002, (SCALED ? 34 : 10) * 4 / NC / MT, 0);  // conversions
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -367,15 +379,25 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
       for (int d = 4; d < ND; ++d) hi += (int64_t)acc[m][d][r] * place[d - 4];
       rems[r][tid] = mod.rem(lo, hi);
     }
-#pragma unroll 4
-    for (int r = 0; r < 16; ++r) {
-      const int up = m * 32 + (r >> 2) * 8 + (r & 3), j = rb * ROWS + row0 + up;
-      const ulonglong2 k = kc[row0 + up];
-      uint64_t v = below(below(mul_shoup_lazy_split(rems[r][tid], k.x, k.y, pc.q), 2 * pc.q), pc.q);
-      if (a.tok) v = mul_mod(v, tok, pc.q, pc.r64, pc.r64p, pc.inv1);
-      if (j < a.nj) {
-        if (bias) v = add_mod(v, bias[2 * (a.j0 + j)], pc.q);
-        o[up * per] = v;
+    // four rows next to each other at a time: chains that do not wait for one another
+#pragma unroll 1
+    for (int r = 0; r < 16; r += 4) {
+      const int up = m * 32 + r * 2, j = rb * ROWS + row0 + up;
+      uint64_t v[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const ulonglong2 k = kc[row0 + up + n];
+        v[n] = below(below(mul_shoup_lazy_split(rems[r + n][tid], k.x, k.y, pc.q), 2 * pc.q), pc.q);
+      }
+      if (a.tok) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) v[n] = mul_mod(v[n], tok, pc.q, pc.r64, pc.r64p, pc.inv1);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        if (j + n >= a.nj) break;
+        if (bias) v[n] = add_mod(v[n], bias[2 * (a.j0 + j + n)], pc.q);
+        o[(up + n) * per] = v[n];
       }
     }
   }
