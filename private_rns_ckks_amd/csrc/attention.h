@@ -54,6 +54,10 @@ int launch_plain_mul(Ctx* c, hipStream_t s, const PlainMul& m, uint64_t* out, ui
 // words between items of either.
 int rescale_mul_fused(Ctx* c, hipStream_t s, const PlainMul& m, const uint64_t* v, uint64_t* w, uint64_t per, int batch);
 
+// Items of a launch of rescale_products at most.  Each launch's tail leaves the
+// chip part empty: 768 outputs at 3 limbs of 2^16 take CHUNKFIG.
+constexpr int kMaxProducts = 1024;
+
 // Rescales of n products by their top `drop` (1 or 2) limbs, in one transform:
 // `top` holds the dropped limbs q_(level+1-drop)..q_level ([2][drop][N] an item, used up), `out` the limbs
 // that stay times the inverses of the dropped primes ([2][level+1-drop][N] an

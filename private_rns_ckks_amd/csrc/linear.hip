@@ -59,7 +59,7 @@ int matmul_i8(Ctx* c, const uint64_t* x, int n_blk, int n_in, const int8_t* w, i
   const uint64_t pack_words = matmul_pack_words(n_in, n_out), kw = const_words(n_k, nl), iw = const_words(n_ki, nl);
   const uint64_t bw = const_words((int)kb.size(), nl);
   const uint64_t tops = drop ? held_words(top, std::min(items, kGroup), hold.block) : 0;
-  const uint64_t step = drop ? held_words(w_per, std::min<uint64_t>(items, kMaxChunk), hold.step) : 0;
+  const uint64_t step = drop ? held_words(w_per, std::min<uint64_t>(items, kMaxProducts), hold.step) : 0;
   auto even = [](uint64_t v) { return (v + 1) & ~1ull; };  // 16-byte parts
   if ((rc = ensure_aux(c, tops + even(pack_words) + kw + iw + bw)) || (drop && (rc = ensure_workspace(c, step)))) return rc;
   uint64_t *T = c->aux, *pack = T + tops, *tk = pack + even(pack_words), *ti = tk + kw, *tb = ti + iw;

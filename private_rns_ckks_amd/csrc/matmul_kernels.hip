@@ -259,6 +259,7 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
 #pragma unroll
     for (int d = 0; d < ND; ++d) part[d][g] = o[d];
   };
+  auto quarters = [](int c) { return c == 0 ? 0 : NC < 4 ? 4 : c == 1 ? 2 : min(c + 1, 4); };  // done before chunk c
   auto put = [&](int t) {
 #pragma unroll
     for (int d = 0; d < ND; ++d) dig[t & 1][d][grp][col] = make_uint4(part[d][0], part[d][1], part[d][2], part[d][3]);
@@ -315,8 +316,10 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
         // instructions
         load_matrix(t + 1, c, frag[buf ^ 1]);
         load(t + 2, c * 16 / NC, (c + 1) * 16 / NC, after);
+        // (in fewer chunks than there are, to lay the digits out in the last)
 #pragma unroll
-        for (int g = c * 4 / NC; g < (c + 1) * 4 / NC; ++g) quarter(buf ^ 1, next, g);
+        for (int g = quarters(c); g < quarters(c + 1); ++g) quarter(buf ^ 1, next, g);
+        if (c + 1 == NC) put(buf ^ 1);
       }
 #pragma unroll
       for (int d = 0; d < ND; ++d)
@@ -329,7 +332,8 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction,
           if (c + 1 < NC && d < ND) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read,
           if (d < MT + 16 / NC) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);      // a load,
-          __builtin_amdgcn_sched_group_barrier(0x002, (SCALED ? 34 : 10) * 4 / NC / MT, 0);  // conversions
+          if (c + 1 == NC && d < ND) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // a write,
+          __builtin_amdgcn_sched_group_barrier(0x002, SCALED ? 24 : 7, 0);               // conversions
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -337,8 +341,8 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
     if (AHEAD == 1) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) quarter(buf ^ 1, next, g);
+      put(buf ^ 1);
     }
-    put(buf ^ 1);
     // step t + 2's constants take the place of step t's, which every thread
     // read before the last barrier
     if (SCALED && tid < KS) kin[buf][tid] = kn;
@@ -365,40 +369,57 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
   const uint64_t per = (uint64_t)(i < low ? 2 * low : 2 * a.drop) << a.log_n;
   const int row0 = wm * MT * 32 + (lane >> 5) * 4;
   uint64_t* o = (i < low ? a.out : a.top) + at + word + ((uint64_t)b * a.nj + rb * ROWS + row0) * per;
-  uint64_t(*rems)[256] = (uint64_t(*)[256])dig;
+  // The rows of a group of four registers lie next to each other; a group's
+  // chains do not wait for one another.
+  auto sums = [&](int m, int r, uint64_t (&v)[4]) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    // through LDS (a thread's own words): the registers' indexes are constants
-    // here, and the code of the rest stays small
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
+    for (int n = 0; n < 4; ++n) {
       int64_t lo = mod.lo0, hi = mod.hi0;
 #pragma unroll
-      for (int d = 0; d < 4; ++d) lo += (int64_t)acc[m][d][r] * place[d];
+      for (int d = 0; d < 4; ++d) lo += (int64_t)acc[m][d][r + n] * place[d];
 #pragma unroll
-      for (int d = 4; d < ND; ++d) hi += (int64_t)acc[m][d][r] * place[d - 4];
-      rems[r][tid] = mod.rem(lo, hi);
+      for (int d = 4; d < ND; ++d) hi += (int64_t)acc[m][d][r + n] * place[d - 4];
+      const ulonglong2 k = kc[row0 + m * 32 + r * 2 + n];
+      v[n] = below(below(mul_shoup_lazy_split(mod.rem(lo, hi), k.x, k.y, pc.q), 2 * pc.q), pc.q);
     }
-    // four rows next to each other at a time: chains that do not wait for one another
+  };
+  auto store = [&](int up, uint64_t (&v)[4]) {
+    const int j = rb * ROWS + row0 + up;
+    uint64_t* p = o + up * per;
+    if (bias) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) v[n] = below(v[n] + bias[2 * (a.j0 + min(j + n, a.nj - 1))], pc.q);
+    }
+    if (j + 3 < a.nj) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n, p += per) *p = v[n];
+    } else {
+#pragma unroll
+      for (int n = 0; n < 3; ++n, p += per)
+        if (j + n < a.nj) *p = v[n];
+    }
+  };
+  uint64_t(*done)[256] = (uint64_t(*)[256])dig;  // a thread's own words
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      uint64_t v[4];
+      sums(m, r, v);
+      if (a.tok) {  // wait in LDS for the loop below, which is not unrolled
+#pragma unroll
+        for (int n = 0; n < 4; ++n) done[r + n][tid] = v[n];
+      } else {
+        store(m * 32 + r * 2, v);
+      }
+    }
+    if (!a.tok) continue;
 #pragma unroll 1
     for (int r = 0; r < 16; r += 4) {
-      const int up = m * 32 + r * 2, j = rb * ROWS + row0 + up;
       uint64_t v[4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const ulonglong2 k = kc[row0 + up + n];
-        v[n] = below(below(mul_shoup_lazy_split(rems[r + n][tid], k.x, k.y, pc.q), 2 * pc.q), pc.q);
-      }
-      if (a.tok) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) v[n] = mul_mod(v[n], tok, pc.q, pc.r64, pc.r64p, pc.inv1);
-      }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        if (j + n >= a.nj) break;
-        if (bias) v[n] = add_mod(v[n], bias[2 * (a.j0 + j + n)], pc.q);
-        o[(up + n) * per] = v[n];
-      }
+      for (int n = 0; n < 4; ++n) v[n] = mul_mod(done[r + n][tid], tok, pc.q, pc.r64, pc.r64p, pc.inv1);
+      store(m * 32 + r * 2, v);
     }
   }
 }
@@ -412,11 +433,20 @@ namespace {
 constexpr int kTileRows = 9;
 bool tiled(int n_in, int nj) { return nj >= kTileRows && n_in >= 16; }
 
+// The tile of a launch: 32, 64, 128 or 256 outputs.  A word costs its conversion
+// for every tile of outputs (some 16 instructions an input) and its sums'
+// joining for every output, those past the last included (some 74).
 struct Tiles {
-  int wm, wn, mt, row_blocks, chunks;
+  int wm = 1, wn, mt = 1, row_blocks, chunks;
   Tiles(int n_in, int nj) {
-    wm = nj > 64 ? 4 : nj > 32 ? 2 : 1;
-    mt = nj > 128 ? 2 : 1;
+    uint64_t least = ~0ull;
+    for (int r = 32; r <= 256; r *= 2) {
+      const uint64_t blocks = (nj + r - 1) / r, cost = blocks * r * 74 + blocks * n_in * 16;
+      if (cost >= least) continue;
+      least = cost;
+      wm = std::min(r / 32, 4);
+      mt = r == 256 ? 2 : 1;
+    }
     wn = 4 / wm;
     row_blocks = (nj + rows() - 1) / rows();
     const int nc = 4 / wn;
@@ -441,7 +471,9 @@ auto pick_tiles(const Tiles& t, bool scaled) {
 }  // namespace
 
 uint64_t matmul_pack_words(int n_in, int nj) {
-  return std::max(2 * Tiles(n_in, nj).lanes(), (uint64_t)((nj + kRows - 1) / kRows) * n_in);
+  // any of the tiles, for this many outputs or fewer: two words a lane
+  const uint64_t rows = (uint64_t)(nj + 255) / 256 * 256, inputs = (uint64_t)(n_in + 127) / 128 * 128;
+  return std::max(rows * inputs / 8, (uint64_t)((nj + kRows - 1) / kRows) * n_in);
 }
 
 int launch_matmul(Ctx* c, hipStream_t s, const MatArgs& a, uint64_t* pack) {

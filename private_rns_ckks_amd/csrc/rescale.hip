@@ -312,7 +312,7 @@ int rescale_products(Ctx* c, hipStream_t s, const ProductRescale& p, uint64_t* w
   const int log_n = (int)c->log_n, lc = logb_col(log_n), lr = logb_row(log_n), level = p.level, drop = p.drop;
   const int low = level + 1 - drop;
   const uint64_t a_per = 2ull * drop * N, w_per = 2ull * (level + 1) * N;
-  const int chunk = (int)std::max<uint64_t>(1, std::min<uint64_t>(kMaxChunk, ws_words / w_per));
+  const int chunk = (int)std::max<uint64_t>(1, std::min<uint64_t>(kMaxProducts, ws_words / w_per));
   auto fc = drop == 1 ? CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 1, true)
                       : CKKS_PICK_PASS(drop_col_kernel, log_n, lc, 2, true);
   auto fr = CKKS_PICK_PASS(product_row_kernel, log_n, lr);
