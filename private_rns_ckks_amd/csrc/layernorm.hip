@@ -10,6 +10,7 @@ namespace ckks {
 namespace {
 
 constexpr int kMaxFeat = 1 << 16;
+constexpr Whole kOne{1, 0};
 
 uint64_t even(uint64_t v) { return (v + 1) & ~1ull; }  // 16-byte parts
 
@@ -53,15 +54,15 @@ int layernorm_var(Ctx* c, const uint64_t* x, int n_blk, int n_feat, int level, d
   if (n_blk == 0) return CKKS_OK;
   CaptureScope cap(c, s);
   Tail t{c, s, rlk, {}, {}, nullptr, 0};
-  const uint64_t per = 3 * lim, tw = const_words(3, l + 1);
+  const uint64_t per = 3 * lim, tw = const_words(3, l + 1), ow = const_words(1, l + 1);
   const int block = t.hold.items(per, n_blk);
-  if ((rc = ensure_aux(c, tw + t.hold.reserve(per, n_blk))) || (rc = t.reserve(t.relin_words(n_blk, l, 2)))) return rc;
-  uint64_t* X = c->aux + tw;
-  if ((rc = launch_consts(c, s, k, 3, l + 1, 0, c->aux))) return rc;
+  if ((rc = ensure_aux(c, tw + ow + t.hold.reserve(per, n_blk))) || (rc = t.reserve(t.relin_words(n_blk, l, 2)))) return rc;
+  uint64_t *to = c->aux + tw, *X = to + ow;
+  if ((rc = launch_consts(c, s, k, 3, l + 1, 0, c->aux)) || (rc = launch_consts(c, s, &kOne, 1, l + 1, 2, to))) return rc;
   for (int b0 = 0; b0 < n_blk; b0 += block) {
     const int n = std::min(block, n_blk - b0);
-    const MomentArgs a{x + (uint64_t)b0 * n_feat * ct, sum + b0 * ct, X, c->aux, c->d_rescale, c->d_prime,
-                       (int)c->log_n, l + 1, (int)c->L, n_feat};
+    const MomentArgs a{x + (uint64_t)b0 * n_feat * ct, sum + b0 * ct, X, c->aux, to, c->d_prime,
+                       (int)c->log_n, l + 1, n_feat};
     if ((rc = launch_moments(c, s, a, n)) || (rc = t.relin_rescale(X, var + b0 * vct, n, l, 2))) return rc;
   }
   return CKKS_OK;
@@ -93,19 +94,19 @@ int layernorm(Ctx* c, const uint64_t* x, const uint64_t* sum, int n_blk, int n_f
   const int nl = t_ + 1, n_k = (int)k.size();
   const uint64_t per = 3 * lim, kw = const_words(n_k, nl), bw = const_words((int)kb.size(), nl), fw = const_words(1, nl);
   const int block = t.hold.items(per, items);
-  if ((rc = ensure_aux(c, kw + bw + fw + t.hold.reserve(per, items))) ||
+  if ((rc = ensure_aux(c, kw + bw + 2 * fw + t.hold.reserve(per, items))) ||
       (rc = t.reserve(t.relin_words((int)items, t_, 2))))
     return rc;
-  uint64_t *tk = c->aux, *tb = tk + kw, *tf = tb + bw, *X = tf + fw;
+  uint64_t *tk = c->aux, *tb = tk + kw, *tf = tb + bw, *to = tf + fw, *X = to + fw;
   const Whole feat{n_feat, 0};
   if ((rc = launch_consts(c, s, k.data(), n_k, nl, 0, tk)) || (rc = launch_consts(c, s, &feat, 1, nl, 0, tf)) ||
-      (beta && (rc = launch_consts(c, s, kb.data(), n_feat, nl, 0, tb))))
+      (rc = launch_consts(c, s, &kOne, 1, nl, 2, to)) || (beta && (rc = launch_consts(c, s, kb.data(), n_feat, nl, 0, tb))))
     return rc;
   for (uint64_t b0 = 0; b0 < items; b0 += block) {
     const int n = (int)std::min<uint64_t>(block, items - b0);
-    const NormArgs a{x, sum, rstd, X, tk, beta ? tb : nullptr, tf, c->d_rescale, c->d_prime, (int)c->log_n, nl,
-                     level + 1, (int)c->L, n_feat, n_k, (int)b0};
-    if ((rc = launch_norm(c, s, a, n)) || (rc = t.relin_rescale(X, y + b0 * yct, n, t_, 2))) return rc;
+    const NormArgs a{x, sum, rstd, X, tk, beta ? tb : nullptr, tf, to, c->d_prime, (int)c->log_n, nl,
+                     level + 1, n_feat, n_k, (int)b0, (int)b0 + n};
+    if ((rc = launch_norm(c, s, a)) || (rc = t.relin_rescale(X, y + b0 * yct, n, t_, 2))) return rc;
   }
   return CKKS_OK;
 }
@@ -155,45 +156,48 @@ int layernorm_grad(Ctx* c, const uint64_t* dy, int n_blk, int n_feat, int level,
   const int bf = dgamma || dbeta ? t.hold.items(per_feat, n_feat) : 0;
   uint64_t need = 0, work = 0;
   if (dx) {
-    need = kw + 3 * fw + t.hold.reserve(per_blk, n_blk) + t.hold.reserve(per_item, items);
+    need = kw + 5 * fw + t.hold.reserve(per_blk, n_blk) + t.hold.reserve(per_item, items);
     work = std::max({t.relin_words(n_blk, l, 2), t.relin_words(n_blk, l - 2, 1), t.relin_words((int)items, l - 3, 2)});
   }
-  if (dgamma || dbeta) need = std::max(need, t.hold.reserve(per_feat, n_feat));
+  if (dgamma || dbeta) need = std::max(need, fw + t.hold.reserve(per_feat, n_feat));
   if (dgamma) work = std::max({work, (uint64_t)t.relin_words(n_feat, l, 1), t.sum_words(n_feat, l - 1)});
   if (dbeta) work = std::max(work, t.sum_words(n_feat, l));
   if ((rc = ensure_aux(c, need)) || (rc = t.reserve(work))) return rc;
   if (dx) {
-    uint64_t *tk = c->aux, *tf = tk + kw, *tc = tf + fw, *td = tc + fw, *B = td + fw;
+    uint64_t *tk = c->aux, *tf = tk + kw, *tc = tf + fw, *t2 = tc + fw, *t1 = t2 + fw, *te = t1 + fw,
+             *B = te + fw;
     uint64_t *X = B, *G = X + 3 * lim * bb, *H = G + rct * bb, *R = H + hct * bb, *Y = R + rct * bb;
     const Whole feat{n_feat, 0};
     if ((rc = launch_consts(c, s, k.data(), n_k, nl, 0, tk)) || (rc = launch_consts(c, s, &feat, 1, nl, 0, tf)) ||
-        (rc = launch_consts(c, s, &cr, 1, l - 1, 1, tc)) || (rc = launch_consts(c, s, &cr, 1, l - 1, 0, td)))
+        (rc = launch_consts(c, s, &cr, 1, l - 1, 0, tc)) || (rc = launch_consts(c, s, &kOne, 1, nl, 2, t2)) ||
+        (rc = launch_consts(c, s, &kOne, 1, l - 1, 1, t1)) || (rc = launch_consts(c, s, &kOne, 1, low, 2, te)))
       return rc;
     for (int b0 = 0; b0 < n_blk; b0 += bb) {
       const int nb = std::min(bb, n_blk - b0);
       const uint64_t *dyb = dy + (uint64_t)b0 * n_feat * ct, *rb = rstd + (uint64_t)b0 * 2 * (rstd_level + 1) * N;
       const uint64_t* xb = xhat + (uint64_t)b0 * n_feat * 2 * (xhat_level + 1) * N;
-      const GradSumArgs a{dyb, xb, G, X, tk, c->d_rescale, c->d_prime, (int)c->log_n, nl, xhat_level + 1, low,
-                          (int)c->L, n_feat, n_k};
+      const GradSumArgs a{dyb, xb, G, X, tk, t2, c->d_prime, (int)c->log_n, nl, xhat_level + 1, low,
+                          n_feat, n_k};
       if ((rc = launch_grad_sums(c, s, a, nb)) || (rc = t.relin_rescale(X, H, nb, l, 2))) return rc;
-      const ScaledPairArgs p{rb, H, X, tc, td, c->d_prime, (int)c->log_n, l - 1, rstd_level + 1};
+      const ScaledPairArgs p{rb, H, X, t1, tc, c->d_prime, (int)c->log_n, l - 1, rstd_level + 1};
       if ((rc = launch_scaled_pair(c, s, p, nb)) || (rc = t.relin_rescale(X, R, nb, l - 2, 1))) return rc;
       for (int i0 = 0; i0 < nb * n_feat; i0 += bi) {
         const int n = std::min(bi, nb * n_feat - i0);
-        const GradArgs g{dyb, xb, rb, G, R, Y, tk, tf, c->d_rescale, c->d_prime, (int)c->log_n, low, nl,
-                         xhat_level + 1, rstd_level + 1, (int)c->L, n_feat, n_k, i0};
-        if ((rc = launch_grad(c, s, g, n)) ||
+        const GradArgs g{dyb, xb, rb, G, R, Y, tk, tf, te, c->d_prime, (int)c->log_n, low, nl,
+                         xhat_level + 1, rstd_level + 1, n_feat, n_k, i0, i0 + n};
+        if ((rc = launch_grad(c, s, g)) ||
             (rc = t.relin_rescale(Y, dx + ((uint64_t)b0 * n_feat + i0) * dct, n, l - 3, 2)))
           return rc;
       }
     }
   }
+  if (dgamma && (rc = launch_consts(c, s, &kOne, 1, nl, 1, c->aux))) return rc;
   for (int f0 = 0; (dgamma || dbeta) && f0 < n_feat; f0 += bf) {
     const int n = std::min(bf, n_feat - f0);
-    uint64_t *X = c->aux, *Z = X + 3 * lim * bf;
+    uint64_t *X = c->aux + fw, *Z = X + 3 * lim * bf;
     uint64_t *tb = dbeta ? t.before_sum(Z, dbeta + f0 * ct) : nullptr;
-    const WeightArgs a{dy, xhat, dgamma ? X : nullptr, tb, c->d_rescale, c->d_prime, (int)c->log_n, nl,
-                       xhat_level + 1, (int)c->L, n_blk, n_feat, f0};
+    const WeightArgs a{dy, xhat, dgamma ? X : nullptr, tb, c->aux, c->d_prime, (int)c->log_n, nl,
+                       xhat_level + 1, n_blk, n_feat, f0};
     if ((rc = launch_weight_sums(c, s, a, n)) || (dbeta && (rc = t.sum(tb, dbeta + f0 * ct, n, l)))) return rc;
     if (!dgamma) continue;
     uint64_t* tg = t.before_sum(Z, dgamma + f0 * gct);
