@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void matmul_rows_kernel(MatArgs a, const uint6
     }
   }
   ep.has_tok = a.tok != nullptr;
-  ep.tok = a.tok ? a.tok[((uint64_t)((a.b0 + b) % a.n_tok) * a.nl + i << a.log_n) + c] : 0;
+  ep.tok = a.tok ? a.tok[(((uint64_t)((a.b0 + b) % a.n_tok) * a.nl + i) << a.log_n) + c] : 0;
   ep.kout = a.kout ? a.kout + (uint64_t)i * a.n_kout * 2 : nullptr;
   ep.kstep = a.n_kout > 1 ? 2 : 0;
   ep.bias = a.bias && comp == 0 ? a.bias + (uint64_t)i * a.n_out * 2 : nullptr;
@@ -192,6 +192,20 @@ struct SumMod {
   }
 };
 
+// A scalar base and a lane's byte offset below 2^32, as one address of a load or
+// store: the base goes through an empty asm statement, or the compiler moves the
+// sum into vector registers, an addition a load.
+typedef __attribute__((address_space(1))) char* GlobalBytes;
+__device__ __forceinline__ GlobalBytes scalar_base(const void* p) {
+  uint64_t u = (uint64_t)p;
+  asm("" : "+s"(u));
+  return (GlobalBytes)u;
+}
+template <typename T>
+__device__ __forceinline__ T load_at(const void* base, uint32_t bytes) {
+  return *(const __attribute__((address_space(1))) T*)(scalar_base(base) + bytes);
+}
+
 template <int ND, int WM, int WN, int MT, bool SCALED>
 __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatArgs a, const uint4* pack, int chunks, int row_blocks,
                                                               int col_blocks) {
@@ -207,7 +221,8 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
   const int slot = blockIdx.x >> 3, per_xcd = (col_blocks + 7) / 8;
   const int rb = slot % row_blocks, cb = (blockIdx.x & 7) * per_xcd + slot / row_blocks;
   if (slot / row_blocks >= per_xcd || cb >= col_blocks) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, wm = wave / WN, wn = wave % WN;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
   const int per_limb = 1 << (a.log_n - (WN == 1 ? 5 : WN == 2 ? 6 : 7));
   const int poly = cb / per_limb, col0 = (cb % per_limb) * W;  // poly = (b, comp, limb)
   const int i = poly % a.nl, comp = poly / a.nl % 2, b = poly / (2 * a.nl);
@@ -226,18 +241,29 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
 
   uint64_t raw[2][16];
   v4i frag[2][NC][MT];
-  const v4i* wp = (const v4i*)pack + (uint64_t)(rb * WM + wm) * MT * chunks * 64 + lane;
+  const v4i* wp = (const v4i*)pack + (uint64_t)(rb * WM + wm) * MT * chunks * 64;
+  const uint32_t lane16 = lane * 16;
   // a step's matrix and words; past the last step those of the last again
   auto load_matrix = [&](int t, int c, v4i (&f)[NC][MT]) {
     t = min(t, steps - 1);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) f[c][m] = wp[(m * chunks + t * NC + c) * 64];
+    for (int m = 0; m < MT; ++m) f[c][m] = load_at<v4i>(wp + (m * chunks + t * NC + c) * 64, lane16);
   };
-  auto load = [&](int t, int k0, int k1, uint64_t (&v)[16]) {
+  // Addresses are a scalar and a lane's 32 bits: a wave of a 32-word tile holds
+  // two groups, the second at most 16 inputs (below 2^27 words) behind the first.
+  const int group0 = __builtin_amdgcn_readfirstlane(tid / W);
+  struct Words {
+    const uint64_t* p;  // the next input's row
+    uint32_t off;
+  };
+  auto words = [&](int t) {
     t = min(t, steps - 1);
-    const uint64_t* p = x + (uint64_t)group_start(t * (KS / 16) + grp, a.n_in) * ct + col;
+    const int at = group_start(t * (KS / 16) + group0, a.n_in), next = group_start(t * (KS / 16) + group0 + 1, a.n_in);
+    return Words{x + (uint64_t)at * ct, ((uint32_t)col + (W == 32 && lane >= 32 ? (uint32_t)(next - at) * (uint32_t)ct : 0)) * 8};
+  };
+  auto load = [&](Words& w, int k0, int k1, uint64_t (&v)[16]) {
 #pragma unroll
-    for (int k = k0; k < k1; ++k) v[k] = p[k * ct];
+    for (int k = k0; k < k1; ++k, w.p += ct) v[k] = load_at<uint64_t>(w.p, w.off);
   };
   // the constants of step t's inputs, by way of one thread each
   auto kin_load = [&](int t) {
@@ -274,8 +300,9 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
       for (int r = 0; r < 16; ++r) acc[m][d][r] = 0;
 #pragma unroll
   for (int c = 0; c < NC; ++c) load_matrix(0, c, frag[0]);
-  load(0, 0, 16, raw[0]);
-  if (AHEAD == 2) load(1, 0, 16, raw[1]);
+  Words w0 = words(0), w1 = words(1);
+  load(w0, 0, 16, raw[0]);
+  if (AHEAD == 2) load(w1, 0, 16, raw[1]);
   if (SCALED) {
     const ulonglong2 k0 = kin_load(0), k1 = kin_load(1);
     if (tid < KS) {
@@ -298,12 +325,13 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
       for (int d = 0; d < ND; ++d) f[c & 1][d] = *(const v4i*)&dig[buf][d][c * 2 + (lane >> 5)][wn * 32 + (lane & 31)];
     };
     const ulonglong2 kn = kin_load(t + 2);
+    Words w = words(t + AHEAD);
     if (AHEAD == 1) {
       // one wave's loads and conversions run beside the other's matrix
       // instructions.  The matrix first: loads return in order
 #pragma unroll
       for (int c = 0; c < NC; ++c) load_matrix(t + 1, c, frag[buf ^ 1]);
-      load(t + 1, 0, 16, next);
+      load(w, 0, 16, next);
     }
     digits(0);
     __builtin_amdgcn_sched_barrier(0);
@@ -315,7 +343,7 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
         // the next step's words and the reads above go between the matrix
         // instructions
         load_matrix(t + 1, c, frag[buf ^ 1]);
-        load(t + 2, c * 16 / NC, (c + 1) * 16 / NC, after);
+        load(w, c * 16 / NC, (c + 1) * 16 / NC, after);
         // (in fewer chunks than there are, to lay the digits out in the last)
 #pragma unroll
         for (int g = quarters(c); g < quarters(c + 1); ++g) quarter(buf ^ 1, next, g);
@@ -362,13 +390,14 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
   for (int d = 0; d < 4; ++d) asm("" : "+s"(place[d]));
   const SumMod mod(pc.q, (uint32_t)((ConstPrime)a.prime)[i].top);
   const int word = col0 + wn * 32 + (lane & 31);
-  const uint64_t tok = a.tok ? a.tok[((uint64_t)((a.b0 + b) % a.n_tok) * a.nl + i << a.log_n) + word] : 0;
+  const uint64_t tok = a.tok ? a.tok[(((uint64_t)((a.b0 + b) % a.n_tok) * a.nl + i) << a.log_n) + word] : 0;
   const uint64_t* bias = a.bias && comp == 0 ? a.bias + (uint64_t)i * a.n_out * 2 : nullptr;
   const int low = a.nl - a.drop;
   const uint64_t at = i < low ? ((uint64_t)(comp * low + i) << a.log_n) : ((uint64_t)(comp * a.drop + i - low) << a.log_n);
   const uint64_t per = (uint64_t)(i < low ? 2 * low : 2 * a.drop) << a.log_n;
   const int row0 = wm * MT * 32 + (lane >> 5) * 4;
-  uint64_t* o = (i < low ? a.out : a.top) + at + word + ((uint64_t)b * a.nj + rb * ROWS + row0) * per;
+  uint64_t* o = (i < low ? a.out : a.top) + at + ((uint64_t)b * a.nj + rb * ROWS + wm * MT * 32) * per;
+  const uint32_t o_off = ((uint32_t)word + (lane >> 5) * 4 * (uint32_t)per) * 8;  // below 2^29
   // The rows of a group of four registers lie next to each other; a group's
   // chains do not wait for one another.
   auto sums = [&](int m, int r, uint64_t (&v)[4]) {
@@ -385,18 +414,17 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
   };
   auto store = [&](int up, uint64_t (&v)[4]) {
     const int j = rb * ROWS + row0 + up;
-    uint64_t* p = o + up * per;
     if (bias) {
 #pragma unroll
       for (int n = 0; n < 4; ++n) v[n] = below(v[n] + bias[2 * (a.j0 + min(j + n, a.nj - 1))], pc.q);
     }
     if (j + 3 < a.nj) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n, p += per) *p = v[n];
+      for (int n = 0; n < 4; ++n) *(__attribute__((address_space(1))) uint64_t*)(scalar_base(o + (up + n) * per) + o_off) = v[n];
     } else {
 #pragma unroll
-      for (int n = 0; n < 3; ++n, p += per)
-        if (j + n < a.nj) *p = v[n];
+      for (int n = 0; n < 3; ++n)
+        if (j + n < a.nj) *(__attribute__((address_space(1))) uint64_t*)(scalar_base(o + (up + n) * per) + o_off) = v[n];
     }
   };
   uint64_t(*done)[256] = (uint64_t(*)[256])dig;  // a thread's own words
