@@ -10,7 +10,7 @@ namespace ckks {
 
 namespace {
 
-constexpr int kRows = 8;  // outputs of a thread
+constexpr int kRows = 8;  // outputs of a thread at most
 
 // pack[tile][i][r] = w[j0 + kRows tile + r][i], zero past the last output.
 __global__ __launch_bounds__(256) void pack_rows_kernel(MatArgs a, uint64_t* pack) {
@@ -49,8 +49,10 @@ struct Epilogue {
   }
 };
 
-// One word of kRows outputs a thread: the word's 31-bit halves times a byte,
-// summed in 64 bits (2^31 2^7 2^16 = 2^54).
+// One word of R outputs a thread: the word's 31-bit halves times a byte, summed
+// in 64 bits (2^31 2^7 2^16 = 2^54).  For few outputs, where the words are all the
+// traffic: ROWSFIG.
+template <int R>
 __global__ __launch_bounds__(256) void matmul_rows_kernel(MatArgs a, const uint64_t* pack) {
   const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
   const int comp = blockIdx.y / a.nl, i = blockIdx.y % a.nl;
@@ -63,19 +65,28 @@ __global__ __launch_bounds__(256) void matmul_rows_kernel(MatArgs a, const uint6
   ep.pc = red_const((ConstPrime)a.prime, i);
   const uint64_t q = ep.pc.q;
   const ConstU64 kin = a.kin ? (ConstU64)(a.kin + (uint64_t)i * a.n_in * 2) : nullptr;
-  int64_t lo[kRows] = {}, hi[kRows] = {};
-  for (int k = 0; k < a.n_in; ++k) {
-    uint64_t v = x[k * ct];
+  int64_t lo[R] = {}, hi[R] = {};
+  auto take = [&](uint64_t v, int k) {
     if (kin) v = reduce_2q(mul_shoup(v, kin[2 * k], kin[2 * k + 1], q), q);
     const int32_t l = (int32_t)(v & 0x7fffffff), h = (int32_t)(v >> 31);
     const uint64_t row = w[k];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    for (int r = 0; r < R; ++r) {
       const int32_t m = (int8_t)(row >> (8 * r));
       lo[r] += (int64_t)l * m;
       hi[r] += (int64_t)h * m;
     }
+  };
+  constexpr int kAhead = 16;  // loads in flight
+  int k = 0;
+  for (; k + kAhead <= a.n_in; k += kAhead, x += kAhead * ct) {
+    uint64_t v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) v[u] = x[u * ct];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) take(v[u], k + u);
   }
+  for (; k < a.n_in; ++k, x += ct) take(*x, k);
   ep.has_tok = a.tok != nullptr;
   ep.tok = a.tok ? a.tok[(((uint64_t)((a.b0 + b) % a.n_tok) * a.nl + i) << a.log_n) + c] : 0;
   ep.kout = a.kout ? a.kout + (uint64_t)i * a.n_kout * 2 : nullptr;
@@ -86,7 +97,7 @@ __global__ __launch_bounds__(256) void matmul_rows_kernel(MatArgs a, const uint6
   uint64_t* o = (i < low ? a.out : a.top) + at + c;
   const uint64_t per = (uint64_t)(i < low ? 2 * low : 2 * a.drop) << a.log_n;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
+  for (int r = 0; r < R; ++r) {
     const int j = tile * kRows + r;
     if (j >= a.nj) break;
     o[((uint64_t)b * a.nj + j) * per] = ep.finish(reduce_signed((__int128)lo[r] + ((__int128)hi[r] << 31), ep.pc), a.j0 + j);
@@ -534,7 +545,8 @@ int launch_matmul(Ctx* c, hipStream_t s, const MatArgs& a, uint64_t* pack) {
   hipLaunchKernelGGL(pack_rows_kernel, dim3((uint32_t)((words + 255) / 256)), dim3(256), 0, s, a, pack);
   CKKS_HIP_CHECK(hipGetLastError());
   TraceScope ts(c, s, "matmul_i8", (double)a.nb * a.nj * a.n_in * 2 * a.nl * c->N);
-  hipLaunchKernelGGL(matmul_rows_kernel, dim3(c->N / 256, 2 * a.nl, a.nb * tiles), dim3(256), 0, s, a, pack);
+  auto fn = a.nj <= 2 ? matmul_rows_kernel<2> : a.nj <= 4 ? matmul_rows_kernel<4> : matmul_rows_kernel<kRows>;
+  hipLaunchKernelGGL(fn, dim3(c->N / 256, 2 * a.nl, a.nb * tiles), dim3(256), 0, s, a, pack);
   CKKS_HIP_CHECK(hipGetLastError());
   return CKKS_OK;
 }
