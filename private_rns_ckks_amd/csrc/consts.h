@@ -27,11 +27,18 @@ inline bool whole(double x, Whole* out) {
   return true;
 }
 
-// Tables of n constants for the limbs i < nl, limb by limb:
+// A table of n constants for the limbs i < nl, limb by limb:
 // table[(i * n + j) * 2] = {k_j mod q_i, Shoup quotient}.  With drop > 0, limbs
 // i <= nl - 1 - drop hold k_j (q_(nl-1) .. q_(nl-drop))^-1 instead, which turns
 // a product into the term that the rescales to come keep (DropOut).
+struct ConstTable {
+  const Whole* k;
+  int n, nl, drop;
+  uint64_t* table;  // const_words(n, nl)
+};
 inline uint64_t const_words(int n, int nl) { return (uint64_t)n * nl * 2; }
-int launch_consts(Ctx* c, hipStream_t s, const Whole* k, int n, int nl, int drop, uint64_t* table);
+// All of a call's tables at once: few launches.
+constexpr int kMaxConstTables = 8;
+int launch_consts(Ctx* c, hipStream_t s, const ConstTable* t, int n_tables);
 
 }  // namespace ckks

@@ -58,7 +58,8 @@ int layernorm_var(Ctx* c, const uint64_t* x, int n_blk, int n_feat, int level, d
   const int block = t.hold.items(per, n_blk);
   if ((rc = ensure_aux(c, tw + ow + t.hold.reserve(per, n_blk))) || (rc = t.reserve(t.relin_words(n_blk, l, 2)))) return rc;
   uint64_t *to = c->aux + tw, *X = to + ow;
-  if ((rc = launch_consts(c, s, k, 3, l + 1, 0, c->aux)) || (rc = launch_consts(c, s, &kOne, 1, l + 1, 2, to))) return rc;
+  const ConstTable tables[] = {{k, 3, l + 1, 0, c->aux}, {&kOne, 1, l + 1, 2, to}};
+  if ((rc = launch_consts(c, s, tables, 2))) return rc;
   for (int b0 = 0; b0 < n_blk; b0 += block) {
     const int n = std::min(block, n_blk - b0);
     const MomentArgs a{x + (uint64_t)b0 * n_feat * ct, sum + b0 * ct, X, c->aux, to, c->d_prime,
@@ -99,9 +100,9 @@ int layernorm(Ctx* c, const uint64_t* x, const uint64_t* sum, int n_blk, int n_f
     return rc;
   uint64_t *tk = c->aux, *tb = tk + kw, *tf = tb + bw, *to = tf + fw, *X = to + fw;
   const Whole feat{n_feat, 0};
-  if ((rc = launch_consts(c, s, k.data(), n_k, nl, 0, tk)) || (rc = launch_consts(c, s, &feat, 1, nl, 0, tf)) ||
-      (rc = launch_consts(c, s, &kOne, 1, nl, 2, to)) || (beta && (rc = launch_consts(c, s, kb.data(), n_feat, nl, 0, tb))))
-    return rc;
+  const ConstTable tables[] = {{k.data(), n_k, nl, 0, tk}, {kb.data(), (int)kb.size(), nl, 0, tb}, {&feat, 1, nl, 0, tf},
+                               {&kOne, 1, nl, 2, to}};
+  if ((rc = launch_consts(c, s, tables, 4))) return rc;
   for (uint64_t b0 = 0; b0 < items; b0 += block) {
     const int n = (int)std::min<uint64_t>(block, items - b0);
     const NormArgs a{x, sum, rstd, X, tk, beta ? tb : nullptr, tf, to, c->d_prime, (int)c->log_n, nl,
@@ -168,10 +169,9 @@ int layernorm_grad(Ctx* c, const uint64_t* dy, int n_blk, int n_feat, int level,
              *B = te + fw;
     uint64_t *X = B, *G = X + 3 * lim * bb, *H = G + rct * bb, *R = H + hct * bb, *Y = R + rct * bb;
     const Whole feat{n_feat, 0};
-    if ((rc = launch_consts(c, s, k.data(), n_k, nl, 0, tk)) || (rc = launch_consts(c, s, &feat, 1, nl, 0, tf)) ||
-        (rc = launch_consts(c, s, &cr, 1, l - 1, 0, tc)) || (rc = launch_consts(c, s, &kOne, 1, nl, 2, t2)) ||
-        (rc = launch_consts(c, s, &kOne, 1, l - 1, 1, t1)) || (rc = launch_consts(c, s, &kOne, 1, low, 2, te)))
-      return rc;
+    const ConstTable tables[] = {{k.data(), n_k, nl, 0, tk}, {&feat, 1, nl, 0, tf},  {&cr, 1, l - 1, 0, tc},
+                                 {&kOne, 1, nl, 2, t2},      {&kOne, 1, l - 1, 1, t1}, {&kOne, 1, low, 2, te}};
+    if ((rc = launch_consts(c, s, tables, 6))) return rc;
     for (int b0 = 0; b0 < n_blk; b0 += bb) {
       const int nb = std::min(bb, n_blk - b0);
       const uint64_t *dyb = dy + (uint64_t)b0 * n_feat * ct, *rb = rstd + (uint64_t)b0 * 2 * (rstd_level + 1) * N;
@@ -191,7 +191,8 @@ int layernorm_grad(Ctx* c, const uint64_t* dy, int n_blk, int n_feat, int level,
       }
     }
   }
-  if (dgamma && (rc = launch_consts(c, s, &kOne, 1, nl, 1, c->aux))) return rc;
+  const ConstTable kept{&kOne, 1, nl, 1, c->aux};
+  if (dgamma && (rc = launch_consts(c, s, &kept, 1))) return rc;
   for (int f0 = 0; (dgamma || dbeta) && f0 < n_feat; f0 += bf) {
     const int n = std::min(bf, n_feat - f0);
     uint64_t *X = c->aux + fw, *Z = X + 3 * lim * bf;

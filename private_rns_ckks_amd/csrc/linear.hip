@@ -63,9 +63,9 @@ int matmul_i8(Ctx* c, const uint64_t* x, int n_blk, int n_in, const int8_t* w, i
   auto even = [](uint64_t v) { return (v + 1) & ~1ull; };  // 16-byte parts
   if ((rc = ensure_aux(c, tops + even(pack_words) + kw + iw + bw)) || (drop && (rc = ensure_workspace(c, step)))) return rc;
   uint64_t *T = c->aux, *pack = T + tops, *tk = pack + even(pack_words), *ti = tk + kw, *tb = ti + iw;
-  if ((rc = launch_consts(c, s, k.data(), n_k, nl, in ? 0 : drop, tk))) return rc;
-  if (in && (rc = launch_consts(c, s, ki.data(), n_ki, nl, drop, ti))) return rc;
-  if (!kb.empty() && (rc = launch_consts(c, s, kb.data(), n_out, nl, 0, tb))) return rc;
+  const ConstTable tables[] = {{k.data(), n_k, nl, in ? 0 : drop, tk}, {ki.data(), n_ki, nl, drop, ti},
+                               {kb.data(), (int)kb.size(), nl, 0, tb}};
+  if ((rc = launch_consts(c, s, tables, 3))) return rc;
   MatArgs a;
   memset(&a, 0, sizeof(a));
   a.x = x;
