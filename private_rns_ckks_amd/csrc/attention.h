@@ -61,7 +61,7 @@ constexpr int kMaxProducts = 1024;
 // Rescales of n products by their top `drop` (1 or 2) limbs, in one transform:
 // `top` holds the dropped limbs q_(level+1-drop)..q_level ([2][drop][N] an item, used up), `out` the limbs
 // that stay times the inverses of the dropped primes ([2][level+1-drop][N] an
-// item, in place).  add (optional): a constant for component 0 of item b,
+// item, in place; below 4q for primes below 2^61, canonical for larger ones).  add (optional): a constant for component 0 of item b,
 // add[(i * n_add + (first + b) % n_add) * 2] in limb i.  ws holds 2 (level+1) N
 // words an item of a chunk, one at least.
 struct ProductRescale {

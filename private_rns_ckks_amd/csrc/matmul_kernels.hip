@@ -409,6 +409,8 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
   const int row0 = wm * MT * 32 + (lane >> 5) * 4;
   uint64_t* o = (i < low ? a.out : a.top) + at + ((uint64_t)b * a.nj + rb * ROWS + wm * MT * 32) * per;
   const uint32_t o_off = ((uint32_t)word + (lane >> 5) * 4 * (uint32_t)per) * 8;  // below 2^29
+  // words that the rescale finishes are left below 4q (primes below 2^61)
+  const bool lazy = ND < 8 && a.drop && i < low;
   // The rows of a group of four registers lie next to each other; a group's
   // chains do not wait for one another.
   auto sums = [&](int m, int r, uint64_t (&v)[4]) {
@@ -420,8 +422,11 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
 #pragma unroll
       for (int d = 4; d < ND; ++d) hi += (int64_t)acc[m][d][r + n] * place[d - 4];
       const ulonglong2 k = kc[row0 + m * 32 + r * 2 + n];
-      v[n] = below(below(mul_shoup_lazy_split(mod.rem(lo, hi), k.x, k.y, pc.q), 2 * pc.q), pc.q);
+      v[n] = mul_shoup_lazy_split(mod.rem(lo, hi), k.x, k.y, pc.q);  // below 4q
     }
+    if (lazy) return;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) v[n] = below(below(v[n], 2 * pc.q), pc.q);
   };
   auto store = [&](int up, uint64_t (&v)[4]) {
     const int j = rb * ROWS + row0 + up;

@@ -272,7 +272,8 @@ __global__ __launch_bounds__(kThreads) void drop_col_kernel(DropArgs a) {
 }
 
 // The row pass of products' rescale: what the limbs that stay keep is in `out`
-// already, times the inverses of the dropped primes.
+// already, times the inverses of the dropped primes, below 4q for primes below
+// 2^61 (the products leave it so), canonical above.
 struct ProductCombineIO {
   struct Ops {
     uint64_t c;
@@ -284,7 +285,8 @@ struct ProductCombineIO {
   __device__ __forceinline__ void after_load(uint32_t, uint64_t) const {}
   __device__ __forceinline__ Ops fetch(uint32_t j) const { return Ops{out[j]}; }
   __device__ __forceinline__ void store(uint32_t j, uint64_t x, const Ops& o) const {
-    out[j] = add_mod(sub_mod(o.c, x, q), add, q);
+    const uint64_t t = o.c + (q - x) + add;  // below 6q, or 3q: below 2^64
+    out[j] = reduce_4q(t >= 4 * q ? t - 4 * q : t, q);
   }
 };
 
