@@ -281,22 +281,30 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
     const int g = min(t, steps - 1) * (KS / 16) + tid / 16;
     return SCALED && tid < KS ? kin_i[group_start(g, a.n_in) + tid % 16] : ulonglong2{};
   };
+  // the constants of words 4g..4g+3, read a quarter ahead
+  ulonglong2 scale[4];
+  auto scales = [&](int t, int g) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) scale[k] = kin[t & 1][grp * 16 + 4 * g + k];
+  };
   // words 4g..4g+3 into their digits; then all 16 into buffer t & 1
   uint32_t part[ND][4];
   auto quarter = [&](int t, uint64_t (&v)[16], int g) {
     if (SCALED) {
 #pragma unroll
-      for (int k = 4 * g; k < 4 * g + 4; ++k) {
-        const ulonglong2 w = kin[t & 1][grp * 16 + k];
-        v[k] = below(below(mul_shoup_lazy_split(v[k], w.x, w.y, pc.q), 2 * pc.q), pc.q);
+      for (int k = 0; k < 4; ++k) {
+        uint64_t& u = v[4 * g + k];
+        u = below(below(mul_shoup_lazy_split(u, scale[k].x, scale[k].y, pc.q), 2 * pc.q), pc.q);
       }
+      if (g < 3) scales(t, g + 1);
     }
     uint32_t o[ND];
     digits4<ND>(v + 4 * g, o);
 #pragma unroll
     for (int d = 0; d < ND; ++d) part[d][g] = o[d];
   };
-  auto quarters = [](int c) { return c == 0 ? 0 : NC < 4 ? 4 : c == 1 ? 2 : min(c + 1, 4); };  // done before chunk c
+  // quarters done before chunk c: a scaled one fills its chunk
+  auto quarters = [](int c) { return c == 0 ? 0 : NC < 4 ? 4 : SCALED ? c : c == 1 ? 2 : min(c + 1, 4); };
   auto put = [&](int t) {
 #pragma unroll
     for (int d = 0; d < ND; ++d) dig[t & 1][d][grp][col] = make_uint4(part[d][0], part[d][1], part[d][2], part[d][3]);
@@ -322,6 +330,7 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
     }
     __syncthreads();
   }
+  if (SCALED) scales(0, 0);
 #pragma unroll
   for (int g = 0; g < 4; ++g) quarter(0, raw[0], g);
   put(0);
@@ -345,6 +354,7 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
       load(w, 0, 16, next);
     }
     digits(0);
+    if (SCALED) scales(buf ^ 1, 0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -369,10 +379,10 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
 #pragma unroll
         for (int d = 0; d < ND * MT; ++d) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction,
-          if (c + 1 < NC && d < ND) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read,
+          if ((c + 1 < NC && d < ND) || (SCALED && d >= ND * MT - 5)) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read,
           if (d < MT + 16 / NC) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);      // a load,
           if (c + 1 == NC && d < ND) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // a write,
-          __builtin_amdgcn_sched_group_barrier(0x002, SCALED ? 24 : 7, 0);               // conversions
+          __builtin_amdgcn_sched_group_barrier(0x002, SCALED ? 13 : 7, 0);               // conversions
         }
       }
       __builtin_amdgcn_sched_barrier(0);
