@@ -515,7 +515,10 @@ int ckks_linattn_step(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, c
  * returns, and a captured graph replays its constants.
  *
  * Buffers, streams and captures as in the attention calls, whose limits
- * (CKKS_BLOCK_MB) hold here too; no internal stream is used. */
+ * (CKKS_BLOCK_MB) hold here too: a call holds its operands' block, one
+ * workspace and, on top, its constants (16 bytes each and limb) and for
+ * ckks_matmul_i8 the matrix laid out for its kernel (up to 255 outputs and 127
+ * inputs more).  No internal stream is used. */
 
 /* Source: AEGIS summary, "Methodology", item 2 (each device multiplies its
  * encrypted activations by its slices of the weights, locally).

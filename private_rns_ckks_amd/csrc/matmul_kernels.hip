@@ -51,7 +51,8 @@ struct Epilogue {
 
 // One word of R outputs a thread: the word's 31-bit halves times a byte, summed
 // in 64 bits (2^31 2^7 2^16 = 2^54).  For few outputs, where the words are all the
-// traffic: ROWSFIG.
+// traffic: 768 inputs of 4 limbs at N = 2^16 (3.2 GB) in 630 us, 5.1 TB/s, with 16
+// loads in flight; 650 us with eight outputs a thread and a load at a time.
 template <int R>
 __global__ __launch_bounds__(256) void matmul_rows_kernel(MatArgs a, const uint64_t* pack) {
   const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
@@ -110,13 +111,23 @@ __global__ __launch_bounds__(256) void matmul_rows_kernel(MatArgs a, const uint6
 // 128 each.  ND products of bytes with 32-bit sums (|s_d w| n_in <= 2^7 2^7 2^16)
 // then give the sum exactly, and the epilogue joins them modulo the prime.
 //
-// A workgroup of 4 waves takes 32 WM outputs x 32 WN words of one limb; a wave
-// 32 outputs x 32 words, all digits, 16 ND accumulators a lane, so that two
-// workgroups share a CU: one's epilogue and conversions run beside the other's
-// matrix instructions.  The words of a step of 128 / WN inputs (16 a thread, of
-// one column) load while the step before is multiplied, are split into digits
-// and laid in LDS in the order the instructions take them (16 inputs of a word
-// and digit together); the matrix comes from L2 in that order already.
+// A workgroup of 4 waves takes 32 MT WM outputs x 32 WN words of one limb; a wave
+// 32 MT outputs x 32 words, all digits: 16 ND MT accumulators a lane.  The words
+// of a step of 128 / WN inputs (16 a thread, of one column) are loaded ahead,
+// split into digits and laid in LDS in the order the instructions take them (16
+// inputs of a word and digit together), which every wave of the word reads; the
+// matrix comes from L2 in that order already.
+//   MT 2: one wave a SIMD, 256 outputs.  A digit read from LDS serves two
+//     instructions (with one it would take LDS's whole rate), and loads, reads,
+//     conversions and writes of the steps around stand between a step's matrix
+//     instructions: 56 of 32 cycles in 3.0 thousand cycles a step.
+//   MT 1: two workgroups a CU, whose phases overlap, for 128, 64 or 32 outputs.
+// 768 -> 768 at 3 limbs of 2^16 (300 M words in and out, 7 digits) takes 2.9-3.0
+// ms: 1.1 P byte operations/s, where a large library product of bytes reaches 2.0 on this card;
+// 3.1 ms with MT 1.  A tile's 39 thousand cycles are 20 of steps, 12 of joining
+// the sums (some 60 vector instructions an output) and 6 before the first words
+// are there; tile after tile in one workgroup, the next words loaded early, gained
+// nothing (2.9 ms).
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
@@ -482,14 +493,17 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
 
 namespace {
 
-// The matrix cores' tiles take outputs from kTileRows on and inputs from a
-// group's 16 on.
+// The matrix cores' tiles take outputs from kTileRows on (up to 8, a thread's
+// own sums read the words once as well) and inputs from a group's 16 on.
 constexpr int kTileRows = 9;
 bool tiled(int n_in, int nj) { return nj >= kTileRows && n_in >= 16; }
 
 // The tile of a launch: 32, 64, 128 or 256 outputs.  A word costs its conversion
 // for every tile of outputs (some 16 instructions an input) and its sums'
-// joining for every output, those past the last included (some 74).
+// joining for every output, those past the last included (some 74): 131 outputs
+// of 77 inputs (two blocks of 6 limbs at 2^14) take 0.92 ms a call in tiles of 64,
+// 1.31 in one of 256; the product of 768 by 768 takes 2.9 ms in tiles of 256, 3.1
+// of 128.
 struct Tiles {
   int wm = 1, wn, mt = 1, row_blocks, chunks;
   Tiles(int n_in, int nj) {

@@ -26,6 +26,7 @@ SETS = {
     "wide": (10, 7, 62, 3, 61, 3),
     "wide61": (11, 8, 61, 4, 62, 2),
     "one": (10, 1, 50, 0, 60, 1),
+    "nokey": (11, 4, 50, 0, 60, 4),
     "deep": (10, 24, 54, 8, 60, 3),
     "full": (16, 8, 54, 3, 60, 3),
 }
@@ -136,6 +137,7 @@ MATMULS = [
     ("q54", 1, 1, 128, 129, "out", 0, True, False), ("q54", 1, 2, 129, 256, "in", 0, False, True),
     ("tiny", 1, 1, 300, 257, "in", 0, True, False), ("small", 1, 1, 256, 300, "out", 0, True, False),
     ("q48", 0, 1, 385, 140, "none", 0, True, False), ("wide", 1, 1, 33, 200, "in", 0, True, False),
+    ("nokey", 3, 1, 19, 12, "out", 1, True, False), ("nokey", 1, 2, 4, 3, "in", 0, True, True),
     ("q56", 1, 1, 31, 150, "out", 0, False, False), ("q47", 2, 1, 20, 190, "out", 1, True, True),
 ]
 
