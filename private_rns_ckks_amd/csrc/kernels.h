@@ -117,6 +117,9 @@ int small_decompose(Ctx* c, hipStream_t s, int level, int n, const uint64_t* src
                     uint64_t* E, uint64_t per);
 int small_back(Ctx* c, hipStream_t s, int level, int drop, int n, const KSItem* it, uint64_t* A, uint64_t per,
                uint64_t add_stride, uint64_t accum_stride, uint64_t out_stride, int out_comp_limbs);
+// Inverse transforms with the 1/N factor, in place, one workgroup a limb (N <=
+// 2^12): item b of n at A + b*per.
+int small_inverse(Ctx* c, hipStream_t s, uint64_t* A, uint64_t per, int n, const NttJobs& jobs);
 int small_rescale(Ctx* c, hipStream_t s, int level, int drop, int n, const uint64_t* X, uint64_t x_stride,
                   const uint64_t* rlk, uint64_t* out, uint64_t out_stride, uint64_t* ws, uint64_t per);
 

@@ -14,6 +14,7 @@
 // results are the same words.  At N = 2^12 and 4 limbs the kernels take 8.7,
 // 11.5, 5 to 7, 8.7 and 12.2 us (17 with a rescale): the latency of the
 // transform's six rounds and of the loads before them, with most CUs empty.
+#include <stddef.h>
 #include <string.h>
 
 #include "arith.h"
@@ -573,6 +574,24 @@ int small_back(Ctx* c, hipStream_t s, int level, int drop, int n, const KSItem* 
   hipLaunchKernelGGL(fn, dim3(2 * low, n), dim3(c->N / 4), 0, s, m);
   CKKS_HIP_CHECK(hipGetLastError());
   return CKKS_OK;
+}
+
+int small_inverse(Ctx* c, hipStream_t s, uint64_t* A, uint64_t per, int n, const NttJobs& jobs) {
+  InverseArgs a;
+  memset(&a, 0, sizeof(a));
+  a.src = a.dst = A;
+  a.src_bstride = a.dst_bstride = per;
+  a.tw = c->d_tw_inv;
+  a.tab = (const uint64_t*)c->d_prime;
+  a.prime = c->d_prime;
+  for (int j = 0; j < jobs.n; ++j) {
+    a.src_limb[j] = jobs.src_limb[j];
+    a.dst_limb[j] = jobs.dst_limb[j];
+    a.prime_idx[j] = jobs.prime[j];
+    a.add_limb[j] = -1;
+    a.scale_off[j] = (uint32_t)((jobs.prime[j] * sizeof(PrimeConst) + offsetof(PrimeConst, ninv)) / 8);  // {N^-1, Shoup}
+  }
+  return launch_inverse(c, s, a, jobs.n, n);
 }
 
 // ks_rescale on a small ring.
