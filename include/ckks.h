@@ -529,7 +529,8 @@ int ckks_linattn_step(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, c
  * d = (scales != NULL) + (d_tok != NULL) rescales, none without either.
  *   d_x     [n_blk][n_in][2][level+1][N]
  *   d_w     [n_out][n_in] bytes, with CKKS_W_TRANSPOSED [n_in][n_out]
- *   scales  [n_out], with CKKS_SCALE_IN [n_in], or NULL: none
+ *   scales  [n_out], with CKKS_SCALE_IN [n_in], or NULL: none.  Each is rounded
+ *           by up to 1 / (2 q_level), as k says; one that rounds to 0 is 0
  *   d_tok   [n_tok][level+1][N] plaintexts (a scale for each token), 1 <= n_tok
  *           <= n_blk, or NULL with n_tok 0.  A zero removes a token.
  *   bias    [n_out] or NULL; added to every slot, also to removed tokens'
@@ -560,9 +561,11 @@ int ckks_matmul_i8(ckks_ctx* ctx, const uint64_t* d_x, int n_blk, int n_in, cons
  *   d_sum  [n_blk][2][level+1][N], for ckks_layernorm
  *   d_var  [n_blk][2][level-1][N]
  * The sums need log2(F F) bits above a feature's square: F^2 times the largest
- * variance times scale^2 k stays below q_0 .. q_l / 2.  1 <= n_feat <= 65536;
- * CKKS_ERANGE below level 2; CKKS_EINVAL when k rounds to 0 or a constant
- * reaches 2^126. */
+ * variance times scale^2 k stays below q_0 .. q_l / 2.  Rounding k moves var's
+ * scale by up to 1 / (2 k) of itself, so k has to be 2^19 or more (2^-20): with
+ * primes and a scale of b bits there is room for F^2 <= 2^(b-19), 45 features at
+ * 30 bits, 1448 at 40.  1 <= n_feat <= 65536; CKKS_ERANGE below level 2;
+ * CKKS_EINVAL when k is below 2^19 or a constant reaches 2^126. */
 int ckks_layernorm_var(ckks_ctx* ctx, const uint64_t* d_x, int n_blk, int n_feat, int level, double scale, double eps,
                        const uint64_t* d_rlk, uint64_t* d_sum, uint64_t* d_var, ckks_stream_t stream);
 
@@ -576,7 +579,9 @@ int ckks_layernorm_var(ckks_ctx* ctx, const uint64_t* d_x, int n_blk, int n_feat
  *                 input that ckks_layernorm_grad takes; gamma and beta may then
  *                 enter the next ckks_matmul_i8 as its inputs' scales and bias.
  *   d_y           [n_blk][n_feat][2][rstd_level-1][N]
- * One relinearisation a feature.  Errors as above. */
+ * A weight gamma_i is rounded by up to F rstd_scale / (2 q_t q_(t-1)): that is
+ * 2^-20 at most, CKKS_EINVAL otherwise.  One relinearisation a feature.  Errors as
+ * above. */
 int ckks_layernorm(ckks_ctx* ctx, const uint64_t* d_x, const uint64_t* d_sum, int n_blk, int n_feat, int level,
                    double scale, const uint64_t* d_rstd, int rstd_level, double rstd_scale, const double* gamma,
                    const double* beta, const uint64_t* d_rlk, uint64_t* d_y, ckks_stream_t stream);
@@ -605,7 +610,8 @@ int ckks_layernorm(ckks_ctx* ctx, const uint64_t* d_x, const uint64_t* d_sum, in
  *   d_dbeta   [n_feat][2][level+1][N]
  * xhat and rstd are read at limbs 0..level.  With n_blk 0, dgamma and dbeta are
  * zero.  CKKS_ERANGE below level 5 with d_dx, 1 with d_dgamma; CKKS_EINVAL when c
- * or k (before gamma) rounds to 0 or a constant reaches 2^126. */
+ * or k (before gamma) is below 2^19, whose rounding would move dx by more than
+ * 2^-20 of itself, or a constant reaches 2^126. */
 int ckks_layernorm_grad(ckks_ctx* ctx, const uint64_t* d_dy, int n_blk, int n_feat, int level, const uint64_t* d_xhat,
                         int xhat_level, double xhat_scale, const uint64_t* d_rstd, int rstd_level, double rstd_scale,
                         const double* gamma, const uint64_t* d_rlk, const ckks_sum_steps* steps, uint64_t* d_dx,

@@ -27,6 +27,11 @@ inline bool whole(double x, Whole* out) {
   return true;
 }
 
+// The least integer for a constant that sets a result's scale: rounding moves it
+// by 2^-20 of itself at most, what decrypted results are held to.
+constexpr int64_t kLeastFactor = 1 << 19;
+inline bool whole_factor(double x, Whole* out) { return whole(x, out) && out->m >= kLeastFactor; }
+
 // A table of n constants for the limbs i < nl, limb by limb:
 // table[(i * n + j) * 2] = {k_j mod q_i, Shoup quotient}.  With drop > 0, limbs
 // i <= nl - 1 - drop hold k_j (q_(nl-1) .. q_(nl-drop))^-1 instead, which turns

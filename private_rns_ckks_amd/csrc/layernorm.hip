@@ -27,7 +27,7 @@ bool positive(double v) { return v > 0 && v < INFINITY; }
 // Gains gamma_i kappa (kappa alone without gamma); *n receives their number.
 int gains(const double* gamma, double kappa, int n_feat, std::vector<Whole>* k) {
   Whole one;
-  if (!whole(kappa, &one) || one.m < 1) return set_error(CKKS_EINVAL, "the scales leave no room for the weights");
+  if (!whole_factor(kappa, &one)) return set_error(CKKS_EINVAL, "the scales leave no room for the weights");
   k->assign(gamma ? n_feat : 1, one);
   for (int i = 0; gamma && i < n_feat; ++i)
     if (!whole(gamma[i] * kappa, &(*k)[i])) return set_error(CKKS_EINVAL, "a rounded weight reaches 2^126");
@@ -45,7 +45,7 @@ int layernorm_var(Ctx* c, const uint64_t* x, int n_blk, int n_feat, int level, d
   if (!positive(scale)) return set_error(CKKS_EINVAL, "the scale must be positive");
   Whole k[3] = {{n_feat, 0}, {}, {}};
   const double f = n_feat;
-  if (!whole((double)c->mod[l] * (double)c->mod[l - 1] / (f * f) / scale, &k[1]) || k[1].m < 1)
+  if (!whole_factor((double)c->mod[l] * (double)c->mod[l - 1] / (f * f) / scale, &k[1]))
     return set_error(CKKS_EINVAL, "the scale leaves no room for the variance");
   if (!whole(eps * scale, &k[2])) return set_error(CKKS_EINVAL, "the rounded eps reaches 2^126");
   const uint64_t N = c->N, lim = (uint64_t)(l + 1) * N, ct = 2 * lim, vct = 2ull * (l - 1) * N;
@@ -132,7 +132,7 @@ int layernorm_grad(Ctx* c, const uint64_t* dy, int n_blk, int n_feat, int level,
   if (dx) {
     auto q = [&](int i) { return (double)c->mod[i]; };
     if ((rc = gains(gamma, q(l - 3) * q(l - 4) / ((double)n_feat * rstd_scale), n_feat, &k))) return rc;
-    if (!whole(q(l) / xhat_scale * q(l - 1) / xhat_scale * q(l - 2), &cr) || cr.m < 1)
+    if (!whole_factor(q(l) / xhat_scale * q(l - 1) / xhat_scale * q(l - 2), &cr))
       return set_error(CKKS_EINVAL, "the scales leave no room for the gradient");
   }
   const uint64_t N = c->N, lim = (uint64_t)(l + 1) * N, ct = 2 * lim, items = (uint64_t)n_blk * n_feat;
