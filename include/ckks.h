@@ -541,7 +541,8 @@ int ckks_linattn_step(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, c
  * outputs' gradients with CKKS_W_TRANSPOSED | CKKS_SCALE_IN, and n_in, n_out
  * exchanged.  The noise of y is that of x, up to 128 n_in times as large.
  * 1 <= n_in <= 65536; CKKS_ERANGE below level d; CKKS_EINVAL for a constant of
- * 2^62 or more.  Needs no key and works with K = 0. */
+ * 2^62 or more and for a scale (or a tok_scale of d_tok, or an s_y) that is not
+ * positive and finite.  Needs no key and works with K = 0. */
 int ckks_matmul_i8(ckks_ctx* ctx, const uint64_t* d_x, int n_blk, int n_in, const int8_t* d_w, int n_out, int level,
                    double scale, const double* scales, const uint64_t* d_tok, int n_tok, double tok_scale,
                    const double* bias, unsigned flags, uint64_t* d_y, double* out_scale, ckks_stream_t stream);

@@ -27,6 +27,9 @@ inline bool whole(double x, Whole* out) {
   return true;
 }
 
+// What a scale has to be.
+inline bool positive(double v) { return v > 0 && v < INFINITY; }
+
 // The least integer for a constant that sets a result's scale: rounding moves it
 // by 2^-20 of itself at most, what decrypted results are held to.
 constexpr int64_t kLeastFactor = 1 << 19;

@@ -22,8 +22,6 @@ int check_norm(const Ctx* c, int n_blk, int n_feat, int level) {
   return check_count((uint64_t)n_blk * n_feat);
 }
 
-bool positive(double v) { return v > 0 && v < INFINITY; }
-
 // Gains gamma_i kappa (kappa alone without gamma); *n receives their number.
 int gains(const double* gamma, double kappa, int n_feat, std::vector<Whole>* k) {
   Whole one;

@@ -32,6 +32,8 @@ int matmul_i8(Ctx* c, const uint64_t* x, int n_blk, int n_in, const int8_t* w, i
     s_out = s_out * tok_scale / (double)c->mod[l - 1];
   else if (tok)
     s_out = s_out * tok_scale / (double)c->mod[l];
+  if (!positive(scale) || (tok && !positive(tok_scale)) || !positive(s_out))
+    return set_error(CKKS_EINVAL, "the scales must be positive");
   const bool in = flags & CKKS_SCALE_IN;
   // Constants of the outputs and, with CKKS_SCALE_IN, the inputs; the dropped
   // primes' inverses go with either.

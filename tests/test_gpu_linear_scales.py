@@ -5,7 +5,7 @@ import pytest
 
 import ckks_synth as S
 from gpu_util import announce, empty_dev, make_pair, to_dev, torch_cuda
-from test_gpu_linear import key, same, words
+from test_gpu_linear import int8_dev, key, same, words
 
 pytestmark = pytest.mark.gpu
 
@@ -101,6 +101,38 @@ def test_gradient_constants(lib, orc, pair):
     same(dx, ref["dx"])
     call(grad, 1, 1, d_dgamma=dg)  # the weights' gradients have no such constant
     same(dg, ref["dgamma"])
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_product_scales(lib, orc, pair, bias):
+    """A scale that is not positive and finite is refused with or without a bias that it would multiply; a token
+    scale only counts with token rows."""
+    ctx, P = pair
+    announce("scales of a product, bias=%s" % bias)
+    n_in, n_out, lv = 3, 2, 2
+    x, tok = words(P, 6, "x", lv + 1, (1, n_in, 2)), words(P, 6, "tok", lv + 1, (1,))
+    w = np.array([[3, -1, 2], [0, 5, -128]], np.int8)
+    d_x, d_t, d_w, y = to_dev(x), to_dev(tok), int8_dev(w), empty_dev((1, n_out, 2, lv + 1, P.N))
+    b = np.array([0.5, -2.0]) if bias else None
+    y.fill_(-7)
+
+    def call(scale, tok_scale=1.0, d_tok=None, out=y):
+        return lib.ckks_matmul_i8(ctx, d_x, 1, n_in, d_w, n_out, lv, scale, out, d_tok=d_tok, n_tok=int(d_tok is not None),
+                                  tok_scale=tok_scale, bias=b)
+
+    for bad in (0.0, -1.0, float("nan"), float("inf"), -float("inf")):
+        refused(lib, call, bad)
+        refused(lib, call, 2.0 ** 30, bad, d_t)
+    refused(lib, call, 2.0 ** 600, 2.0 ** 600, d_t)    # an output scale above the largest double
+    refused(lib, call, 2.0 ** -600, 2.0 ** -600, d_t)  # and below the smallest
+    assert bool((y == -7).all())
+    assert call(2.0 ** 30, float("nan")) == 2.0 ** 30
+    same(y, orc.matmul_i8(P, lv, x, w, 2.0 ** 30, bias=b)[0])
+    low = empty_dev((1, n_out, 2, lv, P.N))
+    got = call(2.0 ** 30, 2.0 ** 25, d_t, low)
+    ref, s = orc.matmul_i8(P, lv, x, w, 2.0 ** 30, None, False, tok, 2.0 ** 25, b)
+    assert got == s
+    same(low, ref)
 
 
 def test_many_features_decrypt_to_the_norm(lib, orc):
