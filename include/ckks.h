@@ -36,7 +36,8 @@
  *              usual encoding is g = 5^k mod 2N.
  *   Memory     d_* arguments are device pointers (HIP), owned by the caller,
  *              not retained after the call's stream work completes, each
- *              16-byte aligned (CKKS_EINVAL otherwise; hipMalloc gives 256).
+ *              16-byte aligned (CKKS_EINVAL otherwise; hipMalloc gives 256)
+ *              unless it holds bytes.
  *              Host arrays (galois element lists, key pointer lists) are
  *              read before the call returns.
  *   Streams    every compute call enqueues on `stream` and returns; outputs
@@ -528,7 +529,8 @@ int ckks_linattn_step(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, c
  *   k         = round(scales[.] q_level)
  * d = (scales != NULL) + (d_tok != NULL) rescales, none without either.
  *   d_x     [n_blk][n_in][2][level+1][N]
- *   d_w     [n_out][n_in] bytes, with CKKS_W_TRANSPOSED [n_in][n_out]
+ *   d_w     [n_out][n_in] bytes, with CKKS_W_TRANSPOSED [n_in][n_out], at any
+ *           address (rows of a larger matrix, say)
  *   scales  [n_out], with CKKS_SCALE_IN [n_in], or NULL: none.  Each is rounded
  *           by up to 1 / (2 q_level), as k says; one that rounds to 0 is 0
  *   d_tok   [n_tok][level+1][N] plaintexts (a scale for each token), 1 <= n_tok

@@ -45,9 +45,12 @@ int matmul_i8(Ctx* c, const uint64_t* x, int n_blk, int n_in, const int8_t* w, i
   for (size_t j = 0; j < kb.size(); ++j)
     if (!whole(bias[j] * s_out, &kb[j]) || kb[j].e) return set_error(CKKS_EINVAL, "a rounded bias reaches 2^62");
   const uint64_t N = c->N, ct = 2ull * nl * N, oct = 2ull * low * N;
-  std::vector<Range> ins = {{x, ct * n_blk * n_in}, {w, ((uint64_t)n_in * n_out + 7) / 8}};
+  std::vector<Range> ins = {{x, ct * n_blk * n_in}};
   if (tok) ins.push_back({tok, ct / 2 * n_tok});
   if ((rc = check_ranges({{y, oct * n_blk * n_out}}, ins))) return rc;
+  // The matrix is read byte by byte and may lie anywhere: the words it touches.
+  const uintptr_t w0 = (uintptr_t)w & ~(uintptr_t)7, w1 = ((uintptr_t)w + (uint64_t)n_in * n_out + 7) & ~(uintptr_t)7;
+  REJECT_OVERLAP(y, oct * n_blk * n_out, (const void*)w0, (w1 - w0) / 8, "an input");
   *out_scale = s_out;
   if (n_blk == 0 || n_out == 0) return CKKS_OK;
   CaptureScope cap(c, s);
