@@ -5,6 +5,7 @@
 
 #include "arith.h"
 #include "convert.h"
+#include "matmul_tiles.h"
 
 namespace ckks {
 
@@ -493,37 +494,6 @@ __global__ __launch_bounds__(256, MT == 2 ? 1 : 2) void matmul_tiles_kernel(MatA
 
 namespace {
 
-// The matrix cores' tiles take outputs from kTileRows on (up to 8, a thread's
-// own sums read the words once as well) and inputs from a group's 16 on.
-constexpr int kTileRows = 9;
-bool tiled(int n_in, int nj) { return nj >= kTileRows && n_in >= 16; }
-
-// The tile of a launch: 32, 64, 128 or 256 outputs.  A word costs its conversion
-// for every tile of outputs (some 16 instructions an input) and its sums'
-// joining for every output, those past the last included (some 74): 131 outputs
-// of 77 inputs (two blocks of 6 limbs at 2^14) take 0.92 ms a call in tiles of 64,
-// 1.31 in one of 256; the product of 768 by 768 takes 2.9 ms in tiles of 256, 3.1
-// of 128.
-struct Tiles {
-  int wm = 1, wn, mt = 1, row_blocks, chunks;
-  Tiles(int n_in, int nj) {
-    uint64_t least = ~0ull;
-    for (int r = 32; r <= 256; r *= 2) {
-      const uint64_t blocks = (nj + r - 1) / r, cost = blocks * r * 74 + blocks * n_in * 16;
-      if (cost >= least) continue;
-      least = cost;
-      wm = std::min(r / 32, 4);
-      mt = r == 256 ? 2 : 1;
-    }
-    wn = 4 / wm;
-    row_blocks = (nj + rows() - 1) / rows();
-    const int nc = 4 / wn;
-    chunks = ((n_in + 31) / 32 + nc - 1) / nc * nc;
-  }
-  int rows() const { return 32 * wm * mt; }
-  uint64_t lanes() const { return (uint64_t)row_blocks * wm * mt * chunks * 64; }
-};
-
 template <int ND, bool SCALED>
 auto pick_rows(const Tiles& t) {
   return t.mt == 2   ? matmul_tiles_kernel<ND, 4, 1, 2, SCALED>
@@ -556,12 +526,11 @@ int launch_matmul(Ctx* c, hipStream_t s, const MatArgs& a, uint64_t* pack) {
     hipLaunchKernelGGL(pack_tiles_kernel, dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, s, a, t.chunks,
                        t.row_blocks * t.wm * t.mt, (uint4*)pack);
     CKKS_HIP_CHECK(hipGetLastError());
-    // nd signed bytes hold words up to 127 sum_d 2^(8d)
-    auto fits = [q](int nd) { return q <= 0x7f7f7f7f7f7f7f7full >> (8 * (8 - nd)); };
-    auto fn = fits(4)   ? pick_tiles<4>(t, a.kin)
-              : fits(5) ? pick_tiles<5>(t, a.kin)
-              : fits(6) ? pick_tiles<6>(t, a.kin)
-              : fits(7) ? pick_tiles<7>(t, a.kin)
+    const int nd = word_digits(q);
+    auto fn = nd == 4   ? pick_tiles<4>(t, a.kin)
+              : nd == 5 ? pick_tiles<5>(t, a.kin)
+              : nd == 6 ? pick_tiles<6>(t, a.kin)
+              : nd == 7 ? pick_tiles<7>(t, a.kin)
                         : pick_tiles<8>(t, a.kin);
     TraceScope ts(c, s, "matmul_i8", (double)a.nb * a.nj * a.n_in * 2 * a.nl * c->N);
     hipLaunchKernelGGL(fn, dim3((uint32_t)blocks), dim3(256), 0, s, a, (const uint4*)pack, t.chunks, t.row_blocks,
