@@ -12,8 +12,6 @@ namespace {
 constexpr int kMaxFeat = 1 << 16;
 constexpr Whole kOne{1, 0};
 
-uint64_t even(uint64_t v) { return (v + 1) & ~1ull; }  // 16-byte parts
-
 int check_norm(const Ctx* c, int n_blk, int n_feat, int level) {
   if (n_blk < 0) return set_error(CKKS_EINVAL, "bad count");
   if (n_feat < 1 || n_feat > kMaxFeat) return set_error(CKKS_EINVAL, "n_feat must be 1.." + std::to_string(kMaxFeat));
