@@ -507,7 +507,8 @@ int ckks_linattn_step(ckks_ctx* ctx, const uint64_t* d_q, const uint64_t* d_k, c
  * b.  Sums over features are sums of ciphertexts, so a linear layer and a layer
  * norm need no rotation; the calls of nonlinear layers (ckks_poly_eval_tree)
  * take the features as their batch.  Slots without a token hold anything; a
- * token row of zeros, or gradients of zero, keep them out of the results.
+ * token row of zeros, or gradients of zero, keep them out of the results.  The
+ * attention calls take features inside the slots; no call moves between the two.
  *
  * Real constants (scales, weights, biases) are host doubles, rounded to the
  * integer llround(v) next to them; from 2^62 on v is an integer itself.  They

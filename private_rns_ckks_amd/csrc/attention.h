@@ -54,9 +54,10 @@ int launch_plain_mul(Ctx* c, hipStream_t s, const PlainMul& m, uint64_t* out, ui
 // words between items of either.
 int rescale_mul_fused(Ctx* c, hipStream_t s, const PlainMul& m, const uint64_t* v, uint64_t* w, uint64_t per, int batch);
 
-// Items of a launch of rescale_products at most.  Each launch's tail leaves the
-// chip part empty: a product of 768 outputs at 3 limbs of 2^16 takes 5.37 ms with
-// 1024 items a launch, 5.46 with 128 and 5.94 with 32.
+// Items of a launch of rescale_products at most (fewer where the workspace holds
+// fewer).  Each launch's tail leaves the chip part empty: a product of 768 outputs
+// at 3 limbs of 2^16, 682 of which a workspace of 2 GiB holds, takes 5.37 ms in
+// launches of 682 and 86, 5.46 in launches of 128 and 5.94 of 32.
 constexpr int kMaxProducts = 1024;
 
 // Rescales of n products by their top `drop` (1 or 2) limbs, in one transform:

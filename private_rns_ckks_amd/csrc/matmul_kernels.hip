@@ -123,12 +123,15 @@ __global__ __launch_bounds__(256) void matmul_rows_kernel(MatArgs a, const uint6
 //     conversions and writes of the steps around stand between a step's matrix
 //     instructions: 56 of 32 cycles in 3.0 thousand cycles a step.
 //   MT 1: two workgroups a CU, whose phases overlap, for 128, 64 or 32 outputs.
-// 768 -> 768 at 3 limbs of 2^16 (300 M words in and out, 7 digits) takes 2.9-3.0
-// ms: 1.1 P byte operations/s, where a large library product of bytes reaches 2.0 on this card;
+// 768 -> 768 at 3 limbs of 2^16 (300 M words in and out, 7 digits) takes 2.7-3.0
+// ms: 1.1-1.2 P byte operations/s, where a large library product of bytes reaches 2.0 on this card;
 // 3.1 ms with MT 1.  A tile's 39 thousand cycles are 20 of steps, 12 of joining
 // the sums (some 60 vector instructions an output) and 6 before the first words
 // are there; tile after tile in one workgroup, the next words loaded early, gained
-// nothing (2.9 ms).
+// nothing (2.9 ms).  With 8 digits (60-bit primes) it takes 2.9 ms where 7 take 2.8;
+// with scales on the inputs the 8-digit kernels of 128 and 256 outputs spill 16
+// registers (768 -> 128: 910 us against 755; 2048 -> 512 at 4 limbs of 2^15: 3.48 ms
+// against 3.24).
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));

@@ -89,7 +89,8 @@ __device__ __forceinline__ void segment(int n_feat, int& k0, int& k1) {
 }
 
 // Reads every word of the features once: memory.  768 features of 13 limbs at N
-// = 2^16 are 10.2 GB, in 1.88 ms (5.4 TB/s; 1.95 with a feature's two loads in flight).
+// = 2^16 are 10.5 GB, in 1.82-1.88 ms (5.6-5.7 TB/s; 1.95 with a feature's two loads in
+// flight).
 template <bool WIDE, int SEG>
 __global__ __launch_bounds__(SEG == 1 ? 256 : 64 * SEG) void moments_kernel(MomentArgs a) {
   const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
